@@ -119,7 +119,8 @@ int convrot_last_hip_error(void);
 cr_status convrot_device_check(void);
 
 /* Dispatch counters: kernel launches per entry point (index = order of the
- * entry points below: 0 rotate_quantize, 1 pack, 2 w4a4, 3 w4a8, 4 int8)
+ * entry points below: 0 rotate_quantize, 1 pack, 2 w4a4, 3 w4a8, 4 int8,
+ * 5 lora_forward / lora_backward, 6 act_checkpoint / act_backward)
  * and the count of non-native fallbacks, which is always 0 because no
  * fallback exists. Process-wide, thread-safe. */
 typedef struct cr_counters {
@@ -519,6 +520,116 @@ cr_status int8_tensorwise_gemm(const void* a_codes, const float* a_scale,
                                const void* bias, void* out, cr_out out_type, int64_t ldc,
                                int64_t M, int64_t N, int64_t K,
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * convrot_lora_forward / convrot_lora_backward - low-rank adapters of many
+ * requests at once beside one shared (quantized) projection, and their
+ * gradients. Where lora_down / lora_up of the entry points above apply one
+ * adapter to every row, here each segment of rows names its own.
+ *
+ * Cites: "Qwen-Image-Edit-2511-W4A8-ConvRot" card, passage on LoRA merge
+ * versus bypass (the delta kept as a separate bf16 branch beside the
+ * quantized weight).
+ *
+ *   rows m of segment s are [seg_offsets[s], seg_offsets[s+1]); its adapter is
+ *   a = seg_adapter[s]:
+ *     lora_act[m, :] = x[m, :] . down[a]^T                            float32
+ *     out[m, :]      = base[m, :] + scale[a] lora_act[m, :] . up[a]^T
+ *   backward, for the gradient dy of out:
+ *     dla[m, :]      = scale[a] dy[m, :] . up[a]                       float32
+ *     dx[m, :]       = dx_base[m, :] + dla[m, :] . down[a]
+ *     d_up[a]        = scale[a] sum_m dy[m, :]^T lora_act[m, :]        float32
+ *     d_down[a]      = sum_m dla[m, :]^T x[m, :]                       float32
+ *   Products are exact in float32 and summed in float32 (float32 factors are
+ *   carried as three bf16 terms); out and dx are rounded once. Results do not
+ *   depend on timing (no atomics), and a row's result does not depend on the
+ *   values of other rows (infinities and NaN stay in their row; in the weight
+ *   gradients they stay in their adapter).
+ *
+ *   x            bf16 [M, K], leading dimension ldx; backward: the same, or the
+ *                INT8 codes that convrot_rotate_quantize made of it (SYM_INT8,
+ *                natural layout, int8 [M, K]) as an 8-bit checkpoint, with
+ *   x_scales     their float32 scales, x_gran CR_GRAN_ROW [M] or CR_GRAN_TENSOR
+ *                [1], and rot_group the rotation they were made with (16, 64,
+ *                256 or 1024; K % 256 == 0, K % rot_group == 0, ldx % 16 == 0).
+ *                x_scales NULL: x is bf16 and x_gran, rot_group are ignored.
+ *                The gradient is summed in the rotated basis and rotated back.
+ *   down, up     bf16 [A, R, K] and [A, N, R] of A = n_adapters; R a multiple of
+ *                8 from 8 to 128 (pad smaller ranks with zeros)
+ *   seg_offsets  int32 [S + 1], not descending; seg_adapter int32 [S]. Empty
+ *                segments are fine. Segments may share an adapter. Rows before
+ *                the first offset or behind the last, and segments whose
+ *                adapter lies outside 0 .. A-1, have no adapter: their lora_act
+ *                is 0, their out is base (their dx dx_base) and they add nothing
+ *                to the gradients. Offsets are read on the device and clamped to
+ *                the batch, so no row outside it is touched whatever they hold;
+ *                descending offsets leave the results of the rows concerned
+ *                unspecified.
+ *   scale        optional float32 [A] (NULL: 1)
+ *   base         optional, of out's type, leading dimension ldb (NULL: 0). It may
+ *                be out itself (ldb == ldo): then rows without adapter are left
+ *                as they are. Any other overlap is not allowed. dx_base likewise.
+ *   out, dx      CR_OUT_BF16 or CR_OUT_F32
+ *   lora_act     float32 [M, R] (written by the forward, read by the backward)
+ *   dx, d_down, d_up   each may be NULL if not wanted, not all of them; x may be
+ *                NULL without d_down, lora_act without d_up. d_down [A, R, K] and
+ *                d_up [A, N, R] are written whole (zeros for adapters without
+ *                rows); with accumulate != 0 they are added to instead.
+ *   workspace    convrot_lora_backward_workspace_size(...) bytes (0 when the
+ *                call refuses the sizes); any contents. Calls that share one
+ *                must be ordered on one stream.
+ * Shape: 1 <= M < 2^26, N and K multiples of 8 from 8 to 32768, 1 <= S <= 65536,
+ * 1 <= A <= 4096, leading dimensions multiples of 8, not below the row length and
+ * below 2^31; backward: A R max(N, K) < 2^31.
+ */
+cr_status convrot_lora_forward(const void* x, int64_t ldx, const void* down, const void* up, int R, int n_adapters,
+                               const int32_t* seg_offsets, const int32_t* seg_adapter, int S, const float* scale,
+                               const void* base, int64_t ldb, void* out, cr_out out_type, int64_t ldo,
+                               float* lora_act, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+size_t convrot_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int R, int n_adapters);
+
+cr_status convrot_lora_backward(const void* dy, int64_t lddy, const float* lora_act,
+                                const void* x, int64_t ldx, const float* x_scales, cr_gran x_gran, int rot_group,
+                                const void* down, const void* up, int R, int n_adapters,
+                                const int32_t* seg_offsets, const int32_t* seg_adapter, int S, const float* scale,
+                                const void* dx_base, int64_t ldb, void* dx, cr_out dx_type, int64_t lddx,
+                                float* d_down, float* d_up, int accumulate,
+                                int64_t M, int64_t N, int64_t K,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * convrot_act_checkpoint / convrot_act_backward - an MLP activation that keeps
+ * its input z as 8-bit codes, and its backward pass from those codes.
+ *
+ * Cites: "Qwen-Image-Edit-2511 INT4 (ComfyUI Optimized)", Kernel Engineering
+ * (the quantized MLP around its GELU); the symmetric quantizer above.
+ *
+ *   act       CR_ACT_GELU       y = z Phi(z)                       z [rows, C]
+ *             CR_ACT_GELU_TANH  y = z (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))) / 2
+ *             CR_ACT_SWIGLU     y = g sigma(g) u,  z = [g | u]     z [rows, 2 C]
+ *   z, y, dy, dz   bf16, leading dimensions ldz, ldy, lddy, lddz
+ *   codes     int8 [rows, W], scales float32 [rows, W / 64], W = C or 2 C: the
+ *             symmetric quantizer (above, qmax 127, ROW_GROUP 64, no rotation) of
+ *             z. Groups of 64 whose largest magnitude is below 3.8e-37 (127 / A
+ *             has no float32 value) are kept as zeros with scale 0; groups that
+ *             hold an infinity or NaN get scale NaN and zero codes, so that the
+ *             gradient of the group is NaN.
+ *   forward   y = act(z) of z itself, rounded once
+ *   backward  dz = dy act'(scale * code), rounded once
+ * Shape: rows >= 1, C % 64 == 0, C <= 32768, rows C < 2^35, leading dimensions
+ * multiples of 8, not below the row length and below 2^31. One launch each.
+ */
+typedef enum cr_act {
+  CR_ACT_GELU = 0,
+  CR_ACT_GELU_TANH = 1,
+  CR_ACT_SWIGLU = 2
+} cr_act;
+
+cr_status convrot_act_checkpoint(const void* z, int64_t ldz, int64_t rows, int64_t C, cr_act act,
+                                 void* y, int64_t ldy, void* codes, float* scales, hipStream_t stream);
+cr_status convrot_act_backward(const void* dy, int64_t lddy, const void* codes, const float* scales,
+                               int64_t rows, int64_t C, cr_act act, void* dz, int64_t lddz, hipStream_t stream);
 
 #ifdef __cplusplus
 }

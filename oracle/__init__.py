@@ -20,10 +20,11 @@ Modules, in the order the path runs:
   pack      - int4 packing (natural and tile-packed layouts)
   gemm      - exact integer GEMM and per-group partial sums
   linear    - epilogues and the composed reference linears
+  adapters  - batched low-rank adapters with gradients, 8-bit activation checkpoints
 
 Every function states the passage it follows, or, where the pages are silent,
 the reading taken and why. The pins that tie this oracle to the mathematics
 and to the pages (closed forms, invariants, brute force on tiny inputs,
 constructed rounding ties) live in tests/test_oracle_*.py.
 """
-from . import hadamard, quant, pack, gemm, linear  # noqa: F401
+from . import hadamard, quant, pack, gemm, linear, adapters  # noqa: F401

@@ -8,6 +8,7 @@ ConvRotError with the library's status text.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -19,6 +20,8 @@ __all__ = [
     "w4_pack_weights_f6", "w4_packed_f6_bytes", "w4_expand_weights_f6", "w4_pack_lora_up",
     "w4a4_gemm", "w4a4_gemm_workspace_size", "w4a8_gemm",
     "int8_tensorwise_gemm", "convrot_rq_workspace_size", "w4_packed_bytes",
+    "ACT", "convrot_lora_forward", "convrot_lora_backward", "convrot_lora_backward_workspace_size",
+    "convrot_act_checkpoint", "convrot_act_backward",
     "get_counters", "reset_counters", "device_check", "status_string",
 ]
 
@@ -60,6 +63,12 @@ class LAYOUT:
     F16 = 4
 
 
+class ACT:
+    GELU = 0
+    GELU_TANH = 1
+    SWIGLU = 2
+
+
 class _Counters(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_uint64 * 8), ("fallbacks", ctypes.c_uint64)]
 
@@ -91,6 +100,13 @@ _SIGS = {
                        _vp, _sz, _vp]),
     "int8_tensorwise_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i64, _i64, _i64, _i64,
                                   _vp, _sz, _vp]),
+    "convrot_lora_forward": (_i, [_vp, _i64, _vp, _vp, _i, _i, _vp, _vp, _i, _vp, _vp, _i64, _vp, _i, _i64, _vp,
+                                  _i64, _i64, _i64, _vp]),
+    "convrot_lora_backward_workspace_size": (_sz, [_i64, _i64, _i64, _i, _i]),
+    "convrot_lora_backward": (_i, [_vp, _i64, _vp, _vp, _i64, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _i, _vp,
+                                   _vp, _i64, _vp, _i, _i64, _vp, _vp, _i, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "convrot_act_checkpoint": (_i, [_vp, _i64, _i64, _i64, _i, _vp, _i64, _vp, _vp, _vp]),
+    "convrot_act_backward": (_i, [_vp, _i64, _vp, _vp, _i64, _i64, _i, _vp, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -134,7 +150,8 @@ def get_counters():
     c = _Counters()
     lib.convrot_get_counters(ctypes.byref(c))
     return {"rotate_quantize": c.launches[0], "pack": c.launches[1], "w4a4": c.launches[2],
-            "w4a8": c.launches[3], "int8": c.launches[4], "fallbacks": c.fallbacks}
+            "w4a8": c.launches[3], "int8": c.launches[4], "lora": c.launches[5], "act": c.launches[6],
+            "fallbacks": c.fallbacks}
 
 
 def reset_counters():
@@ -375,3 +392,204 @@ def int8_tensorwise_gemm(a_codes, a_scale, w, w_scale, M, N, K, bias=None, out_t
                                   _stream(stream))
     _check(st, "int8_tensorwise_gemm")
     return out
+
+
+# ---------------------------------------------------------------------------
+# batched low-rank adapters and 8-bit activation checkpoints
+# ---------------------------------------------------------------------------
+_OUT_DTYPE = {OUT.BF16: torch.bfloat16, OUT.F32: torch.float32}
+
+
+def _tensor(t, what, dtype, device, shape):
+    """A dense tensor argument: dtype, device, shape and contiguity checked."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    return t.data_ptr()
+
+
+def _rows(t, what, dtype, device, rows, cols):
+    """A [rows, cols] argument whose rows may lie further apart: (address, leading dimension)."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a {dtype} [{rows}, {cols}] tensor with contiguous rows on {device}")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _on(device, stream):
+    """The context in which a call allocates and launches: the tensors' device,
+    and the given stream (default: that device's current one)."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return contextlib.nullcontext()
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+def _out_dtype(out_type):
+    if out_type not in _OUT_DTYPE:
+        raise ValueError("the output type is OUT.BF16 or OUT.F32")
+    return _OUT_DTYPE[out_type]
+
+
+def _adapters(x, down, up, seg_offsets, seg_adapter, scale, N, K):
+    """Checks what both adapter calls share; (R, A, S) and the addresses of
+    (down, up, seg_offsets, seg_adapter, scale)."""
+    if down.dim() != 3 or up.dim() != 3 or seg_adapter.dim() != 1:
+        raise ValueError("down is [A, R, K], up [A, N, R], seg_adapter [S]")
+    A, R = down.shape[0], down.shape[1]
+    S, dev = seg_adapter.shape[0], x.device
+    return (R, A, S), (_tensor(down, "down", torch.bfloat16, dev, (A, R, K)),
+                       _tensor(up, "up", torch.bfloat16, dev, (A, N, R)),
+                       _tensor(seg_offsets, "seg_offsets", torch.int32, dev, (S + 1,)),
+                       _tensor(seg_adapter, "seg_adapter", torch.int32, dev, (S,)),
+                       None if scale is None else _tensor(scale, "scale", torch.float32, dev, (A,)))
+
+
+def convrot_lora_forward(x, down, up, seg_offsets, seg_adapter, scale=None, base=None, out_type=OUT.BF16, out=None,
+                         lora_act=None, stream=None):
+    """Low-rank adapters of many requests beside one projection:
+    out = base + scale[a] (x . down[a]^T) . up[a]^T for the rows
+    seg_offsets[s] .. seg_offsets[s+1] of each segment s with adapter
+    a = seg_adapter[s] (outside 0..A-1: none, out = base).
+
+    x: bf16 [M, K]; down: bf16 [A, R, K]; up: bf16 [A, N, R]; seg_offsets:
+    int32 [S+1]; seg_adapter: int32 [S]; scale: float32 [A]; base: [M, N] of
+    the output's type (None: zero), which may be `out` itself. Rows of x, base
+    and out may lie further apart than their length. Returns (out, lora_act):
+    lora_act float32 [M, R] is what convrot_lora_backward reads. Outputs are
+    allocated when not given."""
+    if x.dim() != 2 or up.dim() != 3:
+        raise ValueError("x is [M, K], up [A, N, R]")
+    (M, K), N, dev = x.shape, up.shape[1], x.device
+    dt = _out_dtype(out_type)
+    (R, A, S), (pd, pu, po, pa, ps) = _adapters(x, down, up, seg_offsets, seg_adapter, scale, N, K)
+    px, ldx = _rows(x, "x", torch.bfloat16, dev, M, K)
+    pb, ldb = (None, N) if base is None else _rows(base, "base", dt, dev, M, N)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=dt, device=dev)
+        if lora_act is None:
+            lora_act = torch.empty((M, R), dtype=torch.float32, device=dev)
+        py, ldo = _rows(out, "out", dt, dev, M, N)
+        pl = _tensor(lora_act, "lora_act", torch.float32, dev, (M, R))
+        st = lib.convrot_lora_forward(px, ldx, pd, pu, R, A, po, pa, S, ps, pb, ldb, py, out_type, ldo, pl, M, N, K,
+                                      torch.cuda.current_stream().cuda_stream)
+    _check(st, "convrot_lora_forward")
+    return out, lora_act
+
+
+def convrot_lora_backward_workspace_size(M, N, K, R, n_adapters) -> int:
+    return lib.convrot_lora_backward_workspace_size(M, N, K, R, n_adapters)
+
+
+def convrot_lora_backward(dy, lora_act, x, down, up, seg_offsets, seg_adapter, scale=None, x_scales=None,
+                          rot_group=256, dx_base=None, dx_type=OUT.BF16, dx=None, d_down=None, d_up=None,
+                          want_dx=True, want_weights=True, accumulate=False, workspace=None, stream=None):
+    """Gradients of convrot_lora_forward for dy bf16 [M, N]. Returns
+    (dx, d_down, d_up): dx = dx_base + scale[a] (dy . up[a]) . down[a] in
+    dx_type (None with want_dx=False), d_down float32 [A, R, K] and d_up
+    float32 [A, N, R] (None with want_weights=False; accumulate=True adds to
+    the given ones).
+
+    x is the forward's input: bf16 [M, K], or as an 8-bit checkpoint the int8
+    codes [M, K] that convrot_rotate_quantize (SYM_INT8, per row or per tensor,
+    rot_group) made of it, with x_scales float32 [M] or [1]. x and lora_act are
+    not read with want_weights=False and may be None then."""
+    if dy.dim() != 2 or down.dim() != 3:
+        raise ValueError("dy is [M, N], down [A, R, K]")
+    (M, N), K, dev = dy.shape, down.shape[2], dy.device
+    dt = _out_dtype(dx_type)
+    (R, A, S), (pd, pu, po, pa, ps) = _adapters(dy, down, up, seg_offsets, seg_adapter, scale, N, K)
+    pdy, lddy = _rows(dy, "dy", torch.bfloat16, dev, M, N)
+    pl = px = pxs = pb = pdx = pgd = pgu = None
+    ldx = ldb = lddx = K
+    gran = GRAN.ROW
+    if want_weights:
+        if accumulate and (d_down is None or d_up is None):
+            raise ValueError("accumulate adds to given d_down and d_up")
+        pl = _tensor(lora_act, "lora_act", torch.float32, dev, (M, R))
+        if x_scales is None:
+            px, ldx = _rows(x, "x", torch.bfloat16, dev, M, K)
+        else:
+            px, ldx = _rows(x, "x", torch.int8, dev, M, K)
+            gran = GRAN.ROW if x_scales.numel() == M else GRAN.TENSOR
+            pxs = _tensor(x_scales, "x_scales", torch.float32, dev, (M if gran == GRAN.ROW else 1,))
+    elif not want_dx:
+        raise ValueError("nothing is wanted")
+    if want_dx and dx_base is not None:
+        pb, ldb = _rows(dx_base, "dx_base", dt, dev, M, K)
+    with _on(dev, stream):
+        if want_dx:
+            if dx is None:
+                dx = torch.empty((M, K), dtype=dt, device=dev)
+            pdx, lddx = _rows(dx, "dx", dt, dev, M, K)
+        if want_weights:
+            if d_down is None:
+                d_down = torch.empty((A, R, K), dtype=torch.float32, device=dev)
+            if d_up is None:
+                d_up = torch.empty((A, N, R), dtype=torch.float32, device=dev)
+            pgd = _tensor(d_down, "d_down", torch.float32, dev, (A, R, K))
+            pgu = _tensor(d_up, "d_up", torch.float32, dev, (A, N, R))
+        if workspace is None:
+            need = lib.convrot_lora_backward_workspace_size(M, N, K, R, A)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        st = lib.convrot_lora_backward(pdy, lddy, pl, px, ldx, pxs, gran, rot_group, pd, pu, R, A, po, pa, S, ps,
+                                       pb, ldb, pdx, dx_type, lddx, pgd, pgu, int(bool(accumulate)), M, N, K,
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                       torch.cuda.current_stream().cuda_stream)
+    _check(st, "convrot_lora_backward")
+    return (dx if want_dx else None), (d_down if want_weights else None), (d_up if want_weights else None)
+
+
+def convrot_act_checkpoint(z, act, y=None, codes=None, scales=None, stream=None):
+    """y = act(z) (ACT.GELU, ACT.GELU_TANH: z bf16 [rows, C]; ACT.SWIGLU: z
+    bf16 [rows, 2C], gate then linear half), with z kept as int8 codes and one
+    float32 scale per row and 64 columns. Returns (y, codes, scales)."""
+    if z.dim() != 2 or act not in (ACT.GELU, ACT.GELU_TANH, ACT.SWIGLU):
+        raise ValueError("z is [rows, C] (SWIGLU: [rows, 2C]) and act one of ACT")
+    (rows, W), dev = z.shape, z.device
+    if W % (128 if act == ACT.SWIGLU else 64):
+        raise ValueError("C must be a multiple of 64")
+    C = W // 2 if act == ACT.SWIGLU else W
+    pz, ldz = _rows(z, "z", torch.bfloat16, dev, rows, W)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((rows, C), dtype=torch.bfloat16, device=dev)
+        if codes is None:
+            codes = torch.empty((rows, W), dtype=torch.int8, device=dev)
+        if scales is None:
+            scales = torch.empty((rows, W // 64), dtype=torch.float32, device=dev)
+        py, ldy = _rows(y, "y", torch.bfloat16, dev, rows, C)
+        pc = _tensor(codes, "codes", torch.int8, dev, (rows, W))
+        ps = _tensor(scales, "scales", torch.float32, dev, (rows, W // 64))
+        st = lib.convrot_act_checkpoint(pz, ldz, rows, C, act, py, ldy, pc, ps,
+                                        torch.cuda.current_stream().cuda_stream)
+    _check(st, "convrot_act_checkpoint")
+    return y, codes, scales
+
+
+def convrot_act_backward(dy, codes, scales, act, dz=None, stream=None):
+    """dz = dy act'(z) with z read back from the codes and scales of
+    convrot_act_checkpoint; dy bf16 [rows, C], dz bf16 shaped like codes."""
+    if dy.dim() != 2 or act not in (ACT.GELU, ACT.GELU_TANH, ACT.SWIGLU):
+        raise ValueError("dy is [rows, C] and act one of ACT")
+    (rows, C), dev = dy.shape, dy.device
+    if C % 64:
+        raise ValueError("C must be a multiple of 64")
+    W = 2 * C if act == ACT.SWIGLU else C
+    pdy, lddy = _rows(dy, "dy", torch.bfloat16, dev, rows, C)
+    pc = _tensor(codes, "codes", torch.int8, dev, (rows, W))
+    ps = _tensor(scales, "scales", torch.float32, dev, (rows, W // 64))
+    with _on(dev, stream):
+        if dz is None:
+            dz = torch.empty((rows, W), dtype=torch.bfloat16, device=dev)
+        pz, lddz = _rows(dz, "dz", torch.bfloat16, dev, rows, W)
+        st = lib.convrot_act_backward(pdy, lddy, pc, ps, rows, C, act, pz, lddz,
+                                      torch.cuda.current_stream().cuda_stream)
+    _check(st, "convrot_act_backward")
+    return dz

@@ -18,6 +18,7 @@
 #include <mutex>
 
 #include "../../include/convrot.h"
+#include "host.h"
 #include "kernels.h"
 
 namespace {
@@ -98,6 +99,16 @@ constexpr int64_t KMAX = 32768;
 constexpr int64_t DIM_MAX = (int64_t)1 << 31;
 
 }  // namespace
+
+namespace cr {
+
+cr_status host_device_check() { return device_check(); }
+void host_tag(const char* name, int64_t d0, int64_t d1, int64_t d2, int f0, int f1, int f2) {
+  CallTag tag(name, d0, d1, d2, f0, f1, f2);
+}
+cr_status host_finish(hipError_t e, HostEntry entry, uint64_t kernels) { return finish_launch(e, entry, kernels); }
+
+}  // namespace cr
 
 extern "C" {
 

@@ -1,0 +1,796 @@
+// Low-rank adapters of many requests beside one shared projection, forward
+// and backward (gfx950, bf16 matrix cores).
+//
+// The rows of a batch fall into segments, each with an adapter a (or none):
+//   la[m, r]   = sum_k x[m, k] down[a][r, k]                      "shrink"
+//   out[m, n]  = base[m, n] + c_a sum_r la[m, r] up[a][n, r]       "expand"
+// and backward
+//   dla[m, r]  = c_a sum_n dy[m, n] up[a][n, r]                    shrink by up
+//   dx[m, k]   = dx_base[m, k] + sum_r dla[m, r] down[a][r, k]     expand by down
+//   d_up[a]    = c_a sum_m dy[m, :]^T la[m, :]                     "outer"
+//   d_down[a]  = sum_m dla[m, :]^T x[m, :]                         outer
+// With x saved as rotated INT8 codes, x = (s q) H / sqrt(n) per rotation
+// group, so d_down = (sum_m (dla[m, :] s[m])^T q[m, :]) H / sqrt(n): the long
+// sum runs on the codes and only the small [R, K] result is rotated back.
+//
+// la and dla are float32. Where they meet bf16 operands on the matrix cores
+// they are split into three bf16 terms (8 + 8 + 8 bits of the 24), whose
+// products are exact in float32: the only roundings are those of the float32
+// sums and of the stored outputs.
+#include "common.h"
+#include "lora.h"
+#include "rotate.h"
+
+#include <type_traits>
+
+namespace cr {
+
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+CR_DEV v4f mfma16(v8bf a, v8bf b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+// ---------------------------------------------------------------------------
+// segments -> row tiles
+// ---------------------------------------------------------------------------
+// Boundary v of the S + 2 stretches that cover all M rows: the rows before
+// the first segment, the S segments, and the rows behind the last one. Every
+// value lies in [0, M] whatever the offsets hold, so no tile leaves the batch.
+CR_DEV int seg_bound(const LoraSegments& g, int v) {
+  if (v <= 0) return 0;
+  if (v >= g.S + 2) return g.M;
+  const int o = g.off[v - 1];
+  return o < 0 ? 0 : (o > g.M ? g.M : o);
+}
+CR_DEV int seg_adapter(const LoraSegments& g, int v) {   // adapter of stretch v, or -1
+  if (v < 1 || v > g.S) return -1;
+  const int a = g.id[v - 1];
+  return (a < 0 || a >= g.A) ? -1 : a;
+}
+
+struct RowTile {
+  int lo, hi, a;   // rows [lo, hi) of one stretch and its adapter (-1: none); lo == hi: no tile
+};
+
+// inclusive sum over the wave
+CR_DEV int wave_scan(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// Tile t of T rows, counted through the stretches: each wave scans the tile
+// counts of 64 stretches at a time. All 64 lanes take part; the result is
+// the same in all of them.
+template <int T>
+CR_DEV RowTile find_tile(const LoraSegments& g, int t) {
+  const int lane = threadIdx.x & 63;
+  for (int v0 = 0; v0 < g.S + 2; v0 += 64) {
+    const int v = v0 + lane;
+    int lo = 0, hi = 0;
+    if (v < g.S + 2) {
+      lo = seg_bound(g, v);
+      hi = seg_bound(g, v + 1);
+      hi = hi > lo ? hi : lo;
+    }
+    const int n = (hi - lo + T - 1) / T;
+    const int upto = wave_scan(n, lane);
+    const int total = __builtin_amdgcn_readlane(upto, 63);
+    if (t < total) {
+      const int src = __builtin_ctzll(__ballot(upto > t));
+      const int slo = __builtin_amdgcn_readlane(lo, src), shi = __builtin_amdgcn_readlane(hi, src);
+      const int skip = t - (__builtin_amdgcn_readlane(upto, src) - __builtin_amdgcn_readlane(n, src));
+      RowTile r;
+      r.lo = slo + skip * T;
+      r.hi = r.lo + T < shi ? r.lo + T : shi;
+      r.a = __builtin_amdgcn_readfirstlane(seg_adapter(g, v0 + src));
+      return r;
+    }
+    t -= total;
+  }
+  return RowTile{0, 0, -1};
+}
+
+// tiles of T rows that M rows in S segments can need at most
+static unsigned tile_grid(const LoraSegments& g, int T) {
+  const int64_t n = (int64_t)g.M / T + g.S + 2;
+  return (unsigned)(n < g.M ? n : g.M);
+}
+
+// ---------------------------------------------------------------------------
+// operand fragments
+// ---------------------------------------------------------------------------
+CR_DEV v8bf load8(const uint16_t* p, bool ok) {
+  const u32x4 z = {0, 0, 0, 0};
+  return __builtin_bit_cast(v8bf, ok ? *reinterpret_cast<const u32x4*>(p) : z);
+}
+
+// f = hi + mid + lo, each a bf16 value: truncation leaves remainders that are
+// exact in float32. An infinity or NaN goes into hi alone.
+struct Split {
+  uint32_t hi, mid, lo;   // bf16 bits in the upper half
+};
+CR_DEV Split split3(float f) {
+  const uint32_t b = __float_as_uint(f);
+  const bool special = (b & 0x7F800000u) == 0x7F800000u;
+  Split s;
+  s.hi = b & 0xFFFF0000u;
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) s.hi |= 0x00400000u;
+  const float r1 = special ? 0.f : f - __uint_as_float(b & 0xFFFF0000u);
+  s.mid = __float_as_uint(r1) & 0xFFFF0000u;
+  const float r2 = r1 - __uint_as_float(s.mid);
+  s.lo = __float_as_uint(r2) & 0xFFFF0000u;
+  return s;
+}
+// bf16 pair from the upper halves of two words
+CR_DEV uint32_t upper_pair(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+
+struct Frag3 {
+  v8bf hi, mid, lo;
+};
+CR_DEV Frag3 split_frag(const float (&v)[8]) {
+  u32x4 h, m, l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const Split a = split3(v[2 * i]), b = split3(v[2 * i + 1]);
+    h[i] = upper_pair(a.hi, b.hi);
+    m[i] = upper_pair(a.mid, b.mid);
+    l[i] = upper_pair(a.lo, b.lo);
+  }
+  return Frag3{__builtin_bit_cast(v8bf, h), __builtin_bit_cast(v8bf, m), __builtin_bit_cast(v8bf, l)};
+}
+
+// ---------------------------------------------------------------------------
+// shrink: la[m, r] = (c_a) sum_c x[m, c] w[a][r][c]
+// ---------------------------------------------------------------------------
+struct ShrinkArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* w;     // [A][R][C]
+  LoraSegments seg;
+  const float* scale;    // multiplies the result, or null
+  float* la;
+  int R, C;
+};
+
+// A block takes TM x 16 rows of one segment and 16 RG ranks; its NW waves
+// share the columns in stretches of 64 and add their sums through LDS in a
+// fixed order.
+template <int RG, int TM, int NW>
+__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
+  __shared__ float red[NW / 2][RG * TM * 256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = lane & 15, g = lane >> 4;
+  const int r0 = blockIdx.y * 16 * RG;
+  const RowTile t = find_tile<16 * TM>(p.seg, blockIdx.x);
+  if (t.lo >= t.hi) return;
+  if (t.a < 0) {                                  // rows without adapter: zeros
+    const int nr = p.R - r0 < 16 * RG ? p.R - r0 : 16 * RG;
+    for (int k = threadIdx.x; k < (t.hi - t.lo) * nr; k += 64 * NW)
+      p.la[(int64_t)(t.lo + k / nr) * p.R + r0 + k % nr] = 0.f;
+    return;
+  }
+  const uint16_t* xr[TM];
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm) {
+    const int m = t.lo + 16 * tm + i;
+    xr[tm] = p.x + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldx;   // past the tile: a row computed for nothing
+  }
+  const uint16_t* wr[RG];
+#pragma unroll
+  for (int rg = 0; rg < RG; ++rg) {
+    const int r = r0 + 16 * rg + i;
+    wr[rg] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C;
+  }
+  v4f acc[RG][TM];
+#pragma unroll
+  for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) acc[rg][tm] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int c0 = wave * 64; c0 < p.C; c0 += NW * 64) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 + 32 * h + 8 * g;
+      const bool ok = c < p.C;                     // C % 8 == 0
+      v8bf xf[TM], wf[RG];
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) xf[tm] = load8(xr[tm] + c, ok);
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg) wf[rg] = load8(wr[rg] + c, ok);
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm) acc[rg][tm] = mfma16(wf[rg], xf[tm], acc[rg][tm]);
+    }
+  }
+#pragma unroll
+  for (int n = NW / 2; n >= 1; n >>= 1) {
+    if (wave >= n && wave < 2 * n) {
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+          *reinterpret_cast<v4f*>(&red[wave - n][((rg * TM + tm) * 64 + lane) * 4]) = acc[rg][tm];
+    }
+    __syncthreads();
+    if (wave < n) {
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm) {
+          const v4f o = *reinterpret_cast<const v4f*>(&red[wave][((rg * TM + tm) * 64 + lane) * 4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[rg][tm][e] += o[e];
+        }
+    }
+    __syncthreads();
+  }
+  if (wave != 0) return;
+  const float cs = p.scale ? p.scale[t.a] : 1.f;
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm) {
+    const int m = t.lo + 16 * tm + i;
+    if (m >= t.hi) continue;
+#pragma unroll
+    for (int rg = 0; rg < RG; ++rg) {
+      const int r = r0 + 16 * rg + 4 * g;          // R % 8 == 0: four ranks in or out together
+      if (r >= p.R) continue;
+      v4f o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = acc[rg][tm][e] * cs;
+      *reinterpret_cast<v4f*>(p.la + (int64_t)m * p.R + r) = o;
+    }
+  }
+}
+
+static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
+  const int rg = (p.R + 15) / 16;
+  if (p.seg.M <= 256) {
+    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 8>), dim3(tile_grid(p.seg, 16), rg), dim3(512), 0, s, p);
+  } else if (rg <= 1) {
+    hipLaunchKernelGGL((lora_shrink_kernel<1, 2, 8>), dim3(tile_grid(p.seg, 32)), dim3(512), 0, s, p);
+  } else if (rg <= 2) {
+    hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 8>), dim3(tile_grid(p.seg, 32)), dim3(512), 0, s, p);
+  } else {
+    hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 8>), dim3(tile_grid(p.seg, 32), (rg + 3) / 4), dim3(512), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// expand: out[m, c] = base[m, c] + sum_r (c_a la[m, r]) w[a][c][r]
+// ---------------------------------------------------------------------------
+struct ExpandArgs {
+  const float* la;
+  const uint16_t* w;     // [A][C][R]
+  LoraSegments seg;
+  const float* scale;    // multiplies la, or null
+  const void* base;
+  int64_t ldb;
+  void* out;
+  int64_t ldo;
+  int R, C;
+};
+
+template <typename T>
+CR_DEV void load_out8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf16_lo(w[k]);
+      v[2 * k + 1] = bf16_hi(w[k]);
+    }
+  } else {
+    const v4f a = *reinterpret_cast<const v4f*>(p), b = *reinterpret_cast<const v4f*>(p + 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = a[k];
+      v[4 + k] = b[k];
+    }
+  }
+}
+template <typename T>
+CR_DEV void store_out8(T* p, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    u32x4 w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = __builtin_bit_cast(uint32_t, v2bf{(__bf16)v[2 * k], (__bf16)v[2 * k + 1]});   // half to even, NaN kept
+    *reinterpret_cast<u32x4*>(p) = w;
+  } else {
+    *reinterpret_cast<v4f*>(p) = v4f{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<v4f*>(p + 4) = v4f{v[4], v[5], v[6], v[7]};
+  }
+}
+
+// A wave holds the weights of 32 NP columns as operand fragments and walks the
+// rows of its tile, 16 at a time. Column c0 + 32 p + 8 (i / 4) + 4 j + i % 4 is
+// row i of product j, so that a lane's eight sums of products 2p and 2p + 1 are
+// eight neighbouring columns of one row.
+template <int KS, int NP, typename T>
+__global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
+  constexpr int TILE = 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = lane & 15, g = lane >> 4;
+  const RowTile t = find_tile<TILE>(p.seg, blockIdx.x);
+  if (t.lo >= t.hi) return;
+  const int c0 = (blockIdx.y * 4 + wave) * 32 * NP;
+  const T* base = static_cast<const T*>(p.base);
+  T* out = static_cast<T*>(p.out);
+  if (t.a < 0) {                                  // rows without adapter: the base alone
+    if (static_cast<const void*>(base) == static_cast<const void*>(out)) return;
+    for (int k = lane; k < (t.hi - t.lo) * 4 * NP; k += 64) {
+      const int64_t m = t.lo + k / (4 * NP);
+      const int c = c0 + k % (4 * NP) * 8;
+      if (c >= p.C) continue;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (base) load_out8(base + m * p.ldb + c, v);
+      store_out8(out + m * p.ldo + c, v);
+    }
+    return;
+  }
+  if (c0 >= p.C) return;
+  const float cs = p.scale ? p.scale[t.a] : 1.f;
+  v8bf wf[NP][2][KS];
+#pragma unroll
+  for (int q = 0; q < NP; ++q)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      int c = c0 + 32 * q + 8 * (i >> 2) + 4 * j + (i & 3);
+      c = c < p.C ? c : p.C - 1;
+      const uint16_t* w = p.w + ((int64_t)t.a * p.C + c) * p.R;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) wf[q][j][ks] = load8(w + 32 * ks + 8 * g, 32 * ks + 8 * g < p.R);
+    }
+  for (int mt = t.lo; mt < t.hi; mt += 16) {
+    const int m = mt + i;
+    const bool row = m < t.hi;
+    const int64_t mr = row ? m : t.hi - 1;
+    Frag3 lf[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      if (32 * ks + 8 * g < p.R) {
+        load_out8(p.la + mr * p.R + 32 * ks + 8 * g, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= cs;
+      }
+      lf[ks] = split_frag(v);
+    }
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      v4f acc[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          acc[j] = mfma16(wf[q][j][ks], lf[ks].lo, acc[j]);
+          acc[j] = mfma16(wf[q][j][ks], lf[ks].mid, acc[j]);
+          acc[j] = mfma16(wf[q][j][ks], lf[ks].hi, acc[j]);
+        }
+      }
+      const int c = c0 + 32 * q + 8 * g;
+      if (!row || c >= p.C) continue;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (base) load_out8(base + mr * p.ldb + c, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += acc[0][e];
+        v[4 + e] += acc[1][e];
+      }
+      store_out8(out + mr * p.ldo + c, v);
+    }
+  }
+}
+
+template <typename T>
+static void launch_expand_t(const ExpandArgs& p, hipStream_t s) {
+  const unsigned gx = tile_grid(p.seg, 64);
+  if (p.R <= 32)
+    hipLaunchKernelGGL((lora_expand_kernel<1, 4, T>), dim3(gx, (p.C + 511) / 512), dim3(256), 0, s, p);
+  else if (p.R <= 64)
+    hipLaunchKernelGGL((lora_expand_kernel<2, 4, T>), dim3(gx, (p.C + 511) / 512), dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((lora_expand_kernel<4, 2, T>), dim3(gx, (p.C + 255) / 256), dim3(256), 0, s, p);
+}
+static hipError_t launch_expand(const ExpandArgs& p, bool f32, hipStream_t s) {
+  if (f32) launch_expand_t<float>(p, s);
+  else launch_expand_t<uint16_t>(p, s);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// weights [A][rows][cols] -> [A][cols][rows] (the backward pass contracts over
+// the other index): 64 x 64 tiles through LDS
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* in, uint16_t* out, int rows, int cols) {
+  __shared__ uint16_t tile[64][66];
+  const int64_t at = (int64_t)blockIdx.z * rows * cols;
+  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  for (int k = threadIdx.x; k < 64 * 64; k += 256) {
+    const int r = r0 + k / 64, c = c0 + k % 64;
+    if (r < rows && c < cols) tile[k / 64][k % 64] = in[at + (int64_t)r * cols + c];
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < 64 * 64; k += 256) {
+    const int c = c0 + k / 64, r = r0 + k % 64;
+    if (r < rows && c < cols) out[at + (int64_t)c * rows + r] = tile[k % 64][k / 64];
+  }
+}
+static hipError_t launch_transpose(const uint16_t* in, uint16_t* out, int A, int rows, int cols, hipStream_t s) {
+  hipLaunchKernelGGL(lora_transpose_kernel, dim3((cols + 63) / 64, (rows + 63) / 64, A), dim3(256), 0, s, in, out, rows,
+                     cols);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// outer: G[a][r][c] = (c_a) sum over the rows of adapter a of u[m, r] v[m, c]
+// ---------------------------------------------------------------------------
+struct OuterArgs {
+  const float* u;         // [M][R]
+  const void* v;          // bf16 or int8 [M][ldv]
+  int64_t ldv;
+  const float* v_scales;  // int8: multiplies u[m, :] by v_scales[m] (or [0])
+  int v_row_scales;
+  LoraSegments seg;
+  const float* scale;     // multiplies the result, or null
+  float* out;             // [A][R][C], or [A][C][R] when `up`; partial p at out + p * part
+  int64_t part;
+  int P;                  // parts that the rows of an adapter are split into
+  int accumulate;         // add to what out holds (P == 1)
+  int R, C;
+};
+
+// Transposed fragments of an 8 x 8 block: row e of the lane's block holds
+// eight columns; fragment j gets column j of the eight rows.
+CR_DEV v8bf column_frag(const u32x4 (&row)[8], int j) {
+  u32x4 f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = row[2 * k][j >> 1], b = row[2 * k + 1][j >> 1];
+    f[k] = __builtin_amdgcn_perm(b, a, (j & 1) ? 0x07060302u : 0x05040100u);
+  }
+  return __builtin_bit_cast(v8bf, f);
+}
+CR_DEV v8bf column_frag(const u32x2 (&row)[8], int j) {   // int8 codes, exact in bf16
+  u32x4 f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = (float)(int)(int8_t)(row[2 * k][j >> 2] >> (8 * (j & 3)));
+    const float b = (float)(int)(int8_t)(row[2 * k + 1][j >> 2] >> (8 * (j & 3)));
+    f[k] = upper_pair(__float_as_uint(a), __float_as_uint(b));
+  }
+  return __builtin_bit_cast(v8bf, f);
+}
+
+// A block takes 128 columns, 16 RG ranks and part blockIdx.z of an adapter's
+// rows; its four waves take 32-row steps in turn and add their sums through
+// LDS in a fixed order. Lane i of a 16-lane group holds columns 8 i .. 8 i + 7.
+template <int RG, bool CODES, bool UP>
+__global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
+  typedef typename std::conditional<CODES, u32x2, u32x4>::type Row;
+  __shared__ float red[2][RG * 8 * 256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = lane & 15, g = lane >> 4;
+  const int nrb = (p.R + 16 * RG - 1) / (16 * RG);
+  const int a = blockIdx.y / nrb, r0 = blockIdx.y % nrb * 16 * RG;
+  const int c = blockIdx.x * 128 + 8 * i;
+  const bool cok = c < p.C;
+  v4f acc[RG][8];
+#pragma unroll
+  for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[rg][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  int64_t from = 0, to = (int64_t)1 << 62;        // this part of the adapter's rows, counted through its segments
+  if (p.P > 1) {
+    int64_t n = 0;
+    for (int s = lane; s < p.seg.S; s += 64) {
+      const int lo = seg_bound(p.seg, s + 1), hi = seg_bound(p.seg, s + 2);
+      if (hi > lo && seg_adapter(p.seg, s + 1) == a && s < p.seg.S) n += hi - lo;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+    from = n * blockIdx.z / p.P;
+    to = n * (blockIdx.z + 1) / p.P;
+  }
+  int step = 0;
+  int64_t before = 0;
+  for (int s0 = 0; s0 < p.seg.S; s0 += 64) {
+    const int s = s0 + lane;
+    int lo = 0, len = 0;
+    if (s < p.seg.S && seg_adapter(p.seg, s + 1) == a) {
+      lo = seg_bound(p.seg, s + 1);
+      // the last segment ends at off[S], not at M
+      const int hi = seg_bound(p.seg, s + 2);
+      len = hi > lo ? hi - lo : 0;
+    }
+    for (uint64_t left = __ballot(len > 0); left; left &= left - 1) {
+      const int src = __builtin_ctzll(left);
+      const int slo = __builtin_amdgcn_readlane(lo, src), slen = __builtin_amdgcn_readlane(len, src);
+      const int64_t x0 = from > before ? from - before : 0;
+      const int64_t x1 = to - before < slen ? to - before : slen;
+      before += slen;
+      if (x1 <= x0) continue;
+      const int mlo = slo + (int)x0, mhi = slo + (int)x1;
+      for (int m0 = mlo; m0 < mhi; m0 += 32, ++step) {
+        if ((step & 3) != wave) continue;
+        Row row[8];
+        Frag3 uf[RG];
+        float uv[RG][8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int m = m0 + 8 * g + e;
+          const bool ok = m < mhi;
+          const int64_t mr = ok ? m : mhi - 1;
+          Row z{};
+          if constexpr (CODES) row[e] = ok && cok ? *reinterpret_cast<const Row*>(static_cast<const int8_t*>(p.v) + mr * p.ldv + c) : z;
+          else row[e] = ok && cok ? *reinterpret_cast<const Row*>(static_cast<const uint16_t*>(p.v) + mr * p.ldv + c) : z;
+          float vs = 1.f;
+          if constexpr (CODES) vs = p.v_scales[p.v_row_scales ? mr : 0];
+#pragma unroll
+          for (int rg = 0; rg < RG; ++rg) {
+            const int r = r0 + 16 * rg + i;
+            const float f = p.u[mr * p.R + (r < p.R ? r : p.R - 1)];
+            uv[rg][e] = ok ? f * vs : 0.f;
+          }
+        }
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) uf[rg] = split_frag(uv[rg]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const v8bf vf = column_frag(row, j);
+#pragma unroll
+          for (int rg = 0; rg < RG; ++rg) {
+            acc[rg][j] = mfma16(uf[rg].lo, vf, acc[rg][j]);
+            acc[rg][j] = mfma16(uf[rg].mid, vf, acc[rg][j]);
+            acc[rg][j] = mfma16(uf[rg].hi, vf, acc[rg][j]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 2; n >= 1; n >>= 1) {
+    if (wave >= n && wave < 2 * n) {
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<v4f*>(&red[wave - n][((rg * 8 + j) * 64 + lane) * 4]) = acc[rg][j];
+    }
+    __syncthreads();
+    if (wave < n) {
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const v4f o = *reinterpret_cast<const v4f*>(&red[wave][((rg * 8 + j) * 64 + lane) * 4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[rg][j][e] += o[e];
+        }
+    }
+    __syncthreads();
+  }
+  if (wave != 0 || !cok) return;
+  const float cs = p.scale ? p.scale[a] : 1.f;
+  float* out = p.out + blockIdx.z * p.part + (int64_t)a * p.R * p.C;
+#pragma unroll
+  for (int rg = 0; rg < RG; ++rg) {
+    const int r = r0 + 16 * rg + 4 * g;
+    if (r >= p.R) continue;
+    if constexpr (UP) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v4f* o = reinterpret_cast<v4f*>(out + (int64_t)(c + j) * p.R + r);
+        v4f w;
+        if (p.accumulate) w = *o;
+        else w = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] += acc[rg][j][e] * cs;
+        *o = w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float* o = out + (int64_t)(r + e) * p.C + c;
+        if (p.accumulate) load_out8(o, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += acc[rg][j][e] * cs;
+        store_out8(o, v);
+      }
+    }
+  }
+}
+
+template <bool CODES, bool UP>
+static hipError_t launch_outer(const OuterArgs& p, hipStream_t s) {
+  const int ct = (p.C + 127) / 128;
+  if (p.R <= 16)
+    hipLaunchKernelGGL((lora_outer_kernel<1, CODES, UP>), dim3(ct, p.seg.A, p.P), dim3(256), 0, s, p);
+  else if (p.R <= 32)
+    hipLaunchKernelGGL((lora_outer_kernel<2, CODES, UP>), dim3(ct, p.seg.A, p.P), dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((lora_outer_kernel<4, CODES, UP>), dim3(ct, p.seg.A * ((p.R + 63) / 64), p.P), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+// Parts an adapter's rows are split into: enough blocks for the GPU's 256
+// compute units, at least 128 rows each were the rows even.
+static int outer_parts(int64_t M, int64_t C, int A) {
+  const int64_t blocks = ((C + 127) / 128) * A;
+  int64_t P = (512 + blocks - 1) / blocks;
+  const int64_t most = (M + 127) / 128;
+  if (P > most) P = most;
+  return P < 1 ? 1 : (int)P;
+}
+
+// ---------------------------------------------------------------------------
+// join: out = (out +) sum of the P parts, in order
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void lora_join_kernel(const float* part, int P, int64_t n, float* out, int accumulate) {
+  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (k >= n) return;
+  v4f s = *reinterpret_cast<const v4f*>(part + k);
+  for (int q = 1; q < P; ++q) {
+    const v4f o = *reinterpret_cast<const v4f*>(part + q * n + k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += o[e];
+  }
+  v4f* o = reinterpret_cast<v4f*>(out + k);
+  if (accumulate) {
+    const v4f b = *o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += b[e];
+  }
+  *o = s;
+}
+
+// The same with every rotation group of NR columns rotated back: sixteen
+// lanes hold one row's 256 (NR = 1024: 4 x 256) columns, element 16 gL + e of
+// each chunk in register e of its lane.
+template <int NR>
+__global__ __launch_bounds__(256) void lora_join_rotate_kernel(const float* part, int P, int64_t n, float* out,
+                                                               int accumulate) {
+  constexpr int GPS = NR == 1024 ? 4 : 1;
+  const LaneRot lr = lane_rot<NR>(threadIdx.x & 15);
+  const int64_t items = n / (256 * GPS);           // rows are whole groups: chunks follow one another
+  const int64_t item = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const bool ok = item < items;
+  const int64_t k0 = (ok ? item : items - 1) * (256 * GPS) + 16 * lr.gL;
+  float v[GPS][16];
+#pragma unroll
+  for (int g = 0; g < GPS; ++g) {
+    const float* src = part + k0 + 256 * g;
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      v4f s = *reinterpret_cast<const v4f*>(src + e);
+      for (int q = 1; q < P; ++q) {
+        const v4f o = *reinterpret_cast<const v4f*>(src + q * n + e);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] += o[x];
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[g][e + x] = s[x];
+    }
+    const bool cneg = NR == 1024 && chunk_neg(g);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (dreg_neg(e) != cneg) v[g][e] = -v[g][e];
+    butterflies<NR>(v[g], lr);
+  }
+  if constexpr (NR == 1024) bfly_chunks<GPS>(v);
+  if (!ok) return;
+#pragma unroll
+  for (int g = 0; g < GPS; ++g) {
+    float* dst = out + k0 + 256 * g;
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      v4f s;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool neg = (lr.tau < 0.f) != (dreg_neg(e + x) != (NR == 1024 && chunk_neg(g)));
+        s[x] = (neg ? -v[g][e + x] : v[g][e + x]) * RotSize<NR>::inv_sqrt;
+      }
+      v4f* o = reinterpret_cast<v4f*>(dst + e);
+      if (accumulate) {
+        const v4f b = *o;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] += b[x];
+      }
+      *o = s;
+    }
+  }
+}
+
+static hipError_t launch_join(const float* part, int P, int64_t n, float* out, int accumulate, int rot, hipStream_t s) {
+  const dim3 rgrid((unsigned)((n / (rot == 1024 ? 1024 : 256) + 15) / 16));
+  switch (rot) {
+    case 0: hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, part, P, n, out, accumulate); break;
+    case 16: hipLaunchKernelGGL((lora_join_rotate_kernel<16>), rgrid, dim3(256), 0, s, part, P, n, out, accumulate); break;
+    case 64: hipLaunchKernelGGL((lora_join_rotate_kernel<64>), rgrid, dim3(256), 0, s, part, P, n, out, accumulate); break;
+    case 1024: hipLaunchKernelGGL((lora_join_rotate_kernel<1024>), rgrid, dim3(256), 0, s, part, P, n, out, accumulate); break;
+    default: hipLaunchKernelGGL((lora_join_rotate_kernel<256>), rgrid, dim3(256), 0, s, part, P, n, out, accumulate); break;
+  }
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// entry points
+// ---------------------------------------------------------------------------
+hipError_t launch_lora_forward(const LoraForward& p, hipStream_t s, int* kernels) {
+  *kernels = 2;
+  const ShrinkArgs a{p.x, p.ldx, p.down, p.seg, nullptr, p.la, p.R, (int)p.K};
+  hipError_t e = launch_shrink(a, s);
+  if (e != hipSuccess) return e;
+  const ExpandArgs b{p.la, p.up, p.seg, p.scale, p.base, p.ldb, p.out, p.ldo, p.R, (int)p.N};
+  return launch_expand(b, p.out_f32 != 0, s);
+}
+
+// workspace: dla [M][R] float32, up [A][R][N] and down [A][K][R] transposed
+// (bf16), then the parts of the two gradients
+static size_t pad16(size_t n) { return (n + 15) & ~(size_t)15; }
+size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int R, int A) {
+  return pad16((size_t)M * R * 4) + (size_t)A * R * (N + K) * 2 +
+         (size_t)A * R * 4 * ((size_t)outer_parts(M, N, A) * N + (size_t)outer_parts(M, K, A) * K);
+}
+
+hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kernels) {
+  const int A = p.seg.A, M = p.seg.M;
+  const int64_t wn = (int64_t)A * p.R * p.N, wk = (int64_t)A * p.R * p.K;
+  float* dla = reinterpret_cast<float*>(p.ws);
+  uint16_t* up_t = reinterpret_cast<uint16_t*>(p.ws + pad16((size_t)M * p.R * 4));
+  uint16_t* down_t = up_t + wn;
+  float* part_up = reinterpret_cast<float*>(down_t + wk);
+  const int pn = outer_parts(M, p.N, A), pk = outer_parts(M, p.K, A);
+  float* part_down = part_up + pn * wn;
+  hipError_t e = hipSuccess;
+  *kernels = 0;
+  if (p.dx || p.d_down) {
+    ++*kernels;
+    if ((e = launch_transpose(p.up, up_t, A, (int)p.N, p.R, s)) != hipSuccess) return e;
+    const ShrinkArgs a{p.dy, p.lddy, up_t, p.seg, p.scale, dla, p.R, (int)p.N};
+    ++*kernels;
+    if ((e = launch_shrink(a, s)) != hipSuccess) return e;
+  }
+  if (p.dx) {
+    ++*kernels;
+    if ((e = launch_transpose(p.down, down_t, A, p.R, (int)p.K, s)) != hipSuccess) return e;
+    const ExpandArgs b{dla, down_t, p.seg, nullptr, p.dx_base, p.ldb, p.dx, p.lddx, p.R, (int)p.K};
+    ++*kernels;
+    if ((e = launch_expand(b, p.dx_f32 != 0, s)) != hipSuccess) return e;
+  }
+  if (p.d_up) {
+    const bool join = pn > 1;
+    const OuterArgs o{p.la, p.dy, p.lddy, nullptr, 0, p.seg, p.scale, join ? part_up : p.d_up, wn, pn,
+                      !join && p.accumulate, p.R, (int)p.N};
+    ++*kernels;
+    if ((e = launch_outer<false, true>(o, s)) != hipSuccess) return e;
+    if (join) {
+      ++*kernels;
+      if ((e = launch_join(part_up, pn, wn, p.d_up, p.accumulate, 0, s)) != hipSuccess) return e;
+    }
+  }
+  if (p.d_down) {
+    const bool codes = p.x_scales != nullptr;
+    const int rot = codes ? p.rot_group : 0;
+    const bool join = pk > 1 || rot;
+    const OuterArgs o{dla, p.x, p.ldx, p.x_scales, p.x_row_scales, p.seg, nullptr, join ? part_down : p.d_down, wk, pk,
+                      !join && p.accumulate, p.R, (int)p.K};
+    ++*kernels;
+    if ((e = codes ? launch_outer<true, false>(o, s) : launch_outer<false, false>(o, s)) != hipSuccess) return e;
+    if (join) {
+      ++*kernels;
+      if ((e = launch_join(part_down, pk, wk, p.d_down, p.accumulate, rot, s)) != hipSuccess) return e;
+    }
+  }
+  return e;
+}
+
+}  // namespace cr
