@@ -617,7 +617,7 @@ cr_status convrot_lora_backward(const void* dy, int64_t lddy, const float* lora_
  *             gradient of the group is NaN.
  *   forward   y = act(z) of z itself, rounded once
  *   backward  dz = dy act'(scale * code), rounded once
- * Shape: rows >= 1, C % 64 == 0, C <= 32768, rows C < 2^35, leading dimensions
+ * Shape: rows >= 1, C % 64 == 0, C <= 32768, rows C < 2^34, leading dimensions
  * multiples of 8, not below the row length and below 2^31. One launch each.
  */
 typedef enum cr_act {

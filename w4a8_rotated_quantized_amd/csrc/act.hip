@@ -23,36 +23,62 @@ CR_DEV uint32_t bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi});   // round half to even, NaN kept
 }
 
-// sigma(x) and sigma(-x) from e = exp(-|x|) <= 1: neither overflows, and the
-// small one keeps its relative precision.
-struct Sigmoid {
-  float p, q;
-};
-CR_DEV Sigmoid sigmoid(float x) {
-  const float e = expf(-fabsf(x)), inv = 1.f / (1.f + e), small = e * inv;
-  return x < 0.f ? Sigmoid{small, inv} : Sigmoid{inv, small};
-}
-
-constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
 
+// sigma(x) and sigma(-x) from e = exp(-|x|) <= 1: neither overflows, and the
+// small one keeps its relative precision. The hardware reciprocal is within
+// one unit in the last place.
+struct Sigmoid {
+  float p, q;
+};
+CR_DEV Sigmoid sigmoid(float x) {
+  const float e = exp2f(-kLog2e * fabsf(x)), inv = __builtin_amdgcn_rcpf(1.f + e), small = e * inv;
+  return x < 0.f ? Sigmoid{small, inv} : Sigmoid{inv, small};
+}
+
+// Phi(z) and E = exp(-z^2 / 2). With a = |z|, Phi(-a) = E G(a), where
+// G(a) = erfcx(a / sqrt 2) / 2 falls smoothly like 1 / (a sqrt(2 pi)): a
+// polynomial in w = 1 / (1 + 0.36308432 a) without constant term, fitted here by
+// reweighted least squares on 0 <= a <= 15, has relative error 1.1e-6 in
+// float32. Beyond 15, E is below 2^-149.
+struct Normal {
+  float phi, e;
+};
+CR_DEV Normal normal(float z) {
+  const float w = __builtin_amdgcn_rcpf(__builtin_fmaf(0.36308431899331844f, fabsf(z), 1.f));
+  float g = 0.04788525402545929f;
+  g = __builtin_fmaf(g, w, -0.17834912240505219f);
+  g = __builtin_fmaf(g, w, 0.1719096153974533f);
+  g = __builtin_fmaf(g, w, 0.03162514418363571f);
+  g = __builtin_fmaf(g, w, 0.13871920108795166f);
+  g = __builtin_fmaf(g, w, 0.1432841569185257f);
+  g = __builtin_fmaf(g, w, 0.14492595195770264f);
+  const float e = exp2f((-0.5f * kLog2e) * (z * z));
+  const float t = g * w * e;
+  return Normal{z < 0.f ? t : 1.f - t, e};
+}
+
 template <int ACT>
 CR_DEV float act_value(float z) {
-  if constexpr (ACT == CR_ACT_GELU) return z * 0.5f * erfcf(-z * kSqrtHalf);
-  else if constexpr (ACT == CR_ACT_GELU_TANH) return z * sigmoid(kTanhA * (z + kTanhB * z * z * z)).p;
+  if constexpr (ACT == CR_ACT_GELU) return z * normal(z).phi;
+  else if constexpr (ACT == CR_ACT_GELU_TANH)
+    return z * sigmoid(z * __builtin_fmaf(kTanhA * kTanhB, z * z, kTanhA)).p;
   else return z * sigmoid(z).p;
 }
 
 template <int ACT>
 CR_DEV float act_slope(float z) {
   if constexpr (ACT == CR_ACT_GELU) {
-    return 0.5f * erfcf(-z * kSqrtHalf) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+    const Normal n = normal(z);
+    return __builtin_fmaf(z * kInvSqrt2Pi, n.e, n.phi);
   } else {
     z = z > 20.f ? 20.f : (z < -20.f ? -20.f : z);   // the slope is 1 or 0 beyond; z z could overflow; keeps NaN
-    const Sigmoid s = sigmoid(kTanhA * (z + kTanhB * z * z * z));
-    return s.p + z * s.p * s.q * kTanhA * (1.f + 3.f * kTanhB * z * z);
+    const float zz = z * z;
+    const Sigmoid s = sigmoid(z * __builtin_fmaf(kTanhA * kTanhB, zz, kTanhA));
+    return __builtin_fmaf(z * s.p * s.q, __builtin_fmaf(3.f * kTanhA * kTanhB, zz, kTanhA), s.p);
   }
 }
 
@@ -99,8 +125,8 @@ CR_DEV void quantize8(const u32x4& w, const float (&v)[8], int8_t* codes, float*
   if (r != 0.f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float t = fminf(fmaxf(rintf(__fmul_rn(v[i], r)), -127.f), 127.f);
-      q[i >> 2] |= ((uint32_t)(int)t & 0xFFu) << (8 * (i & 3));
+      // |v r| <= 127 (1 + 2^-23): the rounding stays within the range by itself
+      q[i >> 2] |= (__float_as_uint(__fadd_rn(__fmul_rn(v[i], r), CR_MAGIC_RNE)) & 0xFFu) << (8 * (i & 3));
     }
   }
   *reinterpret_cast<u32x2*>(codes) = u32x2{q[0], q[1]};
@@ -113,14 +139,28 @@ CR_DEV void dequantize8(const int8_t* codes, float s, float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = s * (float)(int)(int8_t)(q[i >> 2] >> (8 * (i & 3)));
 }
 
+// n / d for n < 2^31 and 8 <= d <= 4096: M = ceil(2^(31 + l) / d) with
+// 2^(l-1) < d <= 2^l has M d - 2^(31 + l) < 2^l, so n M / 2^(31 + l) has the
+// quotient's integer part.
+struct RowDiv {
+  uint32_t mul;
+  int shift;
+};
+static RowDiv row_div(uint32_t d) {
+  int l = 3;
+  while ((1u << l) < d) ++l;
+  return RowDiv{(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), l - 1};
+}
+
 // One thread: eight consecutive columns of one row (of both halves for
 // SWIGLU); eight consecutive threads: one scale group.
 template <int ACT>
-__global__ __launch_bounds__(256) void act_checkpoint_kernel(ActArgs p) {
-  const int64_t per_row = p.C / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= p.rows * per_row) return;            // whole groups of eight lanes
-  const int64_t m = i / per_row, c = (i % per_row) * 8;
+__global__ __launch_bounds__(256) void act_checkpoint_kernel(ActArgs p, RowDiv d) {
+  const uint32_t per_row = (uint32_t)p.C / 8;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t row = __umulhi(i, d.mul) >> d.shift;
+  if (row >= p.rows) return;                    // whole groups of eight lanes
+  const int64_t m = row, c = (i - row * per_row) * 8;
   const bool first = (threadIdx.x & 7) == 0;
   const uint16_t* in = p.in + m * p.ldi + c;
   float v[8], y[8];
@@ -144,11 +184,12 @@ __global__ __launch_bounds__(256) void act_checkpoint_kernel(ActArgs p) {
 }
 
 template <int ACT>
-__global__ __launch_bounds__(256) void act_backward_kernel(ActArgs p) {
-  const int64_t per_row = p.C / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= p.rows * per_row) return;
-  const int64_t m = i / per_row, c = (i % per_row) * 8;
+__global__ __launch_bounds__(256) void act_backward_kernel(ActArgs p, RowDiv d) {
+  const uint32_t per_row = (uint32_t)p.C / 8;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t row = __umulhi(i, d.mul) >> d.shift;
+  if (row >= p.rows) return;
+  const int64_t m = row, c = (i - row * per_row) * 8;
   float dy[8], v[8];
   unpack8(*reinterpret_cast<const u32x4*>(p.in + m * p.ldi + c), dy);
   uint16_t* out = p.out + m * p.ldo + c;
@@ -175,20 +216,22 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActArgs p) {
 
 hipError_t launch_act_checkpoint(const ActArgs& p, hipStream_t s) {
   const dim3 grid((unsigned)((p.rows * (p.C / 8) + 255) / 256));
+  const RowDiv d = row_div((uint32_t)(p.C / 8));
   switch (p.act) {
-    case CR_ACT_GELU: hipLaunchKernelGGL((act_checkpoint_kernel<CR_ACT_GELU>), grid, dim3(256), 0, s, p); break;
-    case CR_ACT_GELU_TANH: hipLaunchKernelGGL((act_checkpoint_kernel<CR_ACT_GELU_TANH>), grid, dim3(256), 0, s, p); break;
-    default: hipLaunchKernelGGL((act_checkpoint_kernel<CR_ACT_SWIGLU>), grid, dim3(256), 0, s, p); break;
+    case CR_ACT_GELU: hipLaunchKernelGGL((act_checkpoint_kernel<CR_ACT_GELU>), grid, dim3(256), 0, s, p, d); break;
+    case CR_ACT_GELU_TANH: hipLaunchKernelGGL((act_checkpoint_kernel<CR_ACT_GELU_TANH>), grid, dim3(256), 0, s, p, d); break;
+    default: hipLaunchKernelGGL((act_checkpoint_kernel<CR_ACT_SWIGLU>), grid, dim3(256), 0, s, p, d); break;
   }
   return hipGetLastError();
 }
 
 hipError_t launch_act_backward(const ActArgs& p, hipStream_t s) {
   const dim3 grid((unsigned)((p.rows * (p.C / 8) + 255) / 256));
+  const RowDiv d = row_div((uint32_t)(p.C / 8));
   switch (p.act) {
-    case CR_ACT_GELU: hipLaunchKernelGGL((act_backward_kernel<CR_ACT_GELU>), grid, dim3(256), 0, s, p); break;
-    case CR_ACT_GELU_TANH: hipLaunchKernelGGL((act_backward_kernel<CR_ACT_GELU_TANH>), grid, dim3(256), 0, s, p); break;
-    default: hipLaunchKernelGGL((act_backward_kernel<CR_ACT_SWIGLU>), grid, dim3(256), 0, s, p); break;
+    case CR_ACT_GELU: hipLaunchKernelGGL((act_backward_kernel<CR_ACT_GELU>), grid, dim3(256), 0, s, p, d); break;
+    case CR_ACT_GELU_TANH: hipLaunchKernelGGL((act_backward_kernel<CR_ACT_GELU_TANH>), grid, dim3(256), 0, s, p, d); break;
+    default: hipLaunchKernelGGL((act_backward_kernel<CR_ACT_SWIGLU>), grid, dim3(256), 0, s, p, d); break;
   }
   return hipGetLastError();
 }

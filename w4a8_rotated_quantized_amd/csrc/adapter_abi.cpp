@@ -146,7 +146,7 @@ static cr_status act_validate(const void* in, const void* out, const void* codes
   if (!given(in) || !given(out) || !given(codes) || !given(scales)) return CR_ERR_INVALID_ARGUMENT;
   if (act < 0 || act > 2) return CR_ERR_INVALID_ARGUMENT;
   // C bounds the product below 2^51 before it is formed
-  if (rows < 1 || rows >= LD_MAX || C < 64 || C % 64 || C > KMAX || rows * C >= ((int64_t)1 << 35))
+  if (rows < 1 || rows >= LD_MAX || C < 64 || C % 64 || C > KMAX || rows * C >= ((int64_t)1 << 34))
     return CR_ERR_UNSUPPORTED_SHAPE;
   return CR_OK;
 }
