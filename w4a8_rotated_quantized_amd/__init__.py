@@ -398,34 +398,48 @@ def int8_tensorwise_gemm(a_codes, a_scale, w, w_scale, M, N, K, bias=None, out_t
 # batched low-rank adapters and 8-bit activation checkpoints
 # ---------------------------------------------------------------------------
 _OUT_DTYPE = {OUT.BF16: torch.bfloat16, OUT.F32: torch.float32}
+_BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
+_HERE_ALREADY = contextlib.nullcontext()
 
 
-def _tensor(t, what, dtype, device, shape):
-    """A dense tensor argument: dtype, device, shape and contiguity checked."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+def _gpu(t, what):
+    """Index of the GPU that the call runs on: that of its first tensor."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{what} must be on the GPU")
+    return index
+
+
+def _tensor(t, what, dtype, index, shape):
+    """Address of a dense tensor argument; dtype, GPU, shape and contiguity checked."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {index}")
     return t.data_ptr()
 
 
-def _rows(t, what, dtype, device, rows, cols):
+def _rows(t, what, dtype, index, rows, cols):
     """A [rows, cols] argument whose rows may lie further apart: (address, leading dimension)."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a {dtype} [{rows}, {cols}] tensor with contiguous rows on {device}")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (rows, cols):
+        raise ValueError(f"{what} must be a {dtype} [{rows}, {cols}] tensor on GPU {index}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.data_ptr(), (ld if rows > 1 else cols)
 
 
-def _on(device, stream):
-    """The context in which a call allocates and launches: the tensors' device,
-    and the given stream (default: that device's current one)."""
-    if device.type != "cuda":
-        raise ValueError("tensors must be on the GPU")
+def _on(index, stream):
+    """The context in which a call allocates and launches: the tensors' GPU and
+    the given stream (default: that GPU's current one)."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return contextlib.nullcontext()
-        return torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError("stream belongs to another device than the tensors")
+        return _HERE_ALREADY if index == torch.cuda.current_device() else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError("stream belongs to another GPU than the tensors")
     return torch.cuda.stream(stream)
+
+
+# handle of a GPU's current stream, without the stream object around it
+_current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _out_dtype(out_type):
@@ -434,18 +448,17 @@ def _out_dtype(out_type):
     return _OUT_DTYPE[out_type]
 
 
-def _adapters(x, down, up, seg_offsets, seg_adapter, scale, N, K):
-    """Checks what both adapter calls share; (R, A, S) and the addresses of
-    (down, up, seg_offsets, seg_adapter, scale)."""
-    if down.dim() != 3 or up.dim() != 3 or seg_adapter.dim() != 1:
-        raise ValueError("down is [A, R, K], up [A, N, R], seg_adapter [S]")
-    A, R = down.shape[0], down.shape[1]
-    S, dev = seg_adapter.shape[0], x.device
-    return (R, A, S), (_tensor(down, "down", torch.bfloat16, dev, (A, R, K)),
-                       _tensor(up, "up", torch.bfloat16, dev, (A, N, R)),
-                       _tensor(seg_offsets, "seg_offsets", torch.int32, dev, (S + 1,)),
-                       _tensor(seg_adapter, "seg_adapter", torch.int32, dev, (S,)),
-                       None if scale is None else _tensor(scale, "scale", torch.float32, dev, (A,)))
+def _adapters(index, rows, down, up, seg_offsets, seg_adapter, scale):
+    """Checks what both adapter calls share: (A, R, N, K, S) and the addresses
+    of (down, up, seg_offsets, seg_adapter, scale)."""
+    if rows.dim() != 2 or down.dim() != 3 or up.dim() != 3 or seg_adapter.dim() != 1:
+        raise ValueError("x is [M, K], dy [M, N], down [A, R, K], up [A, N, R], seg_adapter [S]")
+    A, R, K = down.shape
+    N, S = up.shape[1], seg_adapter.shape[0]
+    return A, R, N, K, S, (_tensor(down, "down", _BF16, index, (A, R, K)), _tensor(up, "up", _BF16, index, (A, N, R)),
+                           _tensor(seg_offsets, "seg_offsets", _I32, index, (S + 1,)),
+                           _tensor(seg_adapter, "seg_adapter", _I32, index, (S,)),
+                           None if scale is None else _tensor(scale, "scale", _F32, index, (A,)))
 
 
 def convrot_lora_forward(x, down, up, seg_offsets, seg_adapter, scale=None, base=None, out_type=OUT.BF16, out=None,
@@ -461,22 +474,20 @@ def convrot_lora_forward(x, down, up, seg_offsets, seg_adapter, scale=None, base
     and out may lie further apart than their length. Returns (out, lora_act):
     lora_act float32 [M, R] is what convrot_lora_backward reads. Outputs are
     allocated when not given."""
-    if x.dim() != 2 or up.dim() != 3:
-        raise ValueError("x is [M, K], up [A, N, R]")
-    (M, K), N, dev = x.shape, up.shape[1], x.device
-    dt = _out_dtype(out_type)
-    (R, A, S), (pd, pu, po, pa, ps) = _adapters(x, down, up, seg_offsets, seg_adapter, scale, N, K)
-    px, ldx = _rows(x, "x", torch.bfloat16, dev, M, K)
-    pb, ldb = (None, N) if base is None else _rows(base, "base", dt, dev, M, N)
-    with _on(dev, stream):
+    index = _gpu(x, "x")
+    A, R, N, K, S, (pd, pu, po, pa, ps) = _adapters(index, x, down, up, seg_offsets, seg_adapter, scale)
+    M, dt = x.shape[0], _out_dtype(out_type)
+    px, ldx = _rows(x, "x", _BF16, index, M, K)
+    pb, ldb = (None, N) if base is None else _rows(base, "base", dt, index, M, N)
+    with _on(index, stream):
         if out is None:
-            out = torch.empty((M, N), dtype=dt, device=dev)
+            out = torch.empty((M, N), dtype=dt, device=x.device)
         if lora_act is None:
-            lora_act = torch.empty((M, R), dtype=torch.float32, device=dev)
-        py, ldo = _rows(out, "out", dt, dev, M, N)
-        pl = _tensor(lora_act, "lora_act", torch.float32, dev, (M, R))
+            lora_act = torch.empty((M, R), dtype=_F32, device=x.device)
+        py, ldo = _rows(out, "out", dt, index, M, N)
+        pl = _tensor(lora_act, "lora_act", _F32, index, (M, R))
         st = lib.convrot_lora_forward(px, ldx, pd, pu, R, A, po, pa, S, ps, pb, ldb, py, out_type, ldo, pl, M, N, K,
-                                      torch.cuda.current_stream().cuda_stream)
+                                      _current_stream_handle(index))
     _check(st, "convrot_lora_forward")
     return out, lora_act
 
@@ -498,77 +509,79 @@ def convrot_lora_backward(dy, lora_act, x, down, up, seg_offsets, seg_adapter, s
     codes [M, K] that convrot_rotate_quantize (SYM_INT8, per row or per tensor,
     rot_group) made of it, with x_scales float32 [M] or [1]. x and lora_act are
     not read with want_weights=False and may be None then."""
-    if dy.dim() != 2 or down.dim() != 3:
-        raise ValueError("dy is [M, N], down [A, R, K]")
-    (M, N), K, dev = dy.shape, down.shape[2], dy.device
-    dt = _out_dtype(dx_type)
-    (R, A, S), (pd, pu, po, pa, ps) = _adapters(dy, down, up, seg_offsets, seg_adapter, scale, N, K)
-    pdy, lddy = _rows(dy, "dy", torch.bfloat16, dev, M, N)
+    index = _gpu(dy, "dy")
+    A, R, N, K, S, (pd, pu, po, pa, ps) = _adapters(index, dy, down, up, seg_offsets, seg_adapter, scale)
+    M, dt, dev = dy.shape[0], _out_dtype(dx_type), dy.device
+    pdy, lddy = _rows(dy, "dy", _BF16, index, M, N)
     pl = px = pxs = pb = pdx = pgd = pgu = None
     ldx = ldb = lddx = K
     gran = GRAN.ROW
     if want_weights:
         if accumulate and (d_down is None or d_up is None):
             raise ValueError("accumulate adds to given d_down and d_up")
-        pl = _tensor(lora_act, "lora_act", torch.float32, dev, (M, R))
-        if x_scales is None:
-            px, ldx = _rows(x, "x", torch.bfloat16, dev, M, K)
-        else:
-            px, ldx = _rows(x, "x", torch.int8, dev, M, K)
+        if lora_act is None or x is None:
+            raise ValueError("the weight gradients need x and lora_act")
+        pl = _tensor(lora_act, "lora_act", _F32, index, (M, R))
+        px, ldx = _rows(x, "x", _BF16 if x_scales is None else _I8, index, M, K)
+        if x_scales is not None:
             gran = GRAN.ROW if x_scales.numel() == M else GRAN.TENSOR
-            pxs = _tensor(x_scales, "x_scales", torch.float32, dev, (M if gran == GRAN.ROW else 1,))
+            pxs = _tensor(x_scales, "x_scales", _F32, index, (M if gran == GRAN.ROW else 1,))
     elif not want_dx:
         raise ValueError("nothing is wanted")
     if want_dx and dx_base is not None:
-        pb, ldb = _rows(dx_base, "dx_base", dt, dev, M, K)
-    with _on(dev, stream):
+        pb, ldb = _rows(dx_base, "dx_base", dt, index, M, K)
+    with _on(index, stream):
         if want_dx:
             if dx is None:
                 dx = torch.empty((M, K), dtype=dt, device=dev)
-            pdx, lddx = _rows(dx, "dx", dt, dev, M, K)
+            pdx, lddx = _rows(dx, "dx", dt, index, M, K)
         if want_weights:
             if d_down is None:
-                d_down = torch.empty((A, R, K), dtype=torch.float32, device=dev)
+                d_down = torch.empty((A, R, K), dtype=_F32, device=dev)
             if d_up is None:
-                d_up = torch.empty((A, N, R), dtype=torch.float32, device=dev)
-            pgd = _tensor(d_down, "d_down", torch.float32, dev, (A, R, K))
-            pgu = _tensor(d_up, "d_up", torch.float32, dev, (A, N, R))
+                d_up = torch.empty((A, N, R), dtype=_F32, device=dev)
+            pgd = _tensor(d_down, "d_down", _F32, index, (A, R, K))
+            pgu = _tensor(d_up, "d_up", _F32, index, (A, N, R))
         if workspace is None:
             need = lib.convrot_lora_backward_workspace_size(M, N, K, R, A)
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
+        elif workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on GPU {index}")
         st = lib.convrot_lora_backward(pdy, lddy, pl, px, ldx, pxs, gran, rot_group, pd, pu, R, A, po, pa, S, ps,
                                        pb, ldb, pdx, dx_type, lddx, pgd, pgu, int(bool(accumulate)), M, N, K,
                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                       torch.cuda.current_stream().cuda_stream)
+                                       _current_stream_handle(index))
     _check(st, "convrot_lora_backward")
     return (dx if want_dx else None), (d_down if want_weights else None), (d_up if want_weights else None)
+
+
+def _act_width(t, act, what):
+    if t.dim() != 2 or act not in (0, 1, 2):
+        raise ValueError(f"{what} has two dimensions and act is one of ACT")
+    return t.shape
 
 
 def convrot_act_checkpoint(z, act, y=None, codes=None, scales=None, stream=None):
     """y = act(z) (ACT.GELU, ACT.GELU_TANH: z bf16 [rows, C]; ACT.SWIGLU: z
     bf16 [rows, 2C], gate then linear half), with z kept as int8 codes and one
     float32 scale per row and 64 columns. Returns (y, codes, scales)."""
-    if z.dim() != 2 or act not in (ACT.GELU, ACT.GELU_TANH, ACT.SWIGLU):
-        raise ValueError("z is [rows, C] (SWIGLU: [rows, 2C]) and act one of ACT")
-    (rows, W), dev = z.shape, z.device
-    if W % (128 if act == ACT.SWIGLU else 64):
-        raise ValueError("C must be a multiple of 64")
+    index = _gpu(z, "z")
+    rows, W = _act_width(z, act, "z")
     C = W // 2 if act == ACT.SWIGLU else W
-    pz, ldz = _rows(z, "z", torch.bfloat16, dev, rows, W)
-    with _on(dev, stream):
+    if C % 64 or W % 64:
+        raise ValueError("C must be a multiple of 64")
+    pz, ldz = _rows(z, "z", _BF16, index, rows, W)
+    with _on(index, stream):
         if y is None:
-            y = torch.empty((rows, C), dtype=torch.bfloat16, device=dev)
+            y = torch.empty((rows, C), dtype=_BF16, device=z.device)
         if codes is None:
-            codes = torch.empty((rows, W), dtype=torch.int8, device=dev)
+            codes = torch.empty((rows, W), dtype=_I8, device=z.device)
         if scales is None:
-            scales = torch.empty((rows, W // 64), dtype=torch.float32, device=dev)
-        py, ldy = _rows(y, "y", torch.bfloat16, dev, rows, C)
-        pc = _tensor(codes, "codes", torch.int8, dev, (rows, W))
-        ps = _tensor(scales, "scales", torch.float32, dev, (rows, W // 64))
-        st = lib.convrot_act_checkpoint(pz, ldz, rows, C, act, py, ldy, pc, ps,
-                                        torch.cuda.current_stream().cuda_stream)
+            scales = torch.empty((rows, W // 64), dtype=_F32, device=z.device)
+        py, ldy = _rows(y, "y", _BF16, index, rows, C)
+        pc = _tensor(codes, "codes", _I8, index, (rows, W))
+        ps = _tensor(scales, "scales", _F32, index, (rows, W // 64))
+        st = lib.convrot_act_checkpoint(pz, ldz, rows, C, act, py, ldy, pc, ps, _current_stream_handle(index))
     _check(st, "convrot_act_checkpoint")
     return y, codes, scales
 
@@ -576,20 +589,18 @@ def convrot_act_checkpoint(z, act, y=None, codes=None, scales=None, stream=None)
 def convrot_act_backward(dy, codes, scales, act, dz=None, stream=None):
     """dz = dy act'(z) with z read back from the codes and scales of
     convrot_act_checkpoint; dy bf16 [rows, C], dz bf16 shaped like codes."""
-    if dy.dim() != 2 or act not in (ACT.GELU, ACT.GELU_TANH, ACT.SWIGLU):
-        raise ValueError("dy is [rows, C] and act one of ACT")
-    (rows, C), dev = dy.shape, dy.device
+    index = _gpu(dy, "dy")
+    rows, C = _act_width(dy, act, "dy")
     if C % 64:
         raise ValueError("C must be a multiple of 64")
     W = 2 * C if act == ACT.SWIGLU else C
-    pdy, lddy = _rows(dy, "dy", torch.bfloat16, dev, rows, C)
-    pc = _tensor(codes, "codes", torch.int8, dev, (rows, W))
-    ps = _tensor(scales, "scales", torch.float32, dev, (rows, W // 64))
-    with _on(dev, stream):
+    pdy, lddy = _rows(dy, "dy", _BF16, index, rows, C)
+    pc = _tensor(codes, "codes", _I8, index, (rows, W))
+    ps = _tensor(scales, "scales", _F32, index, (rows, W // 64))
+    with _on(index, stream):
         if dz is None:
-            dz = torch.empty((rows, W), dtype=torch.bfloat16, device=dev)
-        pz, lddz = _rows(dz, "dz", torch.bfloat16, dev, rows, W)
-        st = lib.convrot_act_backward(pdy, lddy, pc, ps, rows, C, act, pz, lddz,
-                                      torch.cuda.current_stream().cuda_stream)
+            dz = torch.empty((rows, W), dtype=_BF16, device=dy.device)
+        pz, lddz = _rows(dz, "dz", _BF16, index, rows, W)
+        st = lib.convrot_act_backward(pdy, lddy, pc, ps, rows, C, act, pz, lddz, _current_stream_handle(index))
     _check(st, "convrot_act_backward")
     return dz

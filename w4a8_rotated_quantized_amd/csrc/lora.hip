@@ -69,11 +69,12 @@ CR_DEV RowTile find_tile(const LoraSegments& g, int t) {
   const int lane = threadIdx.x & 63;
   for (int v0 = 0; v0 < g.S + 2; v0 += 64) {
     const int v = v0 + lane;
-    int lo = 0, hi = 0;
+    int lo = 0, hi = 0, a = -1;
     if (v < g.S + 2) {
       lo = seg_bound(g, v);
       hi = seg_bound(g, v + 1);
       hi = hi > lo ? hi : lo;
+      a = seg_adapter(g, v);        // with the offsets: one wait for all three
     }
     const int n = (hi - lo + T - 1) / T;
     const int upto = wave_scan(n, lane);
@@ -85,7 +86,7 @@ CR_DEV RowTile find_tile(const LoraSegments& g, int t) {
       RowTile r;
       r.lo = slo + skip * T;
       r.hi = r.lo + T < shi ? r.lo + T : shi;
-      r.a = __builtin_amdgcn_readfirstlane(seg_adapter(g, v0 + src));
+      r.a = __builtin_amdgcn_readlane(a, src);
       return r;
     }
     t -= total;
@@ -155,12 +156,12 @@ struct ShrinkArgs {
   int R, C;
 };
 
-// A block takes TM x 16 rows of one segment and 16 RG ranks; its NW waves
-// share the columns in stretches of 64 and add their sums through LDS in a
-// fixed order.
-template <int RG, int TM, int NW>
+// A block takes TM x 16 rows of one segment and 16 RG ranks. Its NW waves
+// share the columns in stretches of 32 U, each with all its loads in flight
+// before the first product, and add their sums through LDS in a fixed order.
+template <int RG, int TM, int NW, int U>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
-  __shared__ float red[NW / 2][RG * TM * 256];
+  __shared__ v4f red[NW][RG * TM * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.y * 16 * RG;
@@ -176,29 +177,55 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
 #pragma unroll
   for (int tm = 0; tm < TM; ++tm) {
     const int m = t.lo + 16 * tm + i;
-    xr[tm] = p.x + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldx;   // past the tile: a row computed for nothing
+    xr[tm] = p.x + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldx + 8 * g;   // past the tile: computed for nothing
   }
   const uint16_t* wr[RG];
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg) {
     const int r = r0 + 16 * rg + i;
-    wr[rg] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C;
+    wr[rg] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C + 8 * g;
   }
   v4f acc[RG][TM];
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) acc[rg][tm] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int c0 = wave * 64; c0 < p.C; c0 += NW * 64) {
+  int c0 = wave * 32 * U;
+  for (; c0 + 32 * U <= p.C; c0 += NW * 32 * U) {
+    u32x4 xf[U][TM], wf[U][RG];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = c0 + 32 * h + 8 * g;
-      const bool ok = c < p.C;                     // C % 8 == 0
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) xf[u][tm] = *reinterpret_cast<const u32x4*>(xr[tm] + c0 + 32 * u);
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg) wf[u][rg] = *reinterpret_cast<const u32x4*>(wr[rg] + c0 + 32 * u);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+          acc[rg][tm] = mfma16(__builtin_bit_cast(v8bf, wf[u][rg]), __builtin_bit_cast(v8bf, xf[u][tm]), acc[rg][tm]);
+  }
+  if (c0 < p.C) {                                 // the last columns: zeros past C (C % 8 == 0)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ok = c0 + 32 * u + 8 * g < p.C;
+      const int c = ok ? c0 + 32 * u : -8 * g;    // past C: the row's first columns, not used
+      const u32x4 z = {0, 0, 0, 0};
       v8bf xf[TM], wf[RG];
 #pragma unroll
-      for (int tm = 0; tm < TM; ++tm) xf[tm] = load8(xr[tm] + c, ok);
+      for (int tm = 0; tm < TM; ++tm) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(xr[tm] + c);
+        xf[tm] = __builtin_bit_cast(v8bf, ok ? v : z);
+      }
 #pragma unroll
-      for (int rg = 0; rg < RG; ++rg) wf[rg] = load8(wr[rg] + c, ok);
+      for (int rg = 0; rg < RG; ++rg) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(wr[rg] + c);
+        wf[rg] = __builtin_bit_cast(v8bf, ok ? v : z);
+      }
 #pragma unroll
       for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
@@ -206,55 +233,36 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
     }
   }
 #pragma unroll
-  for (int n = NW / 2; n >= 1; n >>= 1) {
-    if (wave >= n && wave < 2 * n) {
+  for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm)
-          *reinterpret_cast<v4f*>(&red[wave - n][((rg * TM + tm) * 64 + lane) * 4]) = acc[rg][tm];
-    }
-    __syncthreads();
-    if (wave < n) {
-#pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm) {
-          const v4f o = *reinterpret_cast<const v4f*>(&red[wave][((rg * TM + tm) * 64 + lane) * 4]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[rg][tm][e] += o[e];
-        }
-    }
-    __syncthreads();
-  }
-  if (wave != 0) return;
+    for (int tm = 0; tm < TM; ++tm) red[wave][(rg * TM + tm) * 64 + lane] = acc[rg][tm];
+  __syncthreads();
   const float cs = p.scale ? p.scale[t.a] : 1.f;
+  for (int k = threadIdx.x; k < RG * TM * 64; k += 64 * NW) {
+    const int rg = k / 64 / TM, tm = k / 64 % TM, kl = k % 64;
+    const int m = t.lo + 16 * tm + (kl & 15), r = r0 + 16 * rg + 4 * (kl >> 4);
+    if (m >= t.hi || r >= p.R) continue;           // R % 8 == 0: four ranks in or out together
+    v4f s = red[0][k];
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const int m = t.lo + 16 * tm + i;
-    if (m >= t.hi) continue;
+    for (int n = 1; n < NW; ++n)
 #pragma unroll
-    for (int rg = 0; rg < RG; ++rg) {
-      const int r = r0 + 16 * rg + 4 * g;          // R % 8 == 0: four ranks in or out together
-      if (r >= p.R) continue;
-      v4f o;
+      for (int e = 0; e < 4; ++e) s[e] += red[n][k][e];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = acc[rg][tm][e] * cs;
-      *reinterpret_cast<v4f*>(p.la + (int64_t)m * p.R + r) = o;
-    }
+    for (int e = 0; e < 4; ++e) s[e] *= cs;
+    *reinterpret_cast<v4f*>(p.la + (int64_t)m * p.R + r) = s;
   }
 }
 
 static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
   const int rg = (p.R + 15) / 16;
   if (p.seg.M <= 256) {
-    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 8>), dim3(tile_grid(p.seg, 16), rg), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 8>), dim3(tile_grid(p.seg, 16), rg), dim3(1024), 0, s, p);
   } else if (rg <= 1) {
-    hipLaunchKernelGGL((lora_shrink_kernel<1, 2, 8>), dim3(tile_grid(p.seg, 32)), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<1, 2, 8, 8>), dim3(tile_grid(p.seg, 32)), dim3(512), 0, s, p);
   } else if (rg <= 2) {
-    hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 8>), dim3(tile_grid(p.seg, 32)), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 8, 8>), dim3(tile_grid(p.seg, 32)), dim3(512), 0, s, p);
   } else {
-    hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 8>), dim3(tile_grid(p.seg, 32), (rg + 3) / 4), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 8, 4>), dim3(tile_grid(p.seg, 32), (rg + 3) / 4), dim3(512), 0, s, p);
   }
   return hipGetLastError();
 }
