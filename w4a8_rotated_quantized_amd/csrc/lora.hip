@@ -32,32 +32,35 @@ CR_DEV v4f mfma16(v8bf a, v8bf b, v4f c) { return __builtin_amdgcn_mfma_f32_16x1
 // ---------------------------------------------------------------------------
 // segments -> row tiles
 // ---------------------------------------------------------------------------
-// Boundary v of the S + 2 stretches that cover all M rows: the rows before
-// the first segment, the S segments, and the rows behind the last one. Every
-// value lies in [0, M] whatever the offsets hold, so no tile leaves the batch.
+// Boundary v (0 .. S + 2) of the S + 2 stretches that cover all M rows: the
+// rows before the first segment, the S segments, and the rows behind the last
+// one. Every value lies in [0, M] whatever the offsets hold, so no tile leaves
+// the batch. The load is unconditional, its index clamped: loads of several
+// boundaries are then under way together.
 CR_DEV int seg_bound(const LoraSegments& g, int v) {
-  if (v <= 0) return 0;
-  if (v >= g.S + 2) return g.M;
-  const int o = g.off[v - 1];
-  return o < 0 ? 0 : (o > g.M ? g.M : o);
+  const int at = v - 1;
+  int o = g.off[at < 0 ? 0 : (at > g.S ? g.S : at)];
+  o = o < 0 ? 0 : (o > g.M ? g.M : o);
+  return v <= 0 ? 0 : (v >= g.S + 2 ? g.M : o);
 }
 CR_DEV int seg_adapter(const LoraSegments& g, int v) {   // adapter of stretch v, or -1
-  if (v < 1 || v > g.S) return -1;
-  const int a = g.id[v - 1];
-  return (a < 0 || a >= g.A) ? -1 : a;
+  const int at = v - 1;
+  const int a = g.id[at < 0 ? 0 : (at >= g.S ? g.S - 1 : at)];
+  return (v < 1 || v > g.S || a < 0 || a >= g.A) ? -1 : a;
 }
 
 struct RowTile {
   int lo, hi, a;   // rows [lo, hi) of one stretch and its adapter (-1: none); lo == hi: no tile
 };
 
-// inclusive sum over the wave
-CR_DEV int wave_scan(int x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+// inclusive sum over the wave's 64 lanes: within rows of 16, then across them
+CR_DEV int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);   // row_shr:2
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);   // row_shr:4
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);   // row_shr:8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
   return x;
 }
 
@@ -69,15 +72,10 @@ CR_DEV RowTile find_tile(const LoraSegments& g, int t) {
   const int lane = threadIdx.x & 63;
   for (int v0 = 0; v0 < g.S + 2; v0 += 64) {
     const int v = v0 + lane;
-    int lo = 0, hi = 0, a = -1;
-    if (v < g.S + 2) {
-      lo = seg_bound(g, v);
-      hi = seg_bound(g, v + 1);
-      hi = hi > lo ? hi : lo;
-      a = seg_adapter(g, v);        // with the offsets: one wait for all three
-    }
+    const int lo = seg_bound(g, v), end = seg_bound(g, v + 1), a = seg_adapter(g, v);
+    const int hi = end > lo && v < g.S + 2 ? end : lo;
     const int n = (hi - lo + T - 1) / T;
-    const int upto = wave_scan(n, lane);
+    const int upto = wave_scan(n);
     const int total = __builtin_amdgcn_readlane(upto, 63);
     if (t < total) {
       const int src = __builtin_ctzll(__ballot(upto > t));
@@ -143,6 +141,14 @@ CR_DEV Frag3 split_frag(const float (&v)[8]) {
   return Frag3{__builtin_bit_cast(v8bf, h), __builtin_bit_cast(v8bf, m), __builtin_bit_cast(v8bf, l)};
 }
 
+// Between LDS accesses of one wave to what its other lanes wrote or will
+// write: the hardware keeps their order, the compiler has to as well.
+CR_DEV void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------------------
 // shrink: la[m, r] = (c_a) sum_c x[m, c] w[a][r][c]
 // ---------------------------------------------------------------------------
@@ -156,13 +162,32 @@ struct ShrinkArgs {
   int R, C;
 };
 
+typedef __attribute__((address_space(1))) void* lora_gptr;
+typedef __attribute__((address_space(3))) void* lora_lptr;
+
+// s_waitcnt vmcnt(N), other counters untouched (gfx9 encoding: vmcnt[3:0] in
+// bits 3:0, vmcnt[5:4] in bits 15:14, expcnt in bits 6:4, lgkmcnt in bits 11:8)
+template <int N>
+CR_DEV void wait_vmcnt() {
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
 // A block takes TM x 16 rows of one segment and 16 RG ranks. Its NW waves
-// share the columns in stretches of 32 U, each with all its loads in flight
-// before the first product, and add their sums through LDS in a fixed order.
-template <int RG, int TM, int NW, int U>
+// share the columns in stages of 64 and add their sums through LDS in a fixed
+// order. A stage goes straight from memory into the wave's own LDS ring of D
+// slots: one load moves 8 rows x 128 bytes, neighbouring lanes taking
+// neighbouring 16 bytes, so that every request is a whole line (the operand
+// order of the matrix cores, neighbouring lanes on different rows, reads the
+// same bytes from L2 2.6 times slower: 15.5 against 5.9 us for 256 x 512 KB).
+// Within a row's 128 bytes, chunk q lies at position q ^ (row % 8), which
+// spreads the fragment reads over the banks.
+template <int RG, int TM, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
-  __shared__ v4f red[NW][RG * TM * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int NL = 2 * (TM + RG);                // loads (KB) of a stage
+  constexpr int RED = RG * TM * 64;                // 16-byte sums of a wave
+  constexpr int RING = D * NL * 1024 > RED * 16 ? D * NL * 1024 : RED * 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * RING];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.y * 16 * RG;
   const RowTile t = find_tile<16 * TM>(p.seg, blockIdx.x);
@@ -173,80 +198,86 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
       p.la[(int64_t)(t.lo + k / nr) * p.R + r0 + k % nr] = 0.f;
     return;
   }
-  const uint16_t* xr[TM];
+  const int lr = lane >> 3, lc = 8 * ((lane & 7) ^ lr);   // row and column of the lane's 16 bytes in a load
+  const uint16_t* src[NL];
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const int m = t.lo + 16 * tm + i;
-    xr[tm] = p.x + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldx + 8 * g;   // past the tile: computed for nothing
+  for (int n = 0; n < NL; ++n) {
+    if (n < 2 * TM) {
+      const int m = t.lo + 8 * n + lr;
+      src[n] = p.x + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldx;          // past the tile: computed for nothing
+    } else {
+      const int r = r0 + 8 * (n - 2 * TM) + lr;
+      src[n] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C;
+    }
   }
-  const uint16_t* wr[RG];
+  uint8_t* ring = lds + wave * RING;
+  auto load = [&](int s, int slot) {               // stage s of this wave
+    int c = (s * NW + wave) * 64 + lc;
+    c = c < p.C ? c : 0;                           // past the last column: loaded for nothing
 #pragma unroll
-  for (int rg = 0; rg < RG; ++rg) {
-    const int r = r0 + 16 * rg + i;
-    wr[rg] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C + 8 * g;
-  }
+    for (int n = 0; n < NL; ++n)
+      __builtin_amdgcn_global_load_lds((lora_gptr)(src[n] + c), (lora_lptr)(ring + (slot * NL + n) * 1024), 16, 0, 0);
+  };
   v4f acc[RG][TM];
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) acc[rg][tm] = v4f{0.f, 0.f, 0.f, 0.f};
-  int c0 = wave * 32 * U;
-  for (; c0 + 32 * U <= p.C; c0 += NW * 32 * U) {
-    u32x4 xf[U][TM], wf[U][RG];
+  const int stages = ((p.C + 63) / 64 - wave + NW - 1) / NW;   // may be 0
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+  for (int d = 0; d < D; ++d)
+    if (d < stages) load(d, d);
+  int slot = 0;
+#pragma unroll 1
+  for (int s = 0; s < stages; ++s) {
+    // in flight: stages s .. s + D - 1, fewer at the end
+    if (D > 1 && s + D - 1 < stages) wait_vmcnt<(D - 1) * NL>();
+    else wait_vmcnt<0>();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    u32x4 f[NL / 2][2];                                // n = 2 j, 2 j + 1 hold the 16 rows of operand j
 #pragma unroll
-      for (int tm = 0; tm < TM; ++tm) xf[u][tm] = *reinterpret_cast<const u32x4*>(xr[tm] + c0 + 32 * u);
+    for (int j = 0; j < NL / 2; ++j)
 #pragma unroll
-      for (int rg = 0; rg < RG; ++rg) wf[u][rg] = *reinterpret_cast<const u32x4*>(wr[rg] + c0 + 32 * u);
+      for (int h = 0; h < 2; ++h)
+        f[j][h] = *reinterpret_cast<const u32x4*>(ring + (slot * NL + 2 * j) * 1024 + i * 128 + (((4 * h + g) ^ (i & 7)) * 16));
+    __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): read before the slot is filled again
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    if (s + D < stages) load(s + D, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
+    const int c0 = (s * NW + wave) * 64;
+    if (c0 + 64 > p.C) {                           // the last columns: zeros past C (C % 8 == 0)
+      const u32x4 z = {0, 0, 0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool ok = c0 + 32 * h + 8 * g < p.C;
+#pragma unroll
+        for (int j = 0; j < NL / 2; ++j) f[j][h] = ok ? f[j][h] : z;
+      }
     }
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
-          acc[rg][tm] = mfma16(__builtin_bit_cast(v8bf, wf[u][rg]), __builtin_bit_cast(v8bf, xf[u][tm]), acc[rg][tm]);
+          acc[rg][tm] = mfma16(__builtin_bit_cast(v8bf, f[TM + rg][h]), __builtin_bit_cast(v8bf, f[tm][h]), acc[rg][tm]);
   }
-  if (c0 < p.C) {                                 // the last columns: zeros past C (C % 8 == 0)
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool ok = c0 + 32 * u + 8 * g < p.C;
-      const int c = ok ? c0 + 32 * u : -8 * g;    // past C: the row's first columns, not used
-      const u32x4 z = {0, 0, 0, 0};
-      v8bf xf[TM], wf[RG];
-#pragma unroll
-      for (int tm = 0; tm < TM; ++tm) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(xr[tm] + c);
-        xf[tm] = __builtin_bit_cast(v8bf, ok ? v : z);
-      }
-#pragma unroll
-      for (int rg = 0; rg < RG; ++rg) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(wr[rg] + c);
-        wf[rg] = __builtin_bit_cast(v8bf, ok ? v : z);
-      }
-#pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm) acc[rg][tm] = mfma16(wf[rg], xf[tm], acc[rg][tm]);
-    }
-  }
+  __syncthreads();                                 // the rings are done with: their memory takes the sums
+  v4f* red = reinterpret_cast<v4f*>(lds);
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-    for (int tm = 0; tm < TM; ++tm) red[wave][(rg * TM + tm) * 64 + lane] = acc[rg][tm];
+    for (int tm = 0; tm < TM; ++tm) red[wave * RED + (rg * TM + tm) * 64 + lane] = acc[rg][tm];
   __syncthreads();
   const float cs = p.scale ? p.scale[t.a] : 1.f;
-  for (int k = threadIdx.x; k < RG * TM * 64; k += 64 * NW) {
+  for (int k = threadIdx.x; k < RED; k += 64 * NW) {
     const int rg = k / 64 / TM, tm = k / 64 % TM, kl = k % 64;
     const int m = t.lo + 16 * tm + (kl & 15), r = r0 + 16 * rg + 4 * (kl >> 4);
     if (m >= t.hi || r >= p.R) continue;           // R % 8 == 0: four ranks in or out together
-    v4f s = red[0][k];
-#pragma unroll
+    v4f s = red[k];
     for (int n = 1; n < NW; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] += red[n][k][e];
+      for (int e = 0; e < 4; ++e) s[e] += red[n * RED + k][e];
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] *= cs;
     *reinterpret_cast<v4f*>(p.la + (int64_t)m * p.R + r) = s;
@@ -256,13 +287,13 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
 static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
   const int rg = (p.R + 15) / 16;
   if (p.seg.M <= 256) {
-    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 8>), dim3(tile_grid(p.seg, 16), rg), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 2>), dim3(tile_grid(p.seg, 16), rg), dim3(1024), 0, s, p);
   } else if (rg <= 1) {
-    hipLaunchKernelGGL((lora_shrink_kernel<1, 2, 8, 8>), dim3(tile_grid(p.seg, 32)), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<1, 2, 6, 2>), dim3(tile_grid(p.seg, 32)), dim3(384), 0, s, p);
   } else if (rg <= 2) {
-    hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 8, 8>), dim3(tile_grid(p.seg, 32)), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 4, 2>), dim3(tile_grid(p.seg, 32)), dim3(256), 0, s, p);
   } else {
-    hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 8, 4>), dim3(tile_grid(p.seg, 32), (rg + 3) / 4), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 6, 1>), dim3(tile_grid(p.seg, 32), (rg + 3) / 4), dim3(384), 0, s, p);
   }
   return hipGetLastError();
 }
@@ -314,98 +345,143 @@ CR_DEV void store_out8(T* p, const float (&v)[8]) {
   }
 }
 
-// A wave holds the weights of 32 NP columns as operand fragments and walks the
-// rows of its tile, 16 at a time. Column c0 + 32 p + 8 (i / 4) + 4 j + i % 4 is
-// row i of product j, so that a lane's eight sums of products 2p and 2p + 1 are
-// eight neighbouring columns of one row.
-template <int KS, int NP, typename T>
+// A wave holds the weights of 16 NJ columns as operand fragments and walks the
+// rows of its tile, 16 at a time. The sums of a 16 x 16 NJ block go through LDS,
+// so that base and out move as whole runs of columns, and the next block's base
+// and lora_act are on their way during the products.
+template <int KS, int NJ, typename T, bool BASE>
 __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
-  constexpr int TILE = 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int TILE = 64, W = 16 * NJ;
+  constexpr int V = 16 / sizeof(T);               // columns of one 16-byte access
+  constexpr int CPR = W / V;                      // accesses per row
+  constexpr int NB = 16 * CPR / 64;               // accesses per lane and block
+  __shared__ float lds[4][16][W + 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
   const RowTile t = find_tile<TILE>(p.seg, blockIdx.x);
   if (t.lo >= t.hi) return;
-  const int c0 = (blockIdx.y * 4 + wave) * 32 * NP;
+  const int c0 = (blockIdx.y * 4 + wave) * W;
+  if (c0 >= p.C) return;                          // no barrier below: every wave works for itself
   const T* base = static_cast<const T*>(p.base);
   T* out = static_cast<T*>(p.out);
+  const int brow = lane / CPR, bcol = c0 + lane % CPR * V;   // access q: row brow + q * 64 / CPR, columns bcol ..
+  const bool cok = bcol < p.C;                    // C % 8 == 0: an access lies in or out as a whole
+  const int bc = cok ? bcol : 0;
+  auto load_base = [&](u32x4 (&b)[NB], int mt) {
+#pragma unroll
+    for (int q = 0; q < NB; ++q) {
+      const int m = mt + brow + q * (64 / CPR);
+      b[q] = *reinterpret_cast<const u32x4*>(base + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldb + bc);
+    }
+  };
   if (t.a < 0) {                                  // rows without adapter: the base alone
     if (static_cast<const void*>(base) == static_cast<const void*>(out)) return;
-    for (int k = lane; k < (t.hi - t.lo) * 4 * NP; k += 64) {
-      const int64_t m = t.lo + k / (4 * NP);
-      const int c = c0 + k % (4 * NP) * 8;
-      if (c >= p.C) continue;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (base) load_out8(base + m * p.ldb + c, v);
-      store_out8(out + m * p.ldo + c, v);
+    for (int mt = t.lo; mt < t.hi; mt += 16) {
+      u32x4 b[NB];
+#pragma unroll
+      for (int q = 0; q < NB; ++q) b[q] = u32x4{0, 0, 0, 0};
+      if constexpr (BASE) load_base(b, mt);
+#pragma unroll
+      for (int q = 0; q < NB; ++q) {
+        const int m = mt + brow + q * (64 / CPR);
+        if (m < t.hi && cok) *reinterpret_cast<u32x4*>(out + (int64_t)m * p.ldo + bcol) = b[q];
+      }
     }
     return;
   }
-  if (c0 >= p.C) return;
-  const float cs = p.scale ? p.scale[t.a] : 1.f;
-  v8bf wf[NP][2][KS];
+  u32x4 bb[2][NB];
 #pragma unroll
-  for (int q = 0; q < NP; ++q)
+  for (int q = 0; q < NB; ++q) bb[0][q] = bb[1][q] = u32x4{0, 0, 0, 0};
+  if constexpr (BASE) load_base(bb[0], t.lo);
+  float lf[2][KS][8];
+  auto load_la = [&](float (&l)[KS][8], int mt) {
+    const int64_t m = mt + i < t.hi ? mt + i : t.hi - 1;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      int c = c0 + 32 * q + 8 * (i >> 2) + 4 * j + (i & 3);
-      c = c < p.C ? c : p.C - 1;
-      const uint16_t* w = p.w + ((int64_t)t.a * p.C + c) * p.R;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) wf[q][j][ks] = load8(w + 32 * ks + 8 * g, 32 * ks + 8 * g < p.R);
+    for (int ks = 0; ks < KS; ++ks) {
+      const int r = 32 * ks + 8 * g;
+      load_out8(p.la + m * p.R + (r < p.R ? r : 0), l[ks]);
     }
-  for (int mt = t.lo; mt < t.hi; mt += 16) {
-    const int m = mt + i;
-    const bool row = m < t.hi;
-    const int64_t mr = row ? m : t.hi - 1;
-    Frag3 lf[KS];
+  };
+  load_la(lf[0], t.lo);
+  const float cs = p.scale ? p.scale[t.a] : 1.f;
+  v8bf wf[NJ][KS];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int c = c0 + 16 * j + i < p.C ? c0 + 16 * j + i : p.C - 1;
+    const uint16_t* w = p.w + ((int64_t)t.a * p.C + c) * p.R;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int r = 32 * ks + 8 * g;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(w + (r < p.R ? r : 0)), z = {0, 0, 0, 0};
+      wf[j][ks] = __builtin_bit_cast(v8bf, r < p.R ? v : z);
+    }
+  }
+  auto block = [&](u32x4 (&b)[NB], u32x4 (&bn)[NB], float (&l)[KS][8], float (&ln)[KS][8], int mt) {
+    // behind the tile: its last row once more, for nothing
+    if constexpr (BASE) load_base(bn, mt + 16);
+    load_la(ln, mt + 16);
+    v4f acc[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       float v[8];
+      const bool ok = 32 * ks + 8 * g < p.R;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      if (32 * ks + 8 * g < p.R) {
-        load_out8(p.la + mr * p.R + 32 * ks + 8 * g, v);
+      for (int e = 0; e < 8; ++e) v[e] = ok ? l[ks][e] * cs : 0.f;
+      const Frag3 f = split_frag(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= cs;
-      }
-      lf[ks] = split_frag(v);
+      for (int j = 0; j < NJ; ++j) acc[j] = mfma16(wf[j][ks], f.lo, acc[j]);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[j] = mfma16(wf[j][ks], f.mid, acc[j]);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[j] = mfma16(wf[j][ks], f.hi, acc[j]);
     }
 #pragma unroll
-    for (int q = 0; q < NP; ++q) {
-      v4f acc[2];
+    for (int j = 0; j < NJ; ++j) *reinterpret_cast<v4f*>(&lds[wave][i][16 * j + 4 * g]) = acc[j];
+    wave_lds_order();
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < NB; ++q) {
+      const int row = brow + q * (64 / CPR);
+      float d[V];
+      const float* src = &lds[wave][row][lane % CPR * V];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          acc[j] = mfma16(wf[q][j][ks], lf[ks].lo, acc[j]);
-          acc[j] = mfma16(wf[q][j][ks], lf[ks].mid, acc[j]);
-          acc[j] = mfma16(wf[q][j][ks], lf[ks].hi, acc[j]);
-        }
+      for (int e = 0; e < V; e += 4) {
+        const v4f x = *reinterpret_cast<const v4f*>(src + e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[e + k] = x[k];
       }
-      const int c = c0 + 32 * q + 8 * g;
-      if (!row || c >= p.C) continue;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (base) load_out8(base + mr * p.ldb + c, v);
+      u32x4 o;
+      if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] += acc[0][e];
-        v[4 + e] += acc[1][e];
+        for (int k = 0; k < 4; ++k)                // half to even, NaN kept
+          o[k] = __builtin_bit_cast(uint32_t, v2bf{(__bf16)(bf16_lo(b[q][k]) + d[2 * k]),
+                                                   (__bf16)(bf16_hi(b[q][k]) + d[2 * k + 1])});
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(b[q][k]) + d[k]);
       }
-      store_out8(out + mr * p.ldo + c, v);
+      if (mt + row < t.hi && cok) *reinterpret_cast<u32x4*>(out + (int64_t)(mt + row) * p.ldo + bcol) = o;
     }
+    wave_lds_order();
+  };
+  for (int mt = t.lo; mt < t.hi; mt += 32) {
+    block(bb[0], bb[1], lf[0], lf[1], mt);
+    if (mt + 16 < t.hi) block(bb[1], bb[0], lf[1], lf[0], mt + 16);
   }
 }
 
+template <int KS, int NJ, typename T>
+static void launch_expand_k(const ExpandArgs& p, hipStream_t s) {
+  const dim3 grid(tile_grid(p.seg, 64), (p.C + 64 * NJ - 1) / (64 * NJ));
+  if (p.base) hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, false>), grid, dim3(256), 0, s, p);
+}
 template <typename T>
 static void launch_expand_t(const ExpandArgs& p, hipStream_t s) {
-  const unsigned gx = tile_grid(p.seg, 64);
-  if (p.R <= 32)
-    hipLaunchKernelGGL((lora_expand_kernel<1, 4, T>), dim3(gx, (p.C + 511) / 512), dim3(256), 0, s, p);
-  else if (p.R <= 64)
-    hipLaunchKernelGGL((lora_expand_kernel<2, 4, T>), dim3(gx, (p.C + 511) / 512), dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((lora_expand_kernel<4, 2, T>), dim3(gx, (p.C + 255) / 256), dim3(256), 0, s, p);
+  if (p.R <= 32) launch_expand_k<1, 8, T>(p, s);
+  else if (p.R <= 64) launch_expand_k<2, 8, T>(p, s);
+  else launch_expand_k<4, 4, T>(p, s);
 }
 static hipError_t launch_expand(const ExpandArgs& p, bool f32, hipStream_t s) {
   if (f32) launch_expand_t<float>(p, s);
@@ -484,7 +560,7 @@ template <int RG, bool CODES, bool UP>
 __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   typedef typename std::conditional<CODES, u32x2, u32x4>::type Row;
   __shared__ float red[2][RG * 8 * 256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int nrb = (p.R + 16 * RG - 1) / (16 * RG);
   const int a = blockIdx.y / nrb, r0 = blockIdx.y % nrb * 16 * RG;
