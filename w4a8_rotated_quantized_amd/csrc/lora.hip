@@ -174,18 +174,19 @@ CR_DEV void wait_vmcnt() {
 
 // A block takes TM x 16 rows of one segment and 16 RG ranks. Its NW waves
 // share the columns in stages of 64 and add their sums through LDS in a fixed
-// order. A stage goes straight from memory into the wave's own LDS ring of D
-// slots: one load moves 8 rows x 128 bytes, neighbouring lanes taking
+// order. A stage goes straight from memory into the wave's own LDS rings, DX
+// stages of x (from memory far away) and DW <= DX of the weights (from L2): one load moves 8 rows x 128 bytes, neighbouring lanes taking
 // neighbouring 16 bytes, so that every request is a whole line (the operand
 // order of the matrix cores, neighbouring lanes on different rows, reads the
 // same bytes from L2 2.6 times slower: 15.5 against 5.9 us for 256 x 512 KB).
 // Within a row's 128 bytes, chunk q lies at position q ^ (row % 8), which
 // spreads the fragment reads over the banks.
-template <int RG, int TM, int NW, int D>
+template <int RG, int TM, int NW, int DX, int DW>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
-  constexpr int NL = 2 * (TM + RG);                // loads (KB) of a stage
+  constexpr int NX = 2 * TM, NWT = 2 * RG;         // loads (KB) of a stage: of x, of the weights
   constexpr int RED = RG * TM * 64;                // 16-byte sums of a wave
-  constexpr int RING = D * NL * 1024 > RED * 16 ? D * NL * 1024 : RED * 16;
+  constexpr int KB = DX * NX + DW * NWT;
+  constexpr int RING = KB * 1024 > RED * 16 ? KB * 1024 : RED * 16;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * RING];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -199,59 +200,88 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
     return;
   }
   const int lr = lane >> 3, lc = 8 * ((lane & 7) ^ lr);   // row and column of the lane's 16 bytes in a load
-  const uint16_t* src[NL];
+  const uint16_t* xr[NX];
+  const uint16_t* wr[NWT];
 #pragma unroll
-  for (int n = 0; n < NL; ++n) {
-    if (n < 2 * TM) {
-      const int m = t.lo + 8 * n + lr;
-      src[n] = p.x + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldx;          // past the tile: computed for nothing
-    } else {
-      const int r = r0 + 8 * (n - 2 * TM) + lr;
-      src[n] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C;
-    }
+  for (int n = 0; n < NX; ++n) {
+    const int m = t.lo + 8 * n + lr;
+    xr[n] = p.x + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldx;             // past the tile: computed for nothing
   }
-  uint8_t* ring = lds + wave * RING;
-  auto load = [&](int s, int slot) {               // stage s of this wave
-    int c = (s * NW + wave) * 64 + lc;
-    c = c < p.C ? c : 0;                           // past the last column: loaded for nothing
 #pragma unroll
-    for (int n = 0; n < NL; ++n)
-      __builtin_amdgcn_global_load_lds((lora_gptr)(src[n] + c), (lora_lptr)(ring + (slot * NL + n) * 1024), 16, 0, 0);
+  for (int n = 0; n < NWT; ++n) {
+    const int r = r0 + 8 * n + lr;
+    wr[n] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C;
+  }
+  uint8_t* xring = lds + wave * RING;
+  uint8_t* wring = xring + DX * NX * 1024;
+  const int stages = ((p.C + 63) / 64 - wave + NW - 1) / NW;   // may be 0
+  // blocks start at different columns: rows a power of two apart share an L2 channel
+  // (rank 64, K = 4096: 21 against 29 us from the cache)
+  const int first = stages ? blockIdx.x % stages : 0;
+  auto column = [&](int s) { s += first; return ((s < stages ? s : s - stages) * NW + wave) * 64; };
+  auto lane_column = [&](int s) {
+    const int c = column(s) + lc;
+    return c < p.C ? c : 0;                        // past the last column: loaded for nothing
+  };
+  auto load_x = [&](int s, int slot) {
+    const int c = lane_column(s);
+#pragma unroll
+    for (int n = 0; n < NX; ++n)
+      __builtin_amdgcn_global_load_lds((lora_gptr)(xr[n] + c), (lora_lptr)(xring + (slot * NX + n) * 1024), 16, 0, 0);
+  };
+  auto load_w = [&](int s, int slot) {
+    const int c = lane_column(s);
+#pragma unroll
+    for (int n = 0; n < NWT; ++n)
+      __builtin_amdgcn_global_load_lds((lora_gptr)(wr[n] + c), (lora_lptr)(wring + (slot * NWT + n) * 1024), 16, 0, 0);
   };
   v4f acc[RG][TM];
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) acc[rg][tm] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int stages = ((p.C + 63) / 64 - wave + NW - 1) / NW;   // may be 0
+  // Issue order: x 0 .. DX - DW - 1, then for s = 0, 1, ...: w s, x s + DX - DW.
 #pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (d < stages) load(d, d);
-  int slot = 0;
+  for (int d = 0; d < DX; ++d) {
+    if (d >= DX - DW && d - (DX - DW) < stages) load_w(d - (DX - DW), d - (DX - DW));
+    if (d < stages) load_x(d, d);
+  }
+  int xs = 0, ws = 0;
 #pragma unroll 1
   for (int s = 0; s < stages; ++s) {
-    // in flight: stages s .. s + D - 1, fewer at the end
-    if (D > 1 && s + D - 1 < stages) wait_vmcnt<(D - 1) * NL>();
+    // Behind w s and x s in the queue: x s + DX - DW when x s is older than w s, and the
+    // DW - 1 pairs after it; fewer at the end, where everything is waited for.
+    constexpr int LATER = (DW - 1) * (NWT + NX) + (DX > DW ? NX : 0);
+    if (LATER > 0 && s + DX <= stages) wait_vmcnt<LATER>();
     else wait_vmcnt<0>();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    u32x4 f[NL / 2][2];                                // n = 2 j, 2 j + 1 hold the 16 rows of operand j
+    u32x4 xf[TM][2], wf[RG][2];
+    const int at = i * 128, sw = i & 7;            // 16 rows of an operand lie one after the other
 #pragma unroll
-    for (int j = 0; j < NL / 2; ++j)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        f[j][h] = *reinterpret_cast<const u32x4*>(ring + (slot * NL + 2 * j) * 1024 + i * 128 + (((4 * h + g) ^ (i & 7)) * 16));
-    __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): read before the slot is filled again
+      for (int tm = 0; tm < TM; ++tm)
+        xf[tm][h] = *reinterpret_cast<const u32x4*>(xring + (xs * NX + 2 * tm) * 1024 + at + ((4 * h + g) ^ sw) * 16);
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+        wf[rg][h] = *reinterpret_cast<const u32x4*>(wring + (ws * NWT + 2 * rg) * 1024 + at + ((4 * h + g) ^ sw) * 16);
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): read before the slots are filled again
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    if (s + D < stages) load(s + D, slot);
-    slot = slot + 1 == D ? 0 : slot + 1;
-    const int c0 = (s * NW + wave) * 64;
+    if (s + DW < stages) load_w(s + DW, ws);
+    if (s + DX < stages) load_x(s + DX, xs);
+    xs = xs + 1 == DX ? 0 : xs + 1;
+    ws = ws + 1 == DW ? 0 : ws + 1;
+    const int c0 = column(s);
     if (c0 + 64 > p.C) {                           // the last columns: zeros past C (C % 8 == 0)
       const u32x4 z = {0, 0, 0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const bool ok = c0 + 32 * h + 8 * g < p.C;
 #pragma unroll
-        for (int j = 0; j < NL / 2; ++j) f[j][h] = ok ? f[j][h] : z;
+        for (int tm = 0; tm < TM; ++tm) xf[tm][h] = ok ? xf[tm][h] : z;
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) wf[rg][h] = ok ? wf[rg][h] : z;
       }
     }
 #pragma unroll
@@ -260,7 +290,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
       for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
-          acc[rg][tm] = mfma16(__builtin_bit_cast(v8bf, f[TM + rg][h]), __builtin_bit_cast(v8bf, f[tm][h]), acc[rg][tm]);
+          acc[rg][tm] = mfma16(__builtin_bit_cast(v8bf, wf[rg][h]), __builtin_bit_cast(v8bf, xf[tm][h]), acc[rg][tm]);
   }
   __syncthreads();                                 // the rings are done with: their memory takes the sums
   v4f* red = reinterpret_cast<v4f*>(lds);
@@ -287,13 +317,13 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
 static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
   const int rg = (p.R + 15) / 16;
   if (p.seg.M <= 256) {
-    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 2>), dim3(tile_grid(p.seg, 16), rg), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 2, 2>), dim3(tile_grid(p.seg, 16), rg), dim3(1024), 0, s, p);
   } else if (rg <= 1) {
-    hipLaunchKernelGGL((lora_shrink_kernel<1, 2, 6, 2>), dim3(tile_grid(p.seg, 32)), dim3(384), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 8, 3, 2>), dim3(tile_grid(p.seg, 16)), dim3(512), 0, s, p);
   } else if (rg <= 2) {
-    hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 4, 2>), dim3(tile_grid(p.seg, 32)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 5, 2, 2>), dim3(tile_grid(p.seg, 32)), dim3(320), 0, s, p);
   } else {
-    hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 6, 1>), dim3(tile_grid(p.seg, 32), (rg + 3) / 4), dim3(384), 0, s, p);
+    hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 6, 1, 1>), dim3(tile_grid(p.seg, 32), (rg + 3) / 4), dim3(384), 0, s, p);
   }
   return hipGetLastError();
 }
