@@ -126,20 +126,23 @@ CR_DEV Split split3(float f) {
 // bf16 pair from the upper halves of two words
 CR_DEV uint32_t upper_pair(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
 
-struct Frag3 {
-  v8bf hi, mid, lo;
-};
-CR_DEV Frag3 split_frag(const float (&v)[8]) {
-  u32x4 h, m, l;
+// eight values as three operand fragments: hi, mid, lo
+CR_DEV void split8(const float (&v)[8], u32x4 (&f)[3]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const Split a = split3(v[2 * i]), b = split3(v[2 * i + 1]);
-    h[i] = upper_pair(a.hi, b.hi);
-    m[i] = upper_pair(a.mid, b.mid);
-    l[i] = upper_pair(a.lo, b.lo);
+    f[0][i] = upper_pair(a.hi, b.hi);
+    f[1][i] = upper_pair(a.mid, b.mid);
+    f[2][i] = upper_pair(a.lo, b.lo);
   }
-  return Frag3{__builtin_bit_cast(v8bf, h), __builtin_bit_cast(v8bf, m), __builtin_bit_cast(v8bf, l)};
 }
+
+// A float32 [M][R] matrix in the operand order of "outer", whose products run
+// over rows: [3 terms][ceil(M / 8)][R][8 rows] of bf16.
+CR_DEV int64_t rows8_index(int M, int R, int term, int m, int r) {
+  return (((int64_t)term * ((M + 7) / 8) + m / 8) * R + r) * 8 + m % 8;
+}
+static size_t rows8_bytes(int64_t M, int R) { return (size_t)(3 * ((M + 7) / 8) * 8 * R) * 2; }
 
 // Between LDS accesses of one wave to what its other lanes wrote or will
 // write: the hardware keeps their order, the compiler has to as well.
@@ -158,7 +161,10 @@ struct ShrinkArgs {
   const uint16_t* w;     // [A][R][C]
   LoraSegments seg;
   const float* scale;    // multiplies the result, or null
-  float* la;
+  float* la;             // [M][R]
+  uint16_t* rows8;       // the result (times row_scales) once more, for "outer", or null
+  const float* row_scales;   // [M] or [1] (row_scaled 0), or null
+  int row_scaled;
   int R, C;
 };
 
@@ -311,6 +317,16 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] *= cs;
     *reinterpret_cast<v4f*>(p.la + (int64_t)m * p.R + r) = s;
+    if (p.rows8) {
+      const float rs = p.row_scales ? p.row_scales[p.row_scaled ? m : 0] : 1.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const Split q = split3(s[e] * rs);
+        p.rows8[rows8_index(p.seg.M, p.R, 0, m, r + e)] = (uint16_t)(q.hi >> 16);
+        p.rows8[rows8_index(p.seg.M, p.R, 1, m, r + e)] = (uint16_t)(q.mid >> 16);
+        p.rows8[rows8_index(p.seg.M, p.R, 2, m, r + e)] = (uint16_t)(q.lo >> 16);
+      }
+    }
   }
 }
 
@@ -375,23 +391,24 @@ CR_DEV void store_out8(T* p, const float (&v)[8]) {
   }
 }
 
-// A wave holds the weights of 16 NJ columns as operand fragments and walks the
-// rows of its tile, 16 at a time. The sums of a 16 x 16 NJ block go through LDS,
-// so that base and out move as whole runs of columns, and the next block's base
-// and lora_act are on their way during the products.
-template <int KS, int NJ, typename T, bool BASE>
+// A block takes SUB x 64 rows of one segment and 64 NJ columns, a wave 16 NJ of
+// them, whose weights it holds as operand fragments. 64 rows of lora_act are
+// split once for the whole block. The sums of a 16 x 16 NJ block go through
+// LDS, so that base and out move as whole runs of columns, and the next block's
+// base is on its way during the products.
+template <int KS, int NJ, typename T, bool BASE, int SUB>
 __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
-  constexpr int TILE = 64, W = 16 * NJ;
+  constexpr int W = 16 * NJ, RO = 4 * KS;         // columns of a wave; rank octets
   constexpr int V = 16 / sizeof(T);               // columns of one 16-byte access
   constexpr int CPR = W / V;                      // accesses per row
   constexpr int NB = 16 * CPR / 64;               // accesses per lane and block
-  __shared__ float lds[4][16][W + 4];
+  __shared__ float sums[4][16][W + 4];
+  __shared__ u32x4 la3[3][RO][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const RowTile t = find_tile<TILE>(p.seg, blockIdx.x);
+  const RowTile t = find_tile<64 * SUB>(p.seg, blockIdx.x);
   if (t.lo >= t.hi) return;
   const int c0 = (blockIdx.y * 4 + wave) * W;
-  if (c0 >= p.C) return;                          // no barrier below: every wave works for itself
   const T* base = static_cast<const T*>(p.base);
   T* out = static_cast<T*>(p.out);
   const int brow = lane / CPR, bcol = c0 + lane % CPR * V;   // access q: row brow + q * 64 / CPR, columns bcol ..
@@ -423,16 +440,6 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
 #pragma unroll
   for (int q = 0; q < NB; ++q) bb[0][q] = bb[1][q] = u32x4{0, 0, 0, 0};
   if constexpr (BASE) load_base(bb[0], t.lo);
-  float lf[2][KS][8];
-  auto load_la = [&](float (&l)[KS][8], int mt) {
-    const int64_t m = mt + i < t.hi ? mt + i : t.hi - 1;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int r = 32 * ks + 8 * g;
-      load_out8(p.la + m * p.R + (r < p.R ? r : 0), l[ks]);
-    }
-  };
-  load_la(lf[0], t.lo);
   const float cs = p.scale ? p.scale[t.a] : 1.f;
   v8bf wf[NJ][KS];
 #pragma unroll
@@ -446,35 +453,28 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
       wf[j][ks] = __builtin_bit_cast(v8bf, r < p.R ? v : z);
     }
   }
-  auto block = [&](u32x4 (&b)[NB], u32x4 (&bn)[NB], float (&l)[KS][8], float (&ln)[KS][8], int mt) {
+  auto block = [&](u32x4 (&b)[NB], u32x4 (&bn)[NB], int mt, int row0) {
     // behind the tile: its last row once more, for nothing
     if constexpr (BASE) load_base(bn, mt + 16);
-    load_la(ln, mt + 16);
     v4f acc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      float v[8];
-      const bool ok = 32 * ks + 8 * g < p.R;
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = ok ? l[ks][e] * cs : 0.f;
-      const Frag3 f = split_frag(v);
+      for (int term = 2; term >= 0; --term) {     // the small terms first
+        const v8bf f = __builtin_bit_cast(v8bf, la3[term][4 * ks + g][row0 + i]);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[j] = mfma16(wf[j][ks], f.lo, acc[j]);
+        for (int j = 0; j < NJ; ++j) acc[j] = mfma16(wf[j][ks], f, acc[j]);
+      }
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[j] = mfma16(wf[j][ks], f.mid, acc[j]);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[j] = mfma16(wf[j][ks], f.hi, acc[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) *reinterpret_cast<v4f*>(&lds[wave][i][16 * j + 4 * g]) = acc[j];
+    for (int j = 0; j < NJ; ++j) *reinterpret_cast<v4f*>(&sums[wave][i][16 * j + 4 * g]) = acc[j];
     wave_lds_order();
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
       const int row = brow + q * (64 / CPR);
       float d[V];
-      const float* src = &lds[wave][row][lane % CPR * V];
+      const float* src = &sums[wave][row][lane % CPR * V];
 #pragma unroll
       for (int e = 0; e < V; e += 4) {
         const v4f x = *reinterpret_cast<const v4f*>(src + e);
@@ -495,17 +495,41 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
     }
     wave_lds_order();
   };
-  for (int mt = t.lo; mt < t.hi; mt += 32) {
-    block(bb[0], bb[1], lf[0], lf[1], mt);
-    if (mt + 16 < t.hi) block(bb[1], bb[0], lf[1], lf[0], mt + 16);
+  for (int st = t.lo; st < t.hi; st += 64) {
+    if (SUB > 1 && st != t.lo) __syncthreads();   // the last 64 rows' terms have been read
+#pragma unroll
+    for (int k = threadIdx.x; k < 64 * RO; k += 256) {
+      const int ro = k % RO, row = k / RO;
+      const int64_t m = st + row < t.hi ? st + row : t.hi - 1;
+      float v[8];
+      load_out8(p.la + m * p.R + (8 * ro < p.R ? 8 * ro : 0), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 8 * ro < p.R ? v[e] * cs : 0.f;
+      u32x4 f[3];
+      split8(v, f);
+#pragma unroll
+      for (int term = 0; term < 3; ++term) la3[term][ro][row] = f[term];
+    }
+    __syncthreads();
+    const int end = st + 64 < t.hi ? st + 64 : t.hi;
+    for (int mt = st; mt < end; mt += 32) {
+      block(bb[0], bb[1], mt, mt - st);
+      if (mt + 16 < end) block(bb[1], bb[0], mt + 16, mt + 16 - st);
+    }
   }
 }
 
+template <int KS, int NJ, typename T, int SUB>
+static void launch_expand_s(const ExpandArgs& p, hipStream_t s) {
+  const dim3 grid(tile_grid(p.seg, 64 * SUB), (p.C + 64 * NJ - 1) / (64 * NJ));
+  if (p.base) hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, true, SUB>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, false, SUB>), grid, dim3(256), 0, s, p);
+}
 template <int KS, int NJ, typename T>
 static void launch_expand_k(const ExpandArgs& p, hipStream_t s) {
-  const dim3 grid(tile_grid(p.seg, 64), (p.C + 64 * NJ - 1) / (64 * NJ));
-  if (p.base) hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, true>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, false>), grid, dim3(256), 0, s, p);
+  // tall tiles read the weights less often, while there are enough of them for 256 compute units
+  if ((int64_t)(p.seg.M / 256) * ((p.C + 64 * NJ - 1) / (64 * NJ)) >= 512) launch_expand_s<KS, NJ, T, 4>(p, s);
+  else launch_expand_s<KS, NJ, T, 1>(p, s);
 }
 template <typename T>
 static void launch_expand_t(const ExpandArgs& p, hipStream_t s) {
@@ -520,26 +544,86 @@ static hipError_t launch_expand(const ExpandArgs& p, bool f32, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// weights [A][rows][cols] -> [A][cols][rows] (the backward pass contracts over
-// the other index): 64 x 64 tiles through LDS
+// prepare: what the backward pass reads in another order, in one launch: up
+// [A][N][R] -> [A][R][N] and down [A][R][K] -> [A][K][R] (it contracts over the
+// other index of each), and lora_act in the row-octet order of "outer"
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* in, uint16_t* out, int rows, int cols) {
-  __shared__ uint16_t tile[64][66];
-  const int64_t at = (int64_t)blockIdx.z * rows * cols;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  for (int k = threadIdx.x; k < 64 * 64; k += 256) {
-    const int r = r0 + k / 64, c = c0 + k % 64;
-    if (r < rows && c < cols) tile[k / 64][k % 64] = in[at + (int64_t)r * cols + c];
+struct PrepareArgs {
+  const uint16_t* up;      // null: not wanted; so down and la
+  uint16_t* up_t;
+  const uint16_t* down;
+  uint16_t* down_t;
+  const float* la;
+  uint16_t* la8;
+  int M, N, K, R, A;
+  int up_blocks, down_blocks;
+};
+
+// rows x cols (at most 64 x 128 or 128 x 64, multiples of 8) of `in` transposed into `out`
+CR_DEV void transpose_tile(const uint16_t* in, int64_t ldi, uint16_t* out, int64_t ldo, int rows, int cols,
+                           uint16_t* lds) {
+  const int pitch = cols + 2;                      // an odd number of words: columns spread over the banks
+  const int c8 = cols / 8, r8 = rows / 8;
+  for (int k = threadIdx.x; k < rows * c8; k += 256) {
+    const int r = k / c8, c = k % c8 * 8;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(in + r * ldi + c);
+    uint32_t* d = reinterpret_cast<uint32_t*>(lds + r * pitch + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = v[e];
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < 64 * 64; k += 256) {
-    const int c = c0 + k / 64, r = r0 + k % 64;
-    if (r < rows && c < cols) out[at + (int64_t)c * rows + r] = tile[k % 64][k / 64];
+  for (int k = threadIdx.x; k < cols * r8; k += 256) {
+    const int c = k / r8, r = k % r8 * 8;
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = (uint32_t)lds[(r + 2 * e) * pitch + c] | ((uint32_t)lds[(r + 2 * e + 1) * pitch + c] << 16);
+    *reinterpret_cast<u32x4*>(out + c * ldo + r) = v;
   }
 }
-static hipError_t launch_transpose(const uint16_t* in, uint16_t* out, int A, int rows, int cols, hipStream_t s) {
-  hipLaunchKernelGGL(lora_transpose_kernel, dim3((cols + 63) / 64, (rows + 63) / 64, A), dim3(256), 0, s, in, out, rows,
-                     cols);
+
+__global__ __launch_bounds__(256) void lora_prepare_kernel(PrepareArgs p) {
+  __shared__ uint16_t lds[128 * 66 > 64 * 130 ? 128 * 66 : 64 * 130];
+  int b = blockIdx.x;
+  if (b < p.up_blocks) {                           // 64 channels and all ranks of one adapter
+    const int per = (p.N + 63) / 64;
+    const int a = b / per, n0 = b % per * 64;
+    const int n = p.N - n0 < 64 ? p.N - n0 : 64;
+    transpose_tile(p.up + ((int64_t)a * p.N + n0) * p.R, p.R, p.up_t + (int64_t)a * p.R * p.N + n0, p.N, n, p.R, lds);
+    return;
+  }
+  b -= p.up_blocks;
+  if (b < p.down_blocks) {
+    const int per = (p.K + 63) / 64;
+    const int a = b / per, k0 = b % per * 64;
+    const int n = p.K - k0 < 64 ? p.K - k0 : 64;
+    transpose_tile(p.down + (int64_t)a * p.R * p.K + k0, p.K, p.down_t + ((int64_t)a * p.K + k0) * p.R, p.R, p.R, n, lds);
+    return;
+  }
+  b -= p.down_blocks;
+  const int64_t k = (int64_t)b * 256 + threadIdx.x;   // one octet of rows and one rank
+  const int64_t m8 = k / p.R;
+  const int r = (int)(k % p.R);
+  if (m8 * 8 >= p.M) return;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t m = m8 * 8 + e;
+    const float x = p.la[(m < p.M ? m : p.M - 1) * p.R + r];
+    v[e] = m < p.M ? x : 0.f;
+  }
+  u32x4 f[3];
+  split8(v, f);
+#pragma unroll
+  for (int term = 0; term < 3; ++term)
+    *reinterpret_cast<u32x4*>(p.la8 + rows8_index(p.M, p.R, term, (int)(m8 * 8), r)) = f[term];
+}
+
+static hipError_t launch_prepare(PrepareArgs p, hipStream_t s) {
+  p.up_blocks = p.up ? p.A * ((p.N + 63) / 64) : 0;
+  p.down_blocks = p.down ? p.A * ((p.K + 63) / 64) : 0;
+  const int64_t la_blocks = p.la ? ((int64_t)((p.M + 7) / 8) * p.R + 255) / 256 : 0;
+  hipLaunchKernelGGL(lora_prepare_kernel, dim3((unsigned)(p.up_blocks + p.down_blocks + la_blocks)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -547,18 +631,17 @@ static hipError_t launch_transpose(const uint16_t* in, uint16_t* out, int A, int
 // outer: G[a][r][c] = (c_a) sum over the rows of adapter a of u[m, r] v[m, c]
 // ---------------------------------------------------------------------------
 struct OuterArgs {
-  const float* u;         // [M][R]
+  const uint16_t* u8;     // u in row-octet order (see rows8_index)
   const void* v;          // bf16 or int8 [M][ldv]
   int64_t ldv;
-  const float* v_scales;  // int8: multiplies u[m, :] by v_scales[m] (or [0])
-  int v_row_scales;
   LoraSegments seg;
   const float* scale;     // multiplies the result, or null
-  float* out;             // [A][R][C], or [A][C][R] when `up`; partial p at out + p * part
+  float* out;             // [A][R][C], or [A][C][R] for up; part q at out + q * part
   int64_t part;
   int P;                  // parts that the rows of an adapter are split into
   int accumulate;         // add to what out holds (P == 1)
   int R, C;
+  int blocks;             // of this product in the launch; 0: not wanted
 };
 
 // Transposed fragments of an 8 x 8 block: row e of the lane's block holds
@@ -583,19 +666,31 @@ CR_DEV v8bf column_frag(const u32x2 (&row)[8], int j) {   // int8 codes, exact i
   return __builtin_bit_cast(v8bf, f);
 }
 
-// A block takes 128 columns, 16 RG ranks and part blockIdx.z of an adapter's
-// rows; its four waves take 32-row steps in turn and add their sums through
-// LDS in a fixed order. Lane i of a 16-lane group holds columns 8 i .. 8 i + 7.
+// A block takes 128 columns, 16 RG ranks and one part of an adapter's rows;
+// its four waves take steps of 32 rows in turn and add their sums through LDS in
+// a fixed order. Lane i of a 16-lane group holds columns 8 i .. 8 i + 7. The next
+// step's v is on its way during the products.
 template <int RG, bool CODES, bool UP>
-__global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
+CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
   typedef typename std::conditional<CODES, u32x2, u32x4>::type Row;
-  __shared__ float red[2][RG * 8 * 256];
+  typedef typename std::conditional<CODES, int8_t, uint16_t>::type Elem;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int nrb = (p.R + 16 * RG - 1) / (16 * RG);
-  const int a = blockIdx.y / nrb, r0 = blockIdx.y % nrb * 16 * RG;
-  const int c = blockIdx.x * 128 + 8 * i;
+  const int ct = (p.C + 127) / 128, nrb = (p.R + 16 * RG - 1) / (16 * RG);
+  const int c = b % ct * 128 + 8 * i;
+  b /= ct;
+  const int r0 = b % nrb * 16 * RG;
+  b /= nrb;
+  const int a = b % p.seg.A, part = b / p.seg.A;
   const bool cok = c < p.C;
+  const Elem* vcol = static_cast<const Elem*>(p.v) + (cok ? c : 0);
+  const uint16_t* ucol[RG];
+#pragma unroll
+  for (int rg = 0; rg < RG; ++rg) {
+    const int r = r0 + 16 * rg + i;
+    ucol[rg] = p.u8 + (r < p.R ? r : p.R - 1) * 8;
+  }
+  const int64_t term = (int64_t)((p.seg.M + 7) / 8) * p.R * 8;
   v4f acc[RG][8];
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg)
@@ -607,24 +702,62 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
     int64_t n = 0;
     for (int s = lane; s < p.seg.S; s += 64) {
       const int lo = seg_bound(p.seg, s + 1), hi = seg_bound(p.seg, s + 2);
-      if (hi > lo && seg_adapter(p.seg, s + 1) == a && s < p.seg.S) n += hi - lo;
+      if (hi > lo && seg_adapter(p.seg, s + 1) == a) n += hi - lo;
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
-    from = n * blockIdx.z / p.P;
-    to = n * (blockIdx.z + 1) / p.P;
+    from = n * part / p.P;
+    to = n * (part + 1) / p.P;
   }
-  int step = 0;
+
+  // rows [mlo, mhi) in steps of 32 that start at multiples of 32; rows of a step
+  // outside them count as zeros, whatever they hold
+  auto load_v = [&](Row (&row)[8], int m0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int m = m0 + 8 * g + e;
+      row[e] = *reinterpret_cast<const Row*>(vcol + (int64_t)(m < p.seg.M ? m : p.seg.M - 1) * p.ldv);
+    }
+  };
+  auto products = [&](Row (&row)[8], int m0, int mlo, int mhi) {
+    u32x4 uf[RG][3];
+    const int m8 = (m0 >> 3) + g < (p.seg.M + 7) / 8 ? (m0 >> 3) + g : 0;
+#pragma unroll
+    for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        uf[rg][q] = *reinterpret_cast<const u32x4*>(ucol[rg] + q * term + (int64_t)m8 * p.R * 8);
+    if (m0 < mlo || m0 + 32 > mhi) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int m = m0 + 8 * g + 2 * k;
+        const bool ok0 = m >= mlo && m < mhi, ok1 = m + 1 >= mlo && m + 1 < mhi;
+        const uint32_t keep = (ok0 ? 0xFFFFu : 0u) | (ok1 ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+          for (int q = 0; q < 3; ++q) uf[rg][q][k] &= keep;
+        const Row z{};
+        row[2 * k] = ok0 ? row[2 * k] : z;
+        row[2 * k + 1] = ok1 ? row[2 * k + 1] : z;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const v8bf vf = column_frag(row, j);
+#pragma unroll
+      for (int q = 2; q >= 0; --q)                 // the small terms first
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) acc[rg][j] = mfma16(__builtin_bit_cast(v8bf, uf[rg][q]), vf, acc[rg][j]);
+    }
+  };
+  Row va[8], vb[8];
+  int turn = 0;                                    // steps so far, over all segments
   int64_t before = 0;
   for (int s0 = 0; s0 < p.seg.S; s0 += 64) {
     const int s = s0 + lane;
-    int lo = 0, len = 0;
-    if (s < p.seg.S && seg_adapter(p.seg, s + 1) == a) {
-      lo = seg_bound(p.seg, s + 1);
-      // the last segment ends at off[S], not at M
-      const int hi = seg_bound(p.seg, s + 2);
-      len = hi > lo ? hi - lo : 0;
-    }
+    const int lo = seg_bound(p.seg, s + 1), hi = seg_bound(p.seg, s + 2);
+    const int len = s < p.seg.S && hi > lo && seg_adapter(p.seg, s + 1) == a ? hi - lo : 0;
     for (uint64_t left = __ballot(len > 0); left; left &= left - 1) {
       const int src = __builtin_ctzll(left);
       const int slo = __builtin_amdgcn_readlane(lo, src), slen = __builtin_amdgcn_readlane(len, src);
@@ -633,40 +766,18 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
       before += slen;
       if (x1 <= x0) continue;
       const int mlo = slo + (int)x0, mhi = slo + (int)x1;
-      for (int m0 = mlo; m0 < mhi; m0 += 32, ++step) {
-        if ((step & 3) != wave) continue;
-        Row row[8];
-        Frag3 uf[RG];
-        float uv[RG][8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int m = m0 + 8 * g + e;
-          const bool ok = m < mhi;
-          const int64_t mr = ok ? m : mhi - 1;
-          Row z{};
-          if constexpr (CODES) row[e] = ok && cok ? *reinterpret_cast<const Row*>(static_cast<const int8_t*>(p.v) + mr * p.ldv + c) : z;
-          else row[e] = ok && cok ? *reinterpret_cast<const Row*>(static_cast<const uint16_t*>(p.v) + mr * p.ldv + c) : z;
-          float vs = 1.f;
-          if constexpr (CODES) vs = p.v_scales[p.v_row_scales ? mr : 0];
-#pragma unroll
-          for (int rg = 0; rg < RG; ++rg) {
-            const int r = r0 + 16 * rg + i;
-            const float f = p.u[mr * p.R + (r < p.R ? r : p.R - 1)];
-            uv[rg][e] = ok ? f * vs : 0.f;
-          }
-        }
-#pragma unroll
-        for (int rg = 0; rg < RG; ++rg) uf[rg] = split_frag(uv[rg]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const v8bf vf = column_frag(row, j);
-#pragma unroll
-          for (int rg = 0; rg < RG; ++rg) {
-            acc[rg][j] = mfma16(uf[rg].lo, vf, acc[rg][j]);
-            acc[rg][j] = mfma16(uf[rg].mid, vf, acc[rg][j]);
-            acc[rg][j] = mfma16(uf[rg].hi, vf, acc[rg][j]);
-          }
-        }
+      const int m00 = mlo & ~31, count = (mhi - m00 + 31) >> 5;
+      int k = (wave - turn) & 3;                   // this wave's steps: k, k + 4, ...
+      turn += count;
+      if (k >= count) continue;
+      load_v(va, m00 + 32 * k);
+      for (; k < count; k += 8) {
+        // past the last step: any rows of the batch, for nothing
+        load_v(vb, m00 + 32 * (k + 4 < count ? k + 4 : k));
+        products(va, m00 + 32 * k, mlo, mhi);
+        if (k + 4 >= count) break;
+        load_v(va, m00 + 32 * (k + 8 < count ? k + 8 : k));
+        products(vb, m00 + 32 * (k + 4), mlo, mhi);
       }
     }
   }
@@ -676,7 +787,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
 #pragma unroll
       for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) *reinterpret_cast<v4f*>(&red[wave - n][((rg * 8 + j) * 64 + lane) * 4]) = acc[rg][j];
+        for (int j = 0; j < 8; ++j) red[wave - n][(rg * 8 + j) * 64 + lane] = acc[rg][j];
     }
     __syncthreads();
     if (wave < n) {
@@ -684,7 +795,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
       for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const v4f o = *reinterpret_cast<const v4f*>(&red[wave][((rg * 8 + j) * 64 + lane) * 4]);
+          const v4f o = red[wave][(rg * 8 + j) * 64 + lane];
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[rg][j][e] += o[e];
         }
@@ -693,7 +804,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   }
   if (wave != 0 || !cok) return;
   const float cs = p.scale ? p.scale[a] : 1.f;
-  float* out = p.out + blockIdx.z * p.part + (int64_t)a * p.R * p.C;
+  float* out = p.out + part * p.part + (int64_t)a * p.R * p.C;
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg) {
     const int r = r0 + 16 * rg + 4 * g;
@@ -723,23 +834,34 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   }
 }
 
-template <bool CODES, bool UP>
-static hipError_t launch_outer(const OuterArgs& p, hipStream_t s) {
-  const int ct = (p.C + 127) / 128;
-  if (p.R <= 16)
-    hipLaunchKernelGGL((lora_outer_kernel<1, CODES, UP>), dim3(ct, p.seg.A, p.P), dim3(256), 0, s, p);
-  else if (p.R <= 32)
-    hipLaunchKernelGGL((lora_outer_kernel<2, CODES, UP>), dim3(ct, p.seg.A, p.P), dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((lora_outer_kernel<4, CODES, UP>), dim3(ct, p.seg.A * ((p.R + 63) / 64), p.P), dim3(256), 0, s, p);
+// both weight gradients in one launch: the first up.blocks blocks make d_up
+template <int RG, bool CODES>
+__global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs up, OuterArgs down) {
+  __shared__ v4f red[2][RG * 8 * 64];
+  const int b = blockIdx.x;
+  if (b < up.blocks) outer_block<RG, false, true>(up, b, red);
+  else outer_block<RG, CODES, false>(down, b - up.blocks, red);
+}
+
+static int outer_blocks(const OuterArgs& p) {
+  const int rb = p.R <= 16 ? 16 : (p.R <= 32 ? 32 : 64);
+  return (p.C + 127) / 128 * ((p.R + rb - 1) / rb) * p.seg.A * p.P;
+}
+template <bool CODES>
+static hipError_t launch_outer(const OuterArgs& up, const OuterArgs& down, hipStream_t s) {
+  const dim3 grid(up.blocks + down.blocks);
+  const int R = up.blocks ? up.R : down.R;
+  if (R <= 16) hipLaunchKernelGGL((lora_outer_kernel<1, CODES>), grid, dim3(256), 0, s, up, down);
+  else if (R <= 32) hipLaunchKernelGGL((lora_outer_kernel<2, CODES>), grid, dim3(256), 0, s, up, down);
+  else hipLaunchKernelGGL((lora_outer_kernel<4, CODES>), grid, dim3(256), 0, s, up, down);
   return hipGetLastError();
 }
 
-// Parts an adapter's rows are split into: enough blocks for the GPU's 256
-// compute units, at least 128 rows each were the rows even.
-static int outer_parts(int64_t M, int64_t C, int A) {
-  const int64_t blocks = ((C + 127) / 128) * A;
-  int64_t P = (512 + blocks - 1) / blocks;
+// Parts an adapter's rows are split into: enough blocks for two on each of the
+// GPU's 256 compute units, at least 128 rows each were the rows even.
+static int outer_parts(int64_t M, int64_t C, int R, int A) {
+  const int64_t blocks = ((C + 127) / 128) * ((R + 63) / 64) * A;
+  int64_t P = 512 / blocks;
   const int64_t most = (M + 127) / 128;
   if (P > most) P = most;
   return P < 1 ? 1 : (int)P;
@@ -748,17 +870,26 @@ static int outer_parts(int64_t M, int64_t C, int A) {
 // ---------------------------------------------------------------------------
 // join: out = (out +) sum of the P parts, in order
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void lora_join_kernel(const float* part, int P, int64_t n, float* out, int accumulate) {
-  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (k >= n) return;
-  v4f s = *reinterpret_cast<const v4f*>(part + k);
-  for (int q = 1; q < P; ++q) {
-    const v4f o = *reinterpret_cast<const v4f*>(part + q * n + k);
+struct JoinArgs {
+  const float* part;
+  int P;
+  int64_t n;              // values of one part
+  float* out;
+  int accumulate;
+  int blocks;             // of this join in the launch; 0: not wanted
+};
+
+CR_DEV void join_block(const JoinArgs& p, int b) {
+  const int64_t k = ((int64_t)b * 256 + threadIdx.x) * 4;
+  if (k >= p.n) return;
+  v4f s = *reinterpret_cast<const v4f*>(p.part + k);
+  for (int q = 1; q < p.P; ++q) {
+    const v4f o = *reinterpret_cast<const v4f*>(p.part + q * p.n + k);
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] += o[e];
   }
-  v4f* o = reinterpret_cast<v4f*>(out + k);
-  if (accumulate) {
+  v4f* o = reinterpret_cast<v4f*>(p.out + k);
+  if (p.accumulate) {
     const v4f b = *o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] += b[e];
@@ -770,23 +901,22 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float* part, int P
 // lanes hold one row's 256 (NR = 1024: 4 x 256) columns, element 16 gL + e of
 // each chunk in register e of its lane.
 template <int NR>
-__global__ __launch_bounds__(256) void lora_join_rotate_kernel(const float* part, int P, int64_t n, float* out,
-                                                               int accumulate) {
+CR_DEV void join_rotate_block(const JoinArgs& p, int b) {
   constexpr int GPS = NR == 1024 ? 4 : 1;
   const LaneRot lr = lane_rot<NR>(threadIdx.x & 15);
-  const int64_t items = n / (256 * GPS);           // rows are whole groups: chunks follow one another
-  const int64_t item = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t items = p.n / (256 * GPS);           // rows are whole groups: chunks follow one another
+  const int64_t item = (int64_t)b * 16 + (threadIdx.x >> 4);
   const bool ok = item < items;
   const int64_t k0 = (ok ? item : items - 1) * (256 * GPS) + 16 * lr.gL;
   float v[GPS][16];
 #pragma unroll
   for (int g = 0; g < GPS; ++g) {
-    const float* src = part + k0 + 256 * g;
+    const float* src = p.part + k0 + 256 * g;
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       v4f s = *reinterpret_cast<const v4f*>(src + e);
-      for (int q = 1; q < P; ++q) {
-        const v4f o = *reinterpret_cast<const v4f*>(src + q * n + e);
+      for (int q = 1; q < p.P; ++q) {
+        const v4f o = *reinterpret_cast<const v4f*>(src + q * p.n + e);
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[x] += o[x];
       }
@@ -803,7 +933,7 @@ __global__ __launch_bounds__(256) void lora_join_rotate_kernel(const float* part
   if (!ok) return;
 #pragma unroll
   for (int g = 0; g < GPS; ++g) {
-    float* dst = out + k0 + 256 * g;
+    float* dst = p.out + k0 + 256 * g;
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       v4f s;
@@ -813,7 +943,7 @@ __global__ __launch_bounds__(256) void lora_join_rotate_kernel(const float* part
         s[x] = (neg ? -v[g][e + x] : v[g][e + x]) * RotSize<NR>::inv_sqrt;
       }
       v4f* o = reinterpret_cast<v4f*>(dst + e);
-      if (accumulate) {
+      if (p.accumulate) {
         const v4f b = *o;
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[x] += b[x];
@@ -823,14 +953,27 @@ __global__ __launch_bounds__(256) void lora_join_rotate_kernel(const float* part
   }
 }
 
-static hipError_t launch_join(const float* part, int P, int64_t n, float* out, int accumulate, int rot, hipStream_t s) {
-  const dim3 rgrid((unsigned)((n / (rot == 1024 ? 1024 : 256) + 15) / 16));
+// both gradients in one launch, d_up's blocks first; NR: the rotation of
+// d_down's columns that is undone (0: none)
+template <int NR>
+__global__ __launch_bounds__(256) void lora_join_kernel(JoinArgs up, JoinArgs down) {
+  const int b = blockIdx.x;
+  if (b < up.blocks) join_block(up, b);
+  else if constexpr (NR == 0) join_block(down, b - up.blocks);
+  else join_rotate_block<NR>(down, b - up.blocks);
+}
+
+static int join_blocks(const JoinArgs& p, int rot) {
+  return rot == 0 ? (int)((p.n / 4 + 255) / 256) : (int)((p.n / (rot == 1024 ? 1024 : 256) + 15) / 16);
+}
+static hipError_t launch_join(const JoinArgs& up, const JoinArgs& down, int rot, hipStream_t s) {
+  const dim3 grid(up.blocks + down.blocks);
   switch (rot) {
-    case 0: hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, part, P, n, out, accumulate); break;
-    case 16: hipLaunchKernelGGL((lora_join_rotate_kernel<16>), rgrid, dim3(256), 0, s, part, P, n, out, accumulate); break;
-    case 64: hipLaunchKernelGGL((lora_join_rotate_kernel<64>), rgrid, dim3(256), 0, s, part, P, n, out, accumulate); break;
-    case 1024: hipLaunchKernelGGL((lora_join_rotate_kernel<1024>), rgrid, dim3(256), 0, s, part, P, n, out, accumulate); break;
-    default: hipLaunchKernelGGL((lora_join_rotate_kernel<256>), rgrid, dim3(256), 0, s, part, P, n, out, accumulate); break;
+    case 0: hipLaunchKernelGGL((lora_join_kernel<0>), grid, dim3(256), 0, s, up, down); break;
+    case 16: hipLaunchKernelGGL((lora_join_kernel<16>), grid, dim3(256), 0, s, up, down); break;
+    case 64: hipLaunchKernelGGL((lora_join_kernel<64>), grid, dim3(256), 0, s, up, down); break;
+    case 1024: hipLaunchKernelGGL((lora_join_kernel<1024>), grid, dim3(256), 0, s, up, down); break;
+    default: hipLaunchKernelGGL((lora_join_kernel<256>), grid, dim3(256), 0, s, up, down); break;
   }
   return hipGetLastError();
 }
@@ -840,69 +983,65 @@ static hipError_t launch_join(const float* part, int P, int64_t n, float* out, i
 // ---------------------------------------------------------------------------
 hipError_t launch_lora_forward(const LoraForward& p, hipStream_t s, int* kernels) {
   *kernels = 2;
-  const ShrinkArgs a{p.x, p.ldx, p.down, p.seg, nullptr, p.la, p.R, (int)p.K};
+  const ShrinkArgs a{p.x, p.ldx, p.down, p.seg, nullptr, p.la, nullptr, nullptr, 0, p.R, (int)p.K};
   hipError_t e = launch_shrink(a, s);
   if (e != hipSuccess) return e;
   const ExpandArgs b{p.la, p.up, p.seg, p.scale, p.base, p.ldb, p.out, p.ldo, p.R, (int)p.N};
   return launch_expand(b, p.out_f32 != 0, s);
 }
 
-// workspace: dla [M][R] float32, up [A][R][N] and down [A][K][R] transposed
-// (bf16), then the parts of the two gradients
+// workspace: dla [M][R] float32, dla and lora_act in row-octet order, up
+// [A][R][N] and down [A][K][R] transposed (bf16), the parts of the two gradients
 static size_t pad16(size_t n) { return (n + 15) & ~(size_t)15; }
 size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int R, int A) {
-  return pad16((size_t)M * R * 4) + (size_t)A * R * (N + K) * 2 +
-         (size_t)A * R * 4 * ((size_t)outer_parts(M, N, A) * N + (size_t)outer_parts(M, K, A) * K);
+  return pad16((size_t)M * R * 4) + 2 * rows8_bytes(M, R) + (size_t)A * R * (N + K) * 2 +
+         (size_t)A * R * 4 * ((size_t)outer_parts(M, N, R, A) * N + (size_t)outer_parts(M, K, R, A) * K);
 }
 
 hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kernels) {
-  const int A = p.seg.A, M = p.seg.M;
-  const int64_t wn = (int64_t)A * p.R * p.N, wk = (int64_t)A * p.R * p.K;
+  const int A = p.seg.A, M = p.seg.M, N = (int)p.N, K = (int)p.K;
+  const int64_t wn = (int64_t)A * p.R * N, wk = (int64_t)A * p.R * K;
   float* dla = reinterpret_cast<float*>(p.ws);
-  uint16_t* up_t = reinterpret_cast<uint16_t*>(p.ws + pad16((size_t)M * p.R * 4));
+  uint16_t* dla8 = reinterpret_cast<uint16_t*>(p.ws + pad16((size_t)M * p.R * 4));
+  uint16_t* la8 = dla8 + rows8_bytes(M, p.R) / 2;
+  uint16_t* up_t = la8 + rows8_bytes(M, p.R) / 2;
   uint16_t* down_t = up_t + wn;
   float* part_up = reinterpret_cast<float*>(down_t + wk);
-  const int pn = outer_parts(M, p.N, A), pk = outer_parts(M, p.K, A);
+  const int pn = outer_parts(M, N, p.R, A), pk = outer_parts(M, K, p.R, A);
   float* part_down = part_up + pn * wn;
+  const bool codes = p.x_scales != nullptr, dla_wanted = p.dx || p.d_down;
   hipError_t e = hipSuccess;
-  *kernels = 0;
-  if (p.dx || p.d_down) {
-    ++*kernels;
-    if ((e = launch_transpose(p.up, up_t, A, (int)p.N, p.R, s)) != hipSuccess) return e;
-    const ShrinkArgs a{p.dy, p.lddy, up_t, p.seg, p.scale, dla, p.R, (int)p.N};
+  *kernels = 1;
+  const PrepareArgs pre{dla_wanted ? p.up : nullptr, up_t, p.dx ? p.down : nullptr, down_t,
+                        p.d_up ? p.la : nullptr, la8, M, N, K, p.R, A, 0, 0};
+  if ((e = launch_prepare(pre, s)) != hipSuccess) return e;
+  if (dla_wanted) {
+    const ShrinkArgs a{p.dy, p.lddy, up_t, p.seg, p.scale, dla, p.d_down ? dla8 : nullptr,
+                       codes ? p.x_scales : nullptr, p.x_row_scales, p.R, N};
     ++*kernels;
     if ((e = launch_shrink(a, s)) != hipSuccess) return e;
   }
   if (p.dx) {
-    ++*kernels;
-    if ((e = launch_transpose(p.down, down_t, A, p.R, (int)p.K, s)) != hipSuccess) return e;
-    const ExpandArgs b{dla, down_t, p.seg, nullptr, p.dx_base, p.ldb, p.dx, p.lddx, p.R, (int)p.K};
+    const ExpandArgs b{dla, down_t, p.seg, nullptr, p.dx_base, p.ldb, p.dx, p.lddx, p.R, K};
     ++*kernels;
     if ((e = launch_expand(b, p.dx_f32 != 0, s)) != hipSuccess) return e;
   }
-  if (p.d_up) {
-    const bool join = pn > 1;
-    const OuterArgs o{p.la, p.dy, p.lddy, nullptr, 0, p.seg, p.scale, join ? part_up : p.d_up, wn, pn,
-                      !join && p.accumulate, p.R, (int)p.N};
+  if (!p.d_up && !p.d_down) return e;
+  const int rot = codes && p.d_down ? p.rot_group : 0;
+  const bool join_up = p.d_up && pn > 1, join_down = p.d_down && (pk > 1 || rot);
+  OuterArgs up{la8, p.dy, p.lddy, p.seg, p.scale, join_up ? part_up : p.d_up, wn, pn, !join_up && p.accumulate, p.R, N, 0};
+  OuterArgs down{dla8, p.x, p.ldx, p.seg, nullptr, join_down ? part_down : p.d_down, wk, pk, !join_down && p.accumulate,
+                 p.R, K, 0};
+  if (p.d_up) up.blocks = outer_blocks(up);
+  if (p.d_down) down.blocks = outer_blocks(down);
+  ++*kernels;
+  if ((e = codes ? launch_outer<true>(up, down, s) : launch_outer<false>(up, down, s)) != hipSuccess) return e;
+  if (join_up || join_down) {
+    JoinArgs ju{part_up, pn, wn, p.d_up, p.accumulate, 0}, jd{part_down, pk, wk, p.d_down, p.accumulate, 0};
+    if (join_up) ju.blocks = join_blocks(ju, 0);
+    if (join_down) jd.blocks = join_blocks(jd, rot);
     ++*kernels;
-    if ((e = launch_outer<false, true>(o, s)) != hipSuccess) return e;
-    if (join) {
-      ++*kernels;
-      if ((e = launch_join(part_up, pn, wn, p.d_up, p.accumulate, 0, s)) != hipSuccess) return e;
-    }
-  }
-  if (p.d_down) {
-    const bool codes = p.x_scales != nullptr;
-    const int rot = codes ? p.rot_group : 0;
-    const bool join = pk > 1 || rot;
-    const OuterArgs o{dla, p.x, p.ldx, p.x_scales, p.x_row_scales, p.seg, nullptr, join ? part_down : p.d_down, wk, pk,
-                      !join && p.accumulate, p.R, (int)p.K};
-    ++*kernels;
-    if ((e = codes ? launch_outer<true, false>(o, s) : launch_outer<false, false>(o, s)) != hipSuccess) return e;
-    if (join) {
-      ++*kernels;
-      if ((e = launch_join(part_down, pk, wk, p.d_down, p.accumulate, rot, s)) != hipSuccess) return e;
-    }
+    e = launch_join(ju, jd, rot, s);
   }
   return e;
 }
