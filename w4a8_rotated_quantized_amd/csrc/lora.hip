@@ -802,34 +802,47 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
     }
     __syncthreads();
   }
-  if (wave != 0 || !cok) return;
   const float cs = p.scale ? p.scale[a] : 1.f;
   float* out = p.out + part * p.part + (int64_t)a * p.R * p.C;
+  if constexpr (UP) {
+    // [C][R]: through LDS, so that neighbouring lanes write neighbouring ranks
+    // (rank 64, 4096 channels: 11 us less than lane by lane)
+    constexpr int PITCH = 4 * RG + 1;              // 16-byte words of a column
+    v4f* tile = red[0];
+    if (wave == 0) {
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tile[(8 * i + j) * PITCH + 4 * rg + g] = acc[rg][j];
+    }
+    __syncthreads();
+    const int cb = c - 8 * i;
+    for (int k = threadIdx.x; k < 128 * 4 * RG; k += 256) {
+      const int cc = cb + k / (4 * RG), r = r0 + k % (4 * RG) * 4;
+      if (cc >= p.C || r >= p.R) continue;         // R % 8 == 0: four ranks in or out together
+      v4f* o = reinterpret_cast<v4f*>(out + (int64_t)cc * p.R + r);
+      const v4f x = tile[k / (4 * RG) * PITCH + k % (4 * RG)];
+      v4f w = {0.f, 0.f, 0.f, 0.f};
+      if (p.accumulate) w = *o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] += x[e] * cs;
+      *o = w;
+    }
+    return;
+  }
+  if (wave != 0 || !cok) return;
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg) {
     const int r = r0 + 16 * rg + 4 * g;
     if (r >= p.R) continue;
-    if constexpr (UP) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v4f* o = reinterpret_cast<v4f*>(out + (int64_t)(c + j) * p.R + r);
-        v4f w;
-        if (p.accumulate) w = *o;
-        else w = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int e = 0; e < 4; ++e) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      float* o = out + (int64_t)(r + e) * p.C + c;
+      if (p.accumulate) load_out8(o, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] += acc[rg][j][e] * cs;
-        *o = w;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        float* o = out + (int64_t)(r + e) * p.C + c;
-        if (p.accumulate) load_out8(o, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += acc[rg][j][e] * cs;
-        store_out8(o, v);
-      }
+      for (int j = 0; j < 8; ++j) v[j] += acc[rg][j][e] * cs;
+      store_out8(o, v);
     }
   }
 }
@@ -857,11 +870,14 @@ static hipError_t launch_outer(const OuterArgs& up, const OuterArgs& down, hipSt
   return hipGetLastError();
 }
 
-// Parts an adapter's rows are split into: enough blocks for two on each of the
-// GPU's 256 compute units, at least 128 rows each were the rows even.
-static int outer_parts(int64_t M, int64_t C, int R, int A) {
-  const int64_t blocks = ((C + 127) / 128) * ((R + 63) / 64) * A;
-  int64_t P = 512 / blocks;
+// Parts an adapter's rows are split into: as many as keep both gradients' blocks
+// in one round on the GPU's 256 compute units, which hold two to four of them by
+// the registers of the rank (a block's
+// start and end cost as much as four of its steps: d_up of rank 64 and 4096
+// channels 28 us in 8 parts, 37 in 16), at least 128 rows each were the rows even.
+static int outer_parts(int64_t M, int64_t N, int64_t K, int R, int A) {
+  const int64_t blocks = ((N + 127) / 128 + (K + 127) / 128) * ((R + 63) / 64) * A;
+  int64_t P = (R <= 16 ? 1024 : (R <= 32 ? 768 : 512)) / blocks;
   const int64_t most = (M + 127) / 128;
   if (P > most) P = most;
   return P < 1 ? 1 : (int)P;
@@ -995,7 +1011,7 @@ hipError_t launch_lora_forward(const LoraForward& p, hipStream_t s, int* kernels
 static size_t pad16(size_t n) { return (n + 15) & ~(size_t)15; }
 size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int R, int A) {
   return pad16((size_t)M * R * 4) + 2 * rows8_bytes(M, R) + (size_t)A * R * (N + K) * 2 +
-         (size_t)A * R * 4 * ((size_t)outer_parts(M, N, R, A) * N + (size_t)outer_parts(M, K, R, A) * K);
+         (size_t)outer_parts(M, N, K, R, A) * A * R * (N + K) * 4;
 }
 
 hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kernels) {
@@ -1007,8 +1023,8 @@ hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kerne
   uint16_t* up_t = la8 + rows8_bytes(M, p.R) / 2;
   uint16_t* down_t = up_t + wn;
   float* part_up = reinterpret_cast<float*>(down_t + wk);
-  const int pn = outer_parts(M, N, p.R, A), pk = outer_parts(M, K, p.R, A);
-  float* part_down = part_up + pn * wn;
+  const int P = outer_parts(M, N, K, p.R, A);
+  float* part_down = part_up + P * wn;
   const bool codes = p.x_scales != nullptr, dla_wanted = p.dx || p.d_down;
   hipError_t e = hipSuccess;
   *kernels = 1;
@@ -1028,16 +1044,16 @@ hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kerne
   }
   if (!p.d_up && !p.d_down) return e;
   const int rot = codes && p.d_down ? p.rot_group : 0;
-  const bool join_up = p.d_up && pn > 1, join_down = p.d_down && (pk > 1 || rot);
-  OuterArgs up{la8, p.dy, p.lddy, p.seg, p.scale, join_up ? part_up : p.d_up, wn, pn, !join_up && p.accumulate, p.R, N, 0};
-  OuterArgs down{dla8, p.x, p.ldx, p.seg, nullptr, join_down ? part_down : p.d_down, wk, pk, !join_down && p.accumulate,
+  const bool join_up = p.d_up && P > 1, join_down = p.d_down && (P > 1 || rot);
+  OuterArgs up{la8, p.dy, p.lddy, p.seg, p.scale, join_up ? part_up : p.d_up, wn, P, !join_up && p.accumulate, p.R, N, 0};
+  OuterArgs down{dla8, p.x, p.ldx, p.seg, nullptr, join_down ? part_down : p.d_down, wk, P, !join_down && p.accumulate,
                  p.R, K, 0};
   if (p.d_up) up.blocks = outer_blocks(up);
   if (p.d_down) down.blocks = outer_blocks(down);
   ++*kernels;
   if ((e = codes ? launch_outer<true>(up, down, s) : launch_outer<false>(up, down, s)) != hipSuccess) return e;
   if (join_up || join_down) {
-    JoinArgs ju{part_up, pn, wn, p.d_up, p.accumulate, 0}, jd{part_down, pk, wk, p.d_down, p.accumulate, 0};
+    JoinArgs ju{part_up, P, wn, p.d_up, p.accumulate, 0}, jd{part_down, P, wk, p.d_down, p.accumulate, 0};
     if (join_up) ju.blocks = join_blocks(ju, 0);
     if (join_down) jd.blocks = join_blocks(jd, rot);
     ++*kernels;
