@@ -332,15 +332,14 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
 
 static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
   const int rg = (p.R + 15) / 16;
-  if (p.seg.M <= 256) {
-    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 2, 2>), dim3(tile_grid(p.seg, 16), rg), dim3(1024), 0, s, p);
-  } else if (rg <= 1) {
-    hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 8, 3, 2>), dim3(tile_grid(p.seg, 16)), dim3(512), 0, s, p);
-  } else if (rg <= 2) {
-    hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 5, 2, 2>), dim3(tile_grid(p.seg, 32)), dim3(320), 0, s, p);
-  } else {
-    hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 6, 1, 1>), dim3(tile_grid(p.seg, 32), (rg + 3) / 4), dim3(384), 0, s, p);
-  }
+  const unsigned t16 = tile_grid(p.seg, 16), t32 = tile_grid(p.seg, 32);
+  const bool many = p.seg.M >= 32 * 256;           // 32-row tiles for every one of the 256 compute units
+  if (p.seg.M <= 256) hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 2, 2>), dim3(t16, rg), dim3(1024), 0, s, p);
+  else if (rg <= 1) hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 8, 3, 2>), dim3(t16), dim3(512), 0, s, p);
+  else if (rg <= 2 && !many) hipLaunchKernelGGL((lora_shrink_kernel<2, 1, 8, 2, 2>), dim3(t16), dim3(512), 0, s, p);
+  else if (rg <= 2) hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 5, 2, 2>), dim3(t32), dim3(320), 0, s, p);
+  else if (!many) hipLaunchKernelGGL((lora_shrink_kernel<4, 1, 8, 1, 1>), dim3(t16, (rg + 3) / 4), dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 6, 1, 1>), dim3(t32, (rg + 3) / 4), dim3(384), 0, s, p);
   return hipGetLastError();
 }
 
@@ -391,22 +390,23 @@ CR_DEV void store_out8(T* p, const float (&v)[8]) {
   }
 }
 
-// A block takes SUB x 64 rows of one segment and 64 NJ columns, a wave 16 NJ of
-// them, whose weights it holds as operand fragments. 64 rows of lora_act are
-// split once for the whole block. The sums of a 16 x 16 NJ block go through
+// A block takes ROWS rows of one segment and 64 NJ columns, a wave 16 NJ of
+// them, whose weights it holds as operand fragments. lora_act is split once for
+// the whole block, up to 64 rows at a time. The sums of a 16 x 16 NJ block go through
 // LDS, so that base and out move as whole runs of columns, and the next block's
 // base is on its way during the products.
-template <int KS, int NJ, typename T, bool BASE, int SUB>
+template <int KS, int NJ, typename T, bool BASE, int ROWS>
 __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
   constexpr int W = 16 * NJ, RO = 4 * KS;         // columns of a wave; rank octets
+  constexpr int SUB = ROWS < 64 ? ROWS : 64;      // rows split at a time
   constexpr int V = 16 / sizeof(T);               // columns of one 16-byte access
   constexpr int CPR = W / V;                      // accesses per row
   constexpr int NB = 16 * CPR / 64;               // accesses per lane and block
   __shared__ float sums[4][16][W + 4];
-  __shared__ u32x4 la3[3][RO][64];
+  __shared__ u32x4 la3[3][RO][SUB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const RowTile t = find_tile<64 * SUB>(p.seg, blockIdx.x);
+  const RowTile t = find_tile<ROWS>(p.seg, blockIdx.x);
   if (t.lo >= t.hi) return;
   const int c0 = (blockIdx.y * 4 + wave) * W;
   const T* base = static_cast<const T*>(p.base);
@@ -495,10 +495,10 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
     }
     wave_lds_order();
   };
-  for (int st = t.lo; st < t.hi; st += 64) {
-    if (SUB > 1 && st != t.lo) __syncthreads();   // the last 64 rows' terms have been read
+  for (int st = t.lo; st < t.hi; st += SUB) {
+    if (ROWS > SUB && st != t.lo) __syncthreads();   // the last rows' terms have been read
 #pragma unroll
-    for (int k = threadIdx.x; k < 64 * RO; k += 256) {
+    for (int k = threadIdx.x; k < SUB * RO; k += 256) {
       const int ro = k % RO, row = k / RO;
       const int64_t m = st + row < t.hi ? st + row : t.hi - 1;
       float v[8];
@@ -511,7 +511,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
       for (int term = 0; term < 3; ++term) la3[term][ro][row] = f[term];
     }
     __syncthreads();
-    const int end = st + 64 < t.hi ? st + 64 : t.hi;
+    const int end = st + SUB < t.hi ? st + SUB : t.hi;
     for (int mt = st; mt < end; mt += 32) {
       block(bb[0], bb[1], mt, mt - st);
       if (mt + 16 < end) block(bb[1], bb[0], mt + 16, mt + 16 - st);
@@ -519,17 +519,20 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
   }
 }
 
-template <int KS, int NJ, typename T, int SUB>
-static void launch_expand_s(const ExpandArgs& p, hipStream_t s) {
-  const dim3 grid(tile_grid(p.seg, 64 * SUB), (p.C + 64 * NJ - 1) / (64 * NJ));
-  if (p.base) hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, true, SUB>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, false, SUB>), grid, dim3(256), 0, s, p);
+template <int KS, int NJ, typename T, int ROWS>
+static void launch_expand_rows(const ExpandArgs& p, hipStream_t s) {
+  const dim3 grid(tile_grid(p.seg, ROWS), (p.C + 64 * NJ - 1) / (64 * NJ));
+  if (p.base) hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, true, ROWS>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, false, ROWS>), grid, dim3(256), 0, s, p);
 }
+// Tall tiles read the weights less often, short ones end sooner: the tallest
+// that still give every one of the 256 compute units two blocks.
 template <int KS, int NJ, typename T>
 static void launch_expand_k(const ExpandArgs& p, hipStream_t s) {
-  // tall tiles read the weights less often, while there are enough of them for 256 compute units
-  if ((int64_t)(p.seg.M / 256) * ((p.C + 64 * NJ - 1) / (64 * NJ)) >= 512) launch_expand_s<KS, NJ, T, 4>(p, s);
-  else launch_expand_s<KS, NJ, T, 1>(p, s);
+  const int64_t columns = (p.C + 64 * NJ - 1) / (64 * NJ);
+  if (p.seg.M / 256 * columns >= 512) launch_expand_rows<KS, NJ, T, 256>(p, s);
+  else if (p.seg.M / 64 * columns >= 512) launch_expand_rows<KS, NJ, T, 64>(p, s);
+  else launch_expand_rows<KS, NJ, T, 16>(p, s);
 }
 template <typename T>
 static void launch_expand_t(const ExpandArgs& p, hipStream_t s) {
@@ -668,8 +671,9 @@ CR_DEV v8bf column_frag(const u32x2 (&row)[8], int j) {   // int8 codes, exact i
 
 // A block takes 128 columns, 16 RG ranks and one part of an adapter's rows;
 // its four waves take steps of 32 rows in turn and add their sums through LDS in
-// a fixed order. Lane i of a 16-lane group holds columns 8 i .. 8 i + 7. The next
-// step's v is on its way during the products.
+// a fixed order. Lane i of a 16-lane group holds columns 8 i .. 8 i + 7. During
+// the products of a step the next one is on its way: v into registers, the
+// fragments of u, which would not fit beside it, into the wave's part of LDS.
 template <int RG, bool CODES, bool UP>
 CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
   typedef typename std::conditional<CODES, u32x2, u32x4>::type Row;
@@ -697,17 +701,29 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[rg][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
+  const float cs = p.scale ? p.scale[a] : 1.f;
+  // lane's segment of the 64 that start at s0: its first row and its rows, 0 if
+  // it is not of this adapter
+  int lo, len;
+  auto segments = [&](int s0) {
+    const int s = s0 + lane;
+    const int hi = seg_bound(p.seg, s + 2), of = seg_adapter(p.seg, s + 1);
+    lo = seg_bound(p.seg, s + 1);
+    len = s < p.seg.S && hi > lo && of == a ? hi - lo : 0;
+  };
+  segments(0);
   int64_t from = 0, to = (int64_t)1 << 62;        // this part of the adapter's rows, counted through its segments
   if (p.P > 1) {
-    int64_t n = 0;
-    for (int s = lane; s < p.seg.S; s += 64) {
-      const int lo = seg_bound(p.seg, s + 1), hi = seg_bound(p.seg, s + 2);
-      if (hi > lo && seg_adapter(p.seg, s + 1) == a) n += hi - lo;
+    int64_t n = len;
+    for (int s0 = 64; s0 < p.seg.S; s0 += 64) {
+      segments(s0);
+      n += len;
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
     from = n * part / p.P;
     to = n * (part + 1) / p.P;
+    if (p.seg.S > 64) segments(0);
   }
 
   // rows [mlo, mhi) in steps of 32 that start at multiples of 32; rows of a step
@@ -719,14 +735,29 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
       row[e] = *reinterpret_cast<const Row*>(vcol + (int64_t)(m < p.seg.M ? m : p.seg.M - 1) * p.ldv);
     }
   };
-  auto products = [&](Row (&row)[8], int m0, int mlo, int mhi) {
-    u32x4 uf[RG][3];
+  u32x4* next_u = reinterpret_cast<u32x4*>(red[0]) + wave * RG * 3 * 64;     // the sums take this memory only after the last step
+  auto load_u = [&](int m0) {
     const int m8 = (m0 >> 3) + g < (p.seg.M + 7) / 8 ? (m0 >> 3) + g : 0;
 #pragma unroll
     for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
       for (int q = 0; q < 3; ++q)
-        uf[rg][q] = *reinterpret_cast<const u32x4*>(ucol[rg] + q * term + (int64_t)m8 * p.R * 8);
+        __builtin_amdgcn_global_load_lds((lora_gptr)(ucol[rg] + q * term + (int64_t)m8 * p.R * 8),
+                                         (lora_lptr)(next_u + (rg * 3 + q) * 64), 16, 0, 0);
+  };
+  // step m0: row holds its v, next_u its u; then the same for step m1 in next_row
+  auto step = [&](Row (&row)[8], Row (&next_row)[8], int m0, int m1, int mlo, int mhi) {
+    wait_vmcnt<0>();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    u32x4 uf[RG][3];
+#pragma unroll
+    for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) uf[rg][q] = next_u[(rg * 3 + q) * 64 + lane];
+    __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): read before the next step's arrive
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    load_u(m1);
+    load_v(next_row, m1);
     if (m0 < mlo || m0 + 32 > mhi) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -755,9 +786,7 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
   int turn = 0;                                    // steps so far, over all segments
   int64_t before = 0;
   for (int s0 = 0; s0 < p.seg.S; s0 += 64) {
-    const int s = s0 + lane;
-    const int lo = seg_bound(p.seg, s + 1), hi = seg_bound(p.seg, s + 2);
-    const int len = s < p.seg.S && hi > lo && seg_adapter(p.seg, s + 1) == a ? hi - lo : 0;
+    if (s0 > 0) segments(s0);
     for (uint64_t left = __ballot(len > 0); left; left &= left - 1) {
       const int src = __builtin_ctzll(left);
       const int slo = __builtin_amdgcn_readlane(lo, src), slen = __builtin_amdgcn_readlane(len, src);
@@ -770,17 +799,20 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
       int k = (wave - turn) & 3;                   // this wave's steps: k, k + 4, ...
       turn += count;
       if (k >= count) continue;
+      wait_vmcnt<0>();                             // the last segment's loads for nothing
+      load_u(m00 + 32 * k);
       load_v(va, m00 + 32 * k);
+      // past the last step: the step itself once more, for nothing
       for (; k < count; k += 8) {
-        // past the last step: any rows of the batch, for nothing
-        load_v(vb, m00 + 32 * (k + 4 < count ? k + 4 : k));
-        products(va, m00 + 32 * k, mlo, mhi);
-        if (k + 4 >= count) break;
-        load_v(va, m00 + 32 * (k + 8 < count ? k + 8 : k));
-        products(vb, m00 + 32 * (k + 4), mlo, mhi);
+        const int k1 = k + 4 < count ? k + 4 : k;
+        step(va, vb, m00 + 32 * k, m00 + 32 * k1, mlo, mhi);
+        if (k1 == k) break;
+        step(vb, va, m00 + 32 * k1, m00 + 32 * (k + 8 < count ? k + 8 : k1), mlo, mhi);
       }
     }
   }
+  wait_vmcnt<0>();
+  __syncthreads();                                 // every wave's u has arrived and been read
 #pragma unroll
   for (int n = 2; n >= 1; n >>= 1) {
     if (wave >= n && wave < 2 * n) {
@@ -802,7 +834,6 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
     }
     __syncthreads();
   }
-  const float cs = p.scale ? p.scale[a] : 1.f;
   float* out = p.out + part * p.part + (int64_t)a * p.R * p.C;
   if constexpr (UP) {
     // [C][R]: through LDS, so that neighbouring lanes write neighbouring ranks
