@@ -745,8 +745,9 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
         __builtin_amdgcn_global_load_lds((lora_gptr)(ucol[rg] + q * term + (int64_t)m8 * p.R * 8),
                                          (lora_lptr)(next_u + (rg * 3 + q) * 64), 16, 0, 0);
   };
-  // step m0: row holds its v, next_u its u; then the same for step m1 in next_row
-  auto step = [&](Row (&row)[8], Row (&next_row)[8], int m0, int m1, int mlo, int mhi) {
+  // step m0: next holds its v, next_u its u; then those of step m1
+  Row next[8];
+  auto step = [&](int m0, int m1, int mlo, int mhi) {
     wait_vmcnt<0>();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     u32x4 uf[RG][3];
@@ -756,8 +757,11 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
       for (int q = 0; q < 3; ++q) uf[rg][q] = next_u[(rg * 3 + q) * 64 + lane];
     __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): read before the next step's arrive
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    Row row[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) row[e] = next[e];
     load_u(m1);
-    load_v(next_row, m1);
+    load_v(next, m1);
     if (m0 < mlo || m0 + 32 > mhi) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -782,7 +786,6 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
         for (int rg = 0; rg < RG; ++rg) acc[rg][j] = mfma16(__builtin_bit_cast(v8bf, uf[rg][q]), vf, acc[rg][j]);
     }
   };
-  Row va[8], vb[8];
   int turn = 0;                                    // steps so far, over all segments
   int64_t before = 0;
   for (int s0 = 0; s0 < p.seg.S; s0 += 64) {
@@ -801,19 +804,16 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
       if (k >= count) continue;
       wait_vmcnt<0>();                             // the last segment's loads for nothing
       load_u(m00 + 32 * k);
-      load_v(va, m00 + 32 * k);
-      // past the last step: the step itself once more, for nothing
-      for (; k < count; k += 8) {
-        const int k1 = k + 4 < count ? k + 4 : k;
-        step(va, vb, m00 + 32 * k, m00 + 32 * k1, mlo, mhi);
-        if (k1 == k) break;
-        step(vb, va, m00 + 32 * k1, m00 + 32 * (k + 8 < count ? k + 8 : k1), mlo, mhi);
-      }
+      load_v(next, m00 + 32 * k);
+      // one copy of the step's code: a block runs it a few times only, and fetching it counts
+#pragma unroll 1
+      for (; k < count; k += 4)
+        step(m00 + 32 * k, m00 + 32 * (k + 4 < count ? k + 4 : k), mlo, mhi);   // behind the last: itself, for nothing
     }
   }
   wait_vmcnt<0>();
   __syncthreads();                                 // every wave's u has arrived and been read
-#pragma unroll
+#pragma unroll 1
   for (int n = 2; n >= 1; n >>= 1) {
     if (wave >= n && wave < 2 * n) {
 #pragma unroll
@@ -834,47 +834,42 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
     }
     __syncthreads();
   }
-  float* out = p.out + part * p.part + (int64_t)a * p.R * p.C;
-  if constexpr (UP) {
-    // [C][R]: through LDS, so that neighbouring lanes write neighbouring ranks
-    // (rank 64, 4096 channels: 11 us less than lane by lane)
-    constexpr int PITCH = 4 * RG + 1;              // 16-byte words of a column
-    v4f* tile = red[0];
-    if (wave == 0) {
+  // The sums go out through LDS, so that neighbouring lanes write neighbouring
+  // values (d_up of rank 64 and 4096 channels: 11 us less than lane by lane).
+  constexpr int PITCH = UP ? 4 * RG + 1 : 33;      // 16-byte words of a column (up) or of a rank
+  constexpr int LINE = UP ? 4 * RG : 32;
+  v4f* tile = red[0];
+  if (wave == 0) {
 #pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
+    for (int rg = 0; rg < RG; ++rg) {
+      if constexpr (UP) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) tile[(8 * i + j) * PITCH + 4 * rg + g] = acc[rg][j];
-    }
-    __syncthreads();
-    const int cb = c - 8 * i;
-    for (int k = threadIdx.x; k < 128 * 4 * RG; k += 256) {
-      const int cc = cb + k / (4 * RG), r = r0 + k % (4 * RG) * 4;
-      if (cc >= p.C || r >= p.R) continue;         // R % 8 == 0: four ranks in or out together
-      v4f* o = reinterpret_cast<v4f*>(out + (int64_t)cc * p.R + r);
-      const v4f x = tile[k / (4 * RG) * PITCH + k % (4 * RG)];
-      v4f w = {0.f, 0.f, 0.f, 0.f};
-      if (p.accumulate) w = *o;
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] += x[e] * cs;
-      *o = w;
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int j = 0; j < 8; j += 4)
+            tile[(16 * rg + 4 * g + e) * PITCH + 2 * i + j / 4] =
+                v4f{acc[rg][j][e], acc[rg][j + 1][e], acc[rg][j + 2][e], acc[rg][j + 3][e]};
+      }
     }
-    return;
   }
-  if (wave != 0 || !cok) return;
+  __syncthreads();
+  float* out = p.out + part * p.part + (int64_t)a * p.R * p.C;
+  const int cb = c - 8 * i;
+#pragma unroll 1
+  for (int k = threadIdx.x; k < 16 * RG * 32; k += 256) {
+    const int row = k / LINE, at = k % LINE;
+    const int cc = cb + (UP ? row : 4 * at), r = r0 + (UP ? 4 * at : row);
+    if (cc >= p.C || r >= p.R) continue;           // C and R are multiples of 8: four values in or out together
+    v4f* o = reinterpret_cast<v4f*>(out + (UP ? (int64_t)cc * p.R + r : (int64_t)r * p.C + cc));
+    v4f w = {0.f, 0.f, 0.f, 0.f};
+    if (p.accumulate) w = *o;
+    const v4f x = tile[row * PITCH + at];
 #pragma unroll
-  for (int rg = 0; rg < RG; ++rg) {
-    const int r = r0 + 16 * rg + 4 * g;
-    if (r >= p.R) continue;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      float* o = out + (int64_t)(r + e) * p.C + c;
-      if (p.accumulate) load_out8(o, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += acc[rg][j][e] * cs;
-      store_out8(o, v);
-    }
+    for (int e = 0; e < 4; ++e) w[e] += x[e] * cs;
+    *o = w;
   }
 }
 
