@@ -114,6 +114,7 @@ SHAPES = [
     (63, 1000, 264, 64, 4, 5, "gaps"), (65, 264, 1000, 128, 2, 3, "ragged"), (256, 136, 136, 120, 3, 9, "gaps"),
     (257, 512, 256, 16, 5, 70, "ragged"), (300, 200, 520, 48, 4, 300, "tokens"), (519, 640, 384, 32, 6, 41, "prompt"),
     (700, 72, 2056, 72, 2, 130, "gaps"), (1033, 384, 640, 64, 3, 7, "ragged"),
+    (64, 4104, 4096, 32, 4, 64, "tokens"), (33, 2056, 136, 24, 2, 3, "gaps"), (200, 2048, 72, 8, 3, 9, "gaps"),
 ]
 
 
@@ -414,11 +415,12 @@ def test_captured_and_replayed(cr):
 
 
 def test_counters(cr):
-    t = Case(20, 72, 64, 8, 2, 3)
-    cr.reset_counters()
-    t.fwd(cr)
-    c = cr.get_counters()
-    assert c["lora"] == 2 and c["fallbacks"] == 0
+    for M, launches in ((20, 1), (300, 2)):          # few rows: one launch
+        t = Case(M, 72, 64, 8, 2, 3)
+        cr.reset_counters()
+        t.fwd(cr)
+        c = cr.get_counters()
+        assert c["lora"] == launches and c["fallbacks"] == 0
 
 
 def test_refusals(cr):

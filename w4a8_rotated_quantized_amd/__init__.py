@@ -481,11 +481,15 @@ def convrot_lora_forward(x, down, up, seg_offsets, seg_adapter, scale=None, base
     pb, ldb = (None, N) if base is None else _rows(base, "base", dt, index, M, N)
     with _on(index, stream):
         if out is None:
-            out = torch.empty((M, N), dtype=dt, device=x.device)
+            out, ldo = torch.empty((M, N), dtype=dt, device=x.device), N
+            py = out.data_ptr()
+        else:
+            py, ldo = _rows(out, "out", dt, index, M, N)
         if lora_act is None:
             lora_act = torch.empty((M, R), dtype=_F32, device=x.device)
-        py, ldo = _rows(out, "out", dt, index, M, N)
-        pl = _tensor(lora_act, "lora_act", _F32, index, (M, R))
+            pl = lora_act.data_ptr()
+        else:
+            pl = _tensor(lora_act, "lora_act", _F32, index, (M, R))
         st = lib.convrot_lora_forward(px, ldx, pd, pu, R, A, po, pa, S, ps, pb, ldb, py, out_type, ldo, pl, M, N, K,
                                       _current_stream_handle(index))
     _check(st, "convrot_lora_forward")
@@ -531,17 +535,22 @@ def convrot_lora_backward(dy, lora_act, x, down, up, seg_offsets, seg_adapter, s
     if want_dx and dx_base is not None:
         pb, ldb = _rows(dx_base, "dx_base", dt, index, M, K)
     with _on(index, stream):
-        if want_dx:
-            if dx is None:
-                dx = torch.empty((M, K), dtype=dt, device=dev)
+        if want_dx and dx is None:
+            dx = torch.empty((M, K), dtype=dt, device=dev)
+            pdx = dx.data_ptr()
+        elif want_dx:
             pdx, lddx = _rows(dx, "dx", dt, index, M, K)
         if want_weights:
             if d_down is None:
                 d_down = torch.empty((A, R, K), dtype=_F32, device=dev)
+                pgd = d_down.data_ptr()
+            else:
+                pgd = _tensor(d_down, "d_down", _F32, index, (A, R, K))
             if d_up is None:
                 d_up = torch.empty((A, N, R), dtype=_F32, device=dev)
-            pgd = _tensor(d_down, "d_down", _F32, index, (A, R, K))
-            pgu = _tensor(d_up, "d_up", _F32, index, (A, N, R))
+                pgu = d_up.data_ptr()
+            else:
+                pgu = _tensor(d_up, "d_up", _F32, index, (A, N, R))
         if workspace is None:
             need = lib.convrot_lora_backward_workspace_size(M, N, K, R, A)
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
@@ -573,14 +582,20 @@ def convrot_act_checkpoint(z, act, y=None, codes=None, scales=None, stream=None)
     pz, ldz = _rows(z, "z", _BF16, index, rows, W)
     with _on(index, stream):
         if y is None:
-            y = torch.empty((rows, C), dtype=_BF16, device=z.device)
+            y, ldy = torch.empty((rows, C), dtype=_BF16, device=z.device), C
+            py = y.data_ptr()
+        else:
+            py, ldy = _rows(y, "y", _BF16, index, rows, C)
         if codes is None:
             codes = torch.empty((rows, W), dtype=_I8, device=z.device)
+            pc = codes.data_ptr()
+        else:
+            pc = _tensor(codes, "codes", _I8, index, (rows, W))
         if scales is None:
             scales = torch.empty((rows, W // 64), dtype=_F32, device=z.device)
-        py, ldy = _rows(y, "y", _BF16, index, rows, C)
-        pc = _tensor(codes, "codes", _I8, index, (rows, W))
-        ps = _tensor(scales, "scales", _F32, index, (rows, W // 64))
+            ps = scales.data_ptr()
+        else:
+            ps = _tensor(scales, "scales", _F32, index, (rows, W // 64))
         st = lib.convrot_act_checkpoint(pz, ldz, rows, C, act, py, ldy, pc, ps, _current_stream_handle(index))
     _check(st, "convrot_act_checkpoint")
     return y, codes, scales
@@ -599,8 +614,10 @@ def convrot_act_backward(dy, codes, scales, act, dz=None, stream=None):
     ps = _tensor(scales, "scales", _F32, index, (rows, W // 64))
     with _on(index, stream):
         if dz is None:
-            dz = torch.empty((rows, W), dtype=_BF16, device=dy.device)
-        pz, lddz = _rows(dz, "dz", _BF16, index, rows, W)
+            dz, lddz = torch.empty((rows, W), dtype=_BF16, device=dy.device), W
+            pz = dz.data_ptr()
+        else:
+            pz, lddz = _rows(dz, "dz", _BF16, index, rows, W)
         st = lib.convrot_act_backward(pdy, lddy, pc, ps, rows, C, act, pz, lddz, _current_stream_handle(index))
     _check(st, "convrot_act_backward")
     return dz

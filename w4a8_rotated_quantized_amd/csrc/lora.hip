@@ -178,9 +178,17 @@ CR_DEV void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
-// A block takes TM x 16 rows of one segment and 16 RG ranks. Its NW waves
+template <int RG, int TM, int NW, int DX, int DW>
+struct ShrinkLds {
+  static constexpr int nx = 2 * TM, nw = 2 * RG;   // loads (KB) of a stage: of x, of the weights
+  static constexpr int red = RG * TM * 64;         // 16-byte sums of a wave
+  static constexpr int ring = (DX * nx + DW * nw) * 1024 > red * 16 ? (DX * nx + DW * nw) * 1024 : red * 16;
+  static constexpr int bytes = NW * ring;
+};
+
+// The sums of TM x 16 rows of one segment and 16 RG ranks. A block's NW waves
 // share the columns in stages of 64 and add their sums through LDS in a fixed
-// order. A stage goes straight from memory into the wave's own LDS rings, DX
+// order (the caller does: lds holds [NW][RG TM 64] of them). A stage goes straight from memory into the wave's own LDS rings, DX
 // stages of x (from memory far away) and DW <= DX of the weights (from L2): one load moves 8 rows x 128 bytes, neighbouring lanes taking
 // neighbouring 16 bytes, so that every request is a whole line (the operand
 // order of the matrix cores, neighbouring lanes on different rows, reads the
@@ -188,23 +196,11 @@ CR_DEV void wait_vmcnt() {
 // Within a row's 128 bytes, chunk q lies at position q ^ (row % 8), which
 // spreads the fragment reads over the banks.
 template <int RG, int TM, int NW, int DX, int DW>
-__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
-  constexpr int NX = 2 * TM, NWT = 2 * RG;         // loads (KB) of a stage: of x, of the weights
-  constexpr int RED = RG * TM * 64;                // 16-byte sums of a wave
-  constexpr int KB = DX * NX + DW * NWT;
-  constexpr int RING = KB * 1024 > RED * 16 ? KB * 1024 : RED * 16;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * RING];
+CR_DEV void shrink_sums(const ShrinkArgs& p, const RowTile& t, int r0, uint8_t* lds) {
+  typedef ShrinkLds<RG, TM, NW, DX, DW> L;
+  constexpr int NX = L::nx, NWT = L::nw, RED = L::red;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int r0 = blockIdx.y * 16 * RG;
-  const RowTile t = find_tile<16 * TM>(p.seg, blockIdx.x);
-  if (t.lo >= t.hi) return;
-  if (t.a < 0) {                                  // rows without adapter: zeros
-    const int nr = p.R - r0 < 16 * RG ? p.R - r0 : 16 * RG;
-    for (int k = threadIdx.x; k < (t.hi - t.lo) * nr; k += 64 * NW)
-      p.la[(int64_t)(t.lo + k / nr) * p.R + r0 + k % nr] = 0.f;
-    return;
-  }
   const int lr = lane >> 3, lc = 8 * ((lane & 7) ^ lr);   // row and column of the lane's 16 bytes in a load
   const uint16_t* xr[NX];
   const uint16_t* wr[NWT];
@@ -218,7 +214,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
     const int r = r0 + 8 * n + lr;
     wr[n] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C;
   }
-  uint8_t* xring = lds + wave * RING;
+  uint8_t* xring = lds + wave * ShrinkLds<RG, TM, NW, DX, DW>::ring;
   uint8_t* wring = xring + DX * NX * 1024;
   const int stages = ((p.C + 63) / 64 - wave + NW - 1) / NW;   // may be 0
   // blocks start at different columns: rows a power of two apart share an L2 channel
@@ -305,6 +301,24 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) red[wave * RED + (rg * TM + tm) * 64 + lane] = acc[rg][tm];
   __syncthreads();
+}
+
+// a block: TM x 16 rows of one segment and 16 RG ranks
+template <int RG, int TM, int NW, int DX, int DW>
+__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
+  constexpr int RED = ShrinkLds<RG, TM, NW, DX, DW>::red;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ShrinkLds<RG, TM, NW, DX, DW>::bytes];
+  const int r0 = blockIdx.y * 16 * RG;
+  const RowTile t = find_tile<16 * TM>(p.seg, blockIdx.x);
+  if (t.lo >= t.hi) return;
+  if (t.a < 0) {                                  // rows without adapter: zeros
+    const int nr = p.R - r0 < 16 * RG ? p.R - r0 : 16 * RG;
+    for (int k = threadIdx.x; k < (t.hi - t.lo) * nr; k += 64 * NW)
+      p.la[(int64_t)(t.lo + k / nr) * p.R + r0 + k % nr] = 0.f;
+    return;
+  }
+  shrink_sums<RG, TM, NW, DX, DW>(p, t, r0, lds);
+  const v4f* red = reinterpret_cast<const v4f*>(lds);
   const float cs = p.scale ? p.scale[t.a] : 1.f;
   for (int k = threadIdx.x; k < RED; k += 64 * NW) {
     const int rg = k / 64 / TM, tm = k / 64 % TM, kl = k % 64;
@@ -390,72 +404,66 @@ CR_DEV void store_out8(T* p, const float (&v)[8]) {
   }
 }
 
-// A block takes ROWS rows of one segment and 64 NJ columns, a wave 16 NJ of
-// them, whose weights it holds as operand fragments. lora_act is split once for
-// the whole block, up to 64 rows at a time. The sums of a 16 x 16 NJ block go through
-// LDS, so that base and out move as whole runs of columns, and the next block's
-// base is on its way during the products.
-template <int KS, int NJ, typename T, bool BASE, int ROWS>
-__global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
-  constexpr int W = 16 * NJ, RO = 4 * KS;         // columns of a wave; rank octets
-  constexpr int SUB = ROWS < 64 ? ROWS : 64;      // rows split at a time
-  constexpr int V = 16 / sizeof(T);               // columns of one 16-byte access
-  constexpr int CPR = W / V;                      // accesses per row
-  constexpr int NB = 16 * CPR / 64;               // accesses per lane and block
-  __shared__ float sums[4][16][W + 4];
-  __shared__ u32x4 la3[3][RO][SUB];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int i = lane & 15, g = lane >> 4;
-  const RowTile t = find_tile<ROWS>(p.seg, blockIdx.x);
-  if (t.lo >= t.hi) return;
-  const int c0 = (blockIdx.y * 4 + wave) * W;
-  const T* base = static_cast<const T*>(p.base);
-  T* out = static_cast<T*>(p.out);
-  const int brow = lane / CPR, bcol = c0 + lane % CPR * V;   // access q: row brow + q * 64 / CPR, columns bcol ..
-  const bool cok = bcol < p.C;                    // C % 8 == 0: an access lies in or out as a whole
-  const int bc = cok ? bcol : 0;
-  auto load_base = [&](u32x4 (&b)[NB], int mt) {
+// What one wave does with 16 NJ columns from c0 on.
+template <int KS, int NJ, typename T>
+struct ExpandWave {
+  static constexpr int W = 16 * NJ;
+  static constexpr int V = 16 / sizeof(T);        // columns of one 16-byte access of base and out
+  static constexpr int CPR = W / V;               // accesses per row
+  static constexpr int NB = 16 * CPR / 64;        // accesses per lane and 16 rows
+  static constexpr int PITCH = W + 4;             // floats of a row of sums in LDS
+  const ExpandArgs& p;
+  const RowTile& t;
+  int c0, lane;
+
+  // access q: row lane / CPR + q * 64 / CPR, columns column() ..; C % 8 == 0: in or out as a whole
+  CR_DEV int row(int q) const { return lane / CPR + q * (64 / CPR); }
+  CR_DEV int column() const { return c0 + lane % CPR * V; }
+  CR_DEV void load_base(u32x4 (&b)[NB], int mt) const {
+    const int c = column() < p.C ? column() : 0;
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
-      const int m = mt + brow + q * (64 / CPR);
-      b[q] = *reinterpret_cast<const u32x4*>(base + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldb + bc);
+      const int m = mt + row(q);                  // past the tile: its last row, for nothing
+      b[q] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.base) + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldb + c);
     }
-  };
-  if (t.a < 0) {                                  // rows without adapter: the base alone
-    if (static_cast<const void*>(base) == static_cast<const void*>(out)) return;
+  }
+  CR_DEV void store(const u32x4& v, int q, int mt) const {
+    const int m = mt + row(q);
+    if (m < t.hi && column() < p.C) *reinterpret_cast<u32x4*>(static_cast<T*>(p.out) + (int64_t)m * p.ldo + column()) = v;
+  }
+  // rows without adapter: the base alone, nothing if that is out itself
+  template <bool BASE>
+  CR_DEV void copy_base() const {
+    if (p.base == p.out) return;
     for (int mt = t.lo; mt < t.hi; mt += 16) {
       u32x4 b[NB];
 #pragma unroll
       for (int q = 0; q < NB; ++q) b[q] = u32x4{0, 0, 0, 0};
       if constexpr (BASE) load_base(b, mt);
 #pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        const int m = mt + brow + q * (64 / CPR);
-        if (m < t.hi && cok) *reinterpret_cast<u32x4*>(out + (int64_t)m * p.ldo + bcol) = b[q];
+      for (int q = 0; q < NB; ++q) store(b[q], q, mt);
+    }
+  }
+  CR_DEV void load_weights(v8bf (&wf)[NJ][KS]) const {
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int c = c0 + 16 * j + i < p.C ? c0 + 16 * j + i : p.C - 1;
+      const uint16_t* w = p.w + ((int64_t)t.a * p.C + c) * p.R;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int r = 32 * ks + 8 * g;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(w + (r < p.R ? r : 0)), z = {0, 0, 0, 0};
+        wf[j][ks] = __builtin_bit_cast(v8bf, r < p.R ? v : z);
       }
     }
-    return;
   }
-  u32x4 bb[2][NB];
-#pragma unroll
-  for (int q = 0; q < NB; ++q) bb[0][q] = bb[1][q] = u32x4{0, 0, 0, 0};
-  if constexpr (BASE) load_base(bb[0], t.lo);
-  const float cs = p.scale ? p.scale[t.a] : 1.f;
-  v8bf wf[NJ][KS];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int c = c0 + 16 * j + i < p.C ? c0 + 16 * j + i : p.C - 1;
-    const uint16_t* w = p.w + ((int64_t)t.a * p.C + c) * p.R;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int r = 32 * ks + 8 * g;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(w + (r < p.R ? r : 0)), z = {0, 0, 0, 0};
-      wf[j][ks] = __builtin_bit_cast(v8bf, r < p.R ? v : z);
-    }
-  }
-  auto block = [&](u32x4 (&b)[NB], u32x4 (&bn)[NB], int mt, int row0) {
-    // behind the tile: its last row once more, for nothing
-    if constexpr (BASE) load_base(bn, mt + 16);
+  // 16 rows from mt on: la3 holds their lora_act as three bf16 terms ([term][octet of ranks][SUB
+  // rows], these from row0 on), sums takes the products and gives them back by rows
+  template <int SUB>
+  CR_DEV void add_rows(const v8bf (&wf)[NJ][KS], const u32x4 (*la3)[4 * KS][SUB], int row0, float* sums,
+                       const u32x4 (&b)[NB], int mt) const {
+    const int i = lane & 15, g = lane >> 4;
     v4f acc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -468,13 +476,12 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
         for (int j = 0; j < NJ; ++j) acc[j] = mfma16(wf[j][ks], f, acc[j]);
       }
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) *reinterpret_cast<v4f*>(&sums[wave][i][16 * j + 4 * g]) = acc[j];
+    for (int j = 0; j < NJ; ++j) *reinterpret_cast<v4f*>(sums + i * PITCH + 16 * j + 4 * g) = acc[j];
     wave_lds_order();
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
-      const int row = brow + q * (64 / CPR);
       float d[V];
-      const float* src = &sums[wave][row][lane % CPR * V];
+      const float* src = sums + row(q) * PITCH + lane % CPR * V;
 #pragma unroll
       for (int e = 0; e < V; e += 4) {
         const v4f x = *reinterpret_cast<const v4f*>(src + e);
@@ -491,10 +498,39 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(b[q][k]) + d[k]);
       }
-      if (mt + row < t.hi && cok) *reinterpret_cast<u32x4*>(out + (int64_t)(mt + row) * p.ldo + bcol) = o;
+      store(o, q, mt);
     }
     wave_lds_order();
-  };
+  }
+};
+
+// A block takes ROWS rows of one segment and 64 NJ columns, a wave 16 NJ of
+// them, whose weights it holds as operand fragments. lora_act is split once for
+// the whole block, up to 64 rows at a time. The sums of a 16 x 16 NJ block go through
+// LDS, so that base and out move as whole runs of columns, and the next block's
+// base is on its way during the products.
+template <int KS, int NJ, typename T, bool BASE, int ROWS>
+__global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
+  typedef ExpandWave<KS, NJ, T> Wave;
+  constexpr int RO = 4 * KS;                      // rank octets
+  constexpr int SUB = ROWS < 64 ? ROWS : 64;      // rows split at a time
+  __shared__ float sums[4][16 * Wave::PITCH];
+  __shared__ u32x4 la3[3][RO][SUB];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const RowTile t = find_tile<ROWS>(p.seg, blockIdx.x);
+  if (t.lo >= t.hi) return;
+  const Wave w{p, t, ((int)blockIdx.y * 4 + wave) * Wave::W, (int)threadIdx.x & 63};
+  if (t.a < 0) {
+    w.template copy_base<BASE>();
+    return;
+  }
+  u32x4 bb[2][Wave::NB];
+#pragma unroll
+  for (int q = 0; q < Wave::NB; ++q) bb[0][q] = bb[1][q] = u32x4{0, 0, 0, 0};
+  if constexpr (BASE) w.load_base(bb[0], t.lo);
+  const float cs = p.scale ? p.scale[t.a] : 1.f;
+  v8bf wf[NJ][KS];
+  w.load_weights(wf);
   for (int st = t.lo; st < t.hi; st += SUB) {
     if (ROWS > SUB && st != t.lo) __syncthreads();   // the last rows' terms have been read
 #pragma unroll
@@ -513,8 +549,12 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
     __syncthreads();
     const int end = st + SUB < t.hi ? st + SUB : t.hi;
     for (int mt = st; mt < end; mt += 32) {
-      block(bb[0], bb[1], mt, mt - st);
-      if (mt + 16 < end) block(bb[1], bb[0], mt + 16, mt + 16 - st);
+      if constexpr (BASE) w.load_base(bb[1], mt + 16);
+      w.add_rows(wf, la3, mt - st, sums[wave], bb[0], mt);
+      if (mt + 16 < end) {
+        if constexpr (BASE) w.load_base(bb[0], mt + 32);
+        w.add_rows(wf, la3, mt + 16 - st, sums[wave], bb[1], mt + 16);
+      }
     }
   }
 }
@@ -543,6 +583,83 @@ static void launch_expand_t(const ExpandArgs& p, hipStream_t s) {
 static hipError_t launch_expand(const ExpandArgs& p, bool f32, hipStream_t s) {
   if (f32) launch_expand_t<float>(p, s);
   else launch_expand_t<uint16_t>(p, s);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Both in one launch, for few rows: a block takes 16 rows of one segment and
+// 2048 columns of out and makes lora_act of the rows for itself. The launch
+// that this saves is worth more than the weights of the shrink that the blocks
+// of other columns read again.
+// ---------------------------------------------------------------------------
+template <int RG, typename T, bool BASE>
+__global__ __launch_bounds__(1024) void lora_few_kernel(ShrinkArgs sp, ExpandArgs p) {
+  constexpr int NW = 16, DX = RG == 1 ? 2 : 1, DW = DX;
+  typedef ExpandWave<1, 8, T> Wave;
+  typedef ShrinkLds<RG, 1, NW, DX, DW> Lds;
+  constexpr int SUMS = NW * 16 * Wave::PITCH * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Lds::bytes > SUMS ? Lds::bytes : SUMS];
+  __shared__ u32x4 la3[3][4][16];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const RowTile t = find_tile<16>(p.seg, blockIdx.x);
+  if (t.lo >= t.hi) return;
+  const Wave w{p, t, ((int)blockIdx.y * NW + wave) * Wave::W, (int)threadIdx.x & 63};
+  if (t.a < 0) {
+    if (blockIdx.y == 0)
+      for (int k = threadIdx.x; k < (t.hi - t.lo) * p.R; k += 64 * NW) sp.la[(int64_t)t.lo * p.R + k] = 0.f;
+    w.template copy_base<BASE>();
+    return;
+  }
+  const float cs = p.scale ? p.scale[t.a] : 1.f;
+  u32x4 b[Wave::NB];
+#pragma unroll
+  for (int q = 0; q < Wave::NB; ++q) b[q] = u32x4{0, 0, 0, 0};
+  constexpr bool EARLY = RG == 1 || sizeof(T) == 2;   // rank 32 and float32: no registers for it yet
+  if constexpr (BASE && EARLY) w.load_base(b, t.lo);
+  v8bf wf[8][1];
+  w.load_weights(wf);
+  shrink_sums<RG, 1, NW, DX, DW>(sp, t, 0, lds);
+  if constexpr (BASE && !EARLY) w.load_base(b, t.lo);
+  const v4f* red = reinterpret_cast<const v4f*>(lds);
+  if (threadIdx.x < 128) {                         // 16 rows x 32 ranks, four ranks a thread
+    const int rg = threadIdx.x >> 6, row = threadIdx.x & 15, r = 16 * rg + 4 * (threadIdx.x >> 4 & 3);
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+    if (r < p.R)                                   // R % 8 == 0
+      for (int n = 0; n < NW; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += red[n * Lds::red + (threadIdx.x & (64 * RG - 1))][e];
+    if (blockIdx.y == 0 && r < p.R && t.lo + row < t.hi)
+      *reinterpret_cast<v4f*>(sp.la + (int64_t)(t.lo + row) * p.R + r) = s;
+    Split q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = split3(s[e] * cs);
+    u32x2* to[3];
+#pragma unroll
+    for (int term = 0; term < 3; ++term) to[term] = reinterpret_cast<u32x2*>(&la3[term][r >> 3][row]) + (r >> 2 & 1);
+    *to[0] = u32x2{upper_pair(q[0].hi, q[1].hi), upper_pair(q[2].hi, q[3].hi)};
+    *to[1] = u32x2{upper_pair(q[0].mid, q[1].mid), upper_pair(q[2].mid, q[3].mid)};
+    *to[2] = u32x2{upper_pair(q[0].lo, q[1].lo), upper_pair(q[2].lo, q[3].lo)};
+  }
+  __syncthreads();                                 // also: the shrink's sums are read before lds takes others
+  if (w.c0 < p.C) w.add_rows(wf, la3, 0, reinterpret_cast<float*>(lds) + wave * 16 * Wave::PITCH, b, t.lo);
+}
+
+// Rows x column groups x weights of the shrink: what the blocks read of it, at
+// most 64 MB (64 rows of 64 requests, rank 32, 4096 x 4096: 2 x 16.8 MB).
+static bool few_rows(const LoraSegments& g, int R, int64_t N, int64_t K) {
+  return R <= 32 && g.M <= 256 && g.M * ((N + 2047) / 2048) * R * K <= ((int64_t)1 << 25);
+}
+template <int RG, typename T>
+static void launch_few_t(const ShrinkArgs& a, const ExpandArgs& b, hipStream_t s) {
+  const dim3 grid(tile_grid(b.seg, 16), (b.C + 2047) / 2048);
+  if (b.base) hipLaunchKernelGGL((lora_few_kernel<RG, T, true>), grid, dim3(1024), 0, s, a, b);
+  else hipLaunchKernelGGL((lora_few_kernel<RG, T, false>), grid, dim3(1024), 0, s, a, b);
+}
+static hipError_t launch_few(const ShrinkArgs& a, const ExpandArgs& b, bool f32, hipStream_t s) {
+  if (a.R <= 16 && f32) launch_few_t<1, float>(a, b, s);
+  else if (a.R <= 16) launch_few_t<1, uint16_t>(a, b, s);
+  else if (f32) launch_few_t<2, float>(a, b, s);
+  else launch_few_t<2, uint16_t>(a, b, s);
   return hipGetLastError();
 }
 
@@ -1024,11 +1141,13 @@ static hipError_t launch_join(const JoinArgs& up, const JoinArgs& down, int rot,
 // entry points
 // ---------------------------------------------------------------------------
 hipError_t launch_lora_forward(const LoraForward& p, hipStream_t s, int* kernels) {
-  *kernels = 2;
   const ShrinkArgs a{p.x, p.ldx, p.down, p.seg, nullptr, p.la, nullptr, nullptr, 0, p.R, (int)p.K};
-  hipError_t e = launch_shrink(a, s);
-  if (e != hipSuccess) return e;
   const ExpandArgs b{p.la, p.up, p.seg, p.scale, p.base, p.ldb, p.out, p.ldo, p.R, (int)p.N};
+  const bool few = few_rows(p.seg, p.R, p.N, p.K);
+  *kernels = few ? 1 : 2;
+  if (few) return launch_few(a, b, p.out_f32 != 0, s);
+  const hipError_t e = launch_shrink(a, s);
+  if (e != hipSuccess) return e;
   return launch_expand(b, p.out_f32 != 0, s);
 }
 
