@@ -118,8 +118,8 @@ CR_DEV void quantize8(const u32x4& w, const float (&v)[8], int8_t* codes, float*
   if (top >= 0x7F800000u) {
     s = __uint_as_float(0x7FC00000u);
   } else if (A > 3.8e-37f) {
-    r = div_rn(127.f, A);
-    s = div_rn(A, 127.f);
+    r = 127.f / A;                                 // float32 division: correctly rounded
+    s = A / 127.f;
   }
   uint32_t q[2] = {0, 0};
   if (r != 0.f) {
