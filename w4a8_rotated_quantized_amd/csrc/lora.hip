@@ -64,17 +64,16 @@ CR_DEV int wave_scan(int x) {
   return x;
 }
 
-// Tile t of T rows, counted through the stretches: each wave scans the tile
+// Tile t of T rows (a power of two), counted through the stretches: each wave scans the tile
 // counts of 64 stretches at a time. All 64 lanes take part; the result is
 // the same in all of them.
-template <int T>
-CR_DEV RowTile find_tile(const LoraSegments& g, int t) {
+CR_DEV RowTile find_tile(const LoraSegments& g, int t, int T) {
   const int lane = threadIdx.x & 63;
   for (int v0 = 0; v0 < g.S + 2; v0 += 64) {
     const int v = v0 + lane;
     const int lo = seg_bound(g, v), end = seg_bound(g, v + 1), a = seg_adapter(g, v);
     const int hi = end > lo && v < g.S + 2 ? end : lo;
-    const int n = (hi - lo + T - 1) / T;
+    const int n = (hi - lo + T - 1) >> __builtin_ctz(T);
     const int upto = wave_scan(n);
     const int total = __builtin_amdgcn_readlane(upto, 63);
     if (t < total) {
@@ -309,7 +308,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
   constexpr int RED = ShrinkLds<RG, TM, NW, DX, DW>::red;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[ShrinkLds<RG, TM, NW, DX, DW>::bytes];
   const int r0 = blockIdx.y * 16 * RG;
-  const RowTile t = find_tile<16 * TM>(p.seg, blockIdx.x);
+  const RowTile t = find_tile(p.seg, blockIdx.x, 16 * TM);
   if (t.lo >= t.hi) return;
   if (t.a < 0) {                                  // rows without adapter: zeros
     const int nr = p.R - r0 < 16 * RG ? p.R - r0 : 16 * RG;
@@ -370,6 +369,8 @@ struct ExpandArgs {
   void* out;
   int64_t ldo;
   int R, C;
+  int rows;              // of a tile, a power of two from 16 on (lora_expand_kernel)
+  int blocks_x;          // tiles at most
 };
 
 template <typename T>
@@ -415,16 +416,22 @@ struct ExpandWave {
   const ExpandArgs& p;
   const RowTile& t;
   int c0, lane;
+  // Without a base the loads go to one row of the adapter's weights, which are at
+  // hand (R >= 8 values of bf16 per column are longer than a row of out), and the
+  // mask makes zeros of them: no branch between a load and its use.
+  CR_DEV uint32_t mask() const { return p.base ? ~0u : 0u; }
 
   // access q: row lane / CPR + q * 64 / CPR, columns column() ..; C % 8 == 0: in or out as a whole
   CR_DEV int row(int q) const { return lane / CPR + q * (64 / CPR); }
   CR_DEV int column() const { return c0 + lane % CPR * V; }
   CR_DEV void load_base(u32x4 (&b)[NB], int mt) const {
     const int c = column() < p.C ? column() : 0;
+    const T* from = static_cast<const T*>(p.base ? p.base : static_cast<const void*>(p.w));
+    const int64_t ld = p.base ? p.ldb : 0;
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
       const int m = mt + row(q);                  // past the tile: its last row, for nothing
-      b[q] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.base) + (int64_t)(m < t.hi ? m : t.hi - 1) * p.ldb + c);
+      b[q] = *reinterpret_cast<const u32x4*>(from + (int64_t)(m < t.hi ? m : t.hi - 1) * ld + c);
     }
   }
   CR_DEV void store(const u32x4& v, int q, int mt) const {
@@ -432,16 +439,14 @@ struct ExpandWave {
     if (m < t.hi && column() < p.C) *reinterpret_cast<u32x4*>(static_cast<T*>(p.out) + (int64_t)m * p.ldo + column()) = v;
   }
   // rows without adapter: the base alone, nothing if that is out itself
-  template <bool BASE>
   CR_DEV void copy_base() const {
     if (p.base == p.out) return;
+    const uint32_t keep = mask();
     for (int mt = t.lo; mt < t.hi; mt += 16) {
       u32x4 b[NB];
+      load_base(b, mt);
 #pragma unroll
-      for (int q = 0; q < NB; ++q) b[q] = u32x4{0, 0, 0, 0};
-      if constexpr (BASE) load_base(b, mt);
-#pragma unroll
-      for (int q = 0; q < NB; ++q) store(b[q], q, mt);
+      for (int q = 0; q < NB; ++q) store(u32x4{b[q][0] & keep, b[q][1] & keep, b[q][2] & keep, b[q][3] & keep}, q, mt);
     }
   }
   CR_DEV void load_weights(v8bf (&wf)[NJ][KS]) const {
@@ -464,6 +469,7 @@ struct ExpandWave {
   CR_DEV void add_rows(const v8bf (&wf)[NJ][KS], const u32x4 (*la3)[4 * KS][SUB], int row0, float* sums,
                        const u32x4 (&b)[NB], int mt) const {
     const int i = lane & 15, g = lane >> 4;
+    const uint32_t keep = mask();
     v4f acc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -492,11 +498,11 @@ struct ExpandWave {
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)                // half to even, NaN kept
-          o[k] = __builtin_bit_cast(uint32_t, v2bf{(__bf16)(bf16_lo(b[q][k]) + d[2 * k]),
-                                                   (__bf16)(bf16_hi(b[q][k]) + d[2 * k + 1])});
+          o[k] = __builtin_bit_cast(uint32_t, v2bf{(__bf16)(bf16_lo(b[q][k] & keep) + d[2 * k]),
+                                                   (__bf16)(bf16_hi(b[q][k] & keep) + d[2 * k + 1])});
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(b[q][k]) + d[k]);
+        for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(b[q][k] & keep) + d[k]);
       }
       store(o, q, mt);
     }
@@ -504,37 +510,37 @@ struct ExpandWave {
   }
 };
 
-// A block takes ROWS rows of one segment and 64 NJ columns, a wave 16 NJ of
+// A block takes p.rows rows of one segment and 64 NJ columns, a wave 16 NJ of
 // them, whose weights it holds as operand fragments. lora_act is split once for
-// the whole block, up to 64 rows at a time. The sums of a 16 x 16 NJ block go through
+// the whole block, up to 32 rows at a time. The sums of a 16 x 16 NJ block go through
 // LDS, so that base and out move as whole runs of columns, and the next block's
 // base is on its way during the products.
-template <int KS, int NJ, typename T, bool BASE, int ROWS>
-__global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
+template <int KS, int NJ, typename T>
+struct ExpandLds {
+  float sums[4][16 * ExpandWave<KS, NJ, T>::PITCH];
+  u32x4 la3[3][4 * KS][32];
+};
+template <int KS, int NJ, typename T>
+CR_DEV void expand_block(const ExpandArgs& p, int bx, int by, ExpandLds<KS, NJ, T>& lds) {
   typedef ExpandWave<KS, NJ, T> Wave;
   constexpr int RO = 4 * KS;                      // rank octets
-  constexpr int SUB = ROWS < 64 ? ROWS : 64;      // rows split at a time
-  __shared__ float sums[4][16 * Wave::PITCH];
-  __shared__ u32x4 la3[3][RO][SUB];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const RowTile t = find_tile<ROWS>(p.seg, blockIdx.x);
+  const RowTile t = find_tile(p.seg, bx, p.rows);
   if (t.lo >= t.hi) return;
-  const Wave w{p, t, ((int)blockIdx.y * 4 + wave) * Wave::W, (int)threadIdx.x & 63};
+  const Wave w{p, t, (by * 4 + wave) * Wave::W, (int)threadIdx.x & 63};
   if (t.a < 0) {
-    w.template copy_base<BASE>();
+    w.copy_base();
     return;
   }
   u32x4 bb[2][Wave::NB];
-#pragma unroll
-  for (int q = 0; q < Wave::NB; ++q) bb[0][q] = bb[1][q] = u32x4{0, 0, 0, 0};
-  if constexpr (BASE) w.load_base(bb[0], t.lo);
+  w.load_base(bb[0], t.lo);
   const float cs = p.scale ? p.scale[t.a] : 1.f;
   v8bf wf[NJ][KS];
   w.load_weights(wf);
-  for (int st = t.lo; st < t.hi; st += SUB) {
-    if (ROWS > SUB && st != t.lo) __syncthreads();   // the last rows' terms have been read
-#pragma unroll
-    for (int k = threadIdx.x; k < SUB * RO; k += 256) {
+  for (int st = t.lo; st < t.hi; st += 32) {
+    if (st != t.lo) __syncthreads();              // the last rows' terms have been read
+    const int end = st + 32 < t.hi ? st + 32 : t.hi;
+    for (int k = threadIdx.x; k < ((end - st + 15) & ~15) * RO; k += 256) {
       const int ro = k % RO, row = k / RO;
       const int64_t m = st + row < t.hi ? st + row : t.hi - 1;
       float v[8];
@@ -544,35 +550,34 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
       u32x4 f[3];
       split8(v, f);
 #pragma unroll
-      for (int term = 0; term < 3; ++term) la3[term][ro][row] = f[term];
+      for (int term = 0; term < 3; ++term) lds.la3[term][ro][row] = f[term];
     }
     __syncthreads();
-    const int end = st + SUB < t.hi ? st + SUB : t.hi;
-    for (int mt = st; mt < end; mt += 32) {
-      if constexpr (BASE) w.load_base(bb[1], mt + 16);
-      w.add_rows(wf, la3, mt - st, sums[wave], bb[0], mt);
-      if (mt + 16 < end) {
-        if constexpr (BASE) w.load_base(bb[0], mt + 32);
-        w.add_rows(wf, la3, mt + 16 - st, sums[wave], bb[1], mt + 16);
-      }
+    w.load_base(bb[1], st + 16);
+    w.add_rows(wf, lds.la3, 0, lds.sums[wave], bb[0], st);
+    if (st + 16 < end) {
+      w.load_base(bb[0], st + 32);
+      w.add_rows(wf, lds.la3, 16, lds.sums[wave], bb[1], st + 16);
     }
   }
 }
-
-template <int KS, int NJ, typename T, int ROWS>
-static void launch_expand_rows(const ExpandArgs& p, hipStream_t s) {
-  const dim3 grid(tile_grid(p.seg, ROWS), (p.C + 64 * NJ - 1) / (64 * NJ));
-  if (p.base) hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, true, ROWS>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T, false, ROWS>), grid, dim3(256), 0, s, p);
+template <int KS, int NJ, typename T>
+__global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
+  __shared__ ExpandLds<KS, NJ, T> lds;
+  expand_block<KS, NJ, T>(p, blockIdx.x, blockIdx.y, lds);
 }
+
 // Tall tiles read the weights less often, short ones end sooner: the tallest
 // that still give every one of the 256 compute units two blocks.
-template <int KS, int NJ, typename T>
-static void launch_expand_k(const ExpandArgs& p, hipStream_t s) {
+static void expand_tiles(ExpandArgs& p, int NJ) {
   const int64_t columns = (p.C + 64 * NJ - 1) / (64 * NJ);
-  if (p.seg.M / 256 * columns >= 512) launch_expand_rows<KS, NJ, T, 256>(p, s);
-  else if (p.seg.M / 64 * columns >= 512) launch_expand_rows<KS, NJ, T, 64>(p, s);
-  else launch_expand_rows<KS, NJ, T, 16>(p, s);
+  p.rows = p.seg.M / 256 * columns >= 512 ? 256 : (p.seg.M / 64 * columns >= 512 ? 64 : 16);
+  p.blocks_x = (int)tile_grid(p.seg, p.rows);
+}
+template <int KS, int NJ, typename T>
+static void launch_expand_k(ExpandArgs p, hipStream_t s) {
+  expand_tiles(p, NJ);
+  hipLaunchKernelGGL((lora_expand_kernel<KS, NJ, T>), dim3(p.blocks_x, (p.C + 64 * NJ - 1) / (64 * NJ)), dim3(256), 0, s, p);
 }
 template <typename T>
 static void launch_expand_t(const ExpandArgs& p, hipStream_t s) {
@@ -592,7 +597,7 @@ static hipError_t launch_expand(const ExpandArgs& p, bool f32, hipStream_t s) {
 // that this saves is worth more than the weights of the shrink that the blocks
 // of other columns read again.
 // ---------------------------------------------------------------------------
-template <int RG, typename T, bool BASE>
+template <int RG, typename T>
 __global__ __launch_bounds__(1024) void lora_few_kernel(ShrinkArgs sp, ExpandArgs p) {
   constexpr int NW = 16, DX = RG == 1 ? 2 : 1, DW = DX;
   typedef ExpandWave<1, 8, T> Wave;
@@ -601,25 +606,23 @@ __global__ __launch_bounds__(1024) void lora_few_kernel(ShrinkArgs sp, ExpandArg
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Lds::bytes > SUMS ? Lds::bytes : SUMS];
   __shared__ u32x4 la3[3][4][16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const RowTile t = find_tile<16>(p.seg, blockIdx.x);
+  const RowTile t = find_tile(p.seg, blockIdx.x, 16);
   if (t.lo >= t.hi) return;
   const Wave w{p, t, ((int)blockIdx.y * NW + wave) * Wave::W, (int)threadIdx.x & 63};
   if (t.a < 0) {
     if (blockIdx.y == 0)
       for (int k = threadIdx.x; k < (t.hi - t.lo) * p.R; k += 64 * NW) sp.la[(int64_t)t.lo * p.R + k] = 0.f;
-    w.template copy_base<BASE>();
+    w.copy_base();
     return;
   }
   const float cs = p.scale ? p.scale[t.a] : 1.f;
   u32x4 b[Wave::NB];
-#pragma unroll
-  for (int q = 0; q < Wave::NB; ++q) b[q] = u32x4{0, 0, 0, 0};
   constexpr bool EARLY = RG == 1 || sizeof(T) == 2;   // rank 32 and float32: no registers for it yet
-  if constexpr (BASE && EARLY) w.load_base(b, t.lo);
+  if constexpr (EARLY) w.load_base(b, t.lo);
   v8bf wf[8][1];
   w.load_weights(wf);
   shrink_sums<RG, 1, NW, DX, DW>(sp, t, 0, lds);
-  if constexpr (BASE && !EARLY) w.load_base(b, t.lo);
+  if constexpr (!EARLY) w.load_base(b, t.lo);
   const v4f* red = reinterpret_cast<const v4f*>(lds);
   if (threadIdx.x < 128) {                         // 16 rows x 32 ranks, four ranks a thread
     const int rg = threadIdx.x >> 6, row = threadIdx.x & 15, r = 16 * rg + 4 * (threadIdx.x >> 4 & 3);
@@ -652,8 +655,7 @@ static bool few_rows(const LoraSegments& g, int R, int64_t N, int64_t K) {
 template <int RG, typename T>
 static void launch_few_t(const ShrinkArgs& a, const ExpandArgs& b, hipStream_t s) {
   const dim3 grid(tile_grid(b.seg, 16), (b.C + 2047) / 2048);
-  if (b.base) hipLaunchKernelGGL((lora_few_kernel<RG, T, true>), grid, dim3(1024), 0, s, a, b);
-  else hipLaunchKernelGGL((lora_few_kernel<RG, T, false>), grid, dim3(1024), 0, s, a, b);
+  hipLaunchKernelGGL((lora_few_kernel<RG, T>), grid, dim3(1024), 0, s, a, b);
 }
 static hipError_t launch_few(const ShrinkArgs& a, const ExpandArgs& b, bool f32, hipStream_t s) {
   if (a.R <= 16 && f32) launch_few_t<1, float>(a, b, s);
@@ -1142,7 +1144,7 @@ static hipError_t launch_join(const JoinArgs& up, const JoinArgs& down, int rot,
 // ---------------------------------------------------------------------------
 hipError_t launch_lora_forward(const LoraForward& p, hipStream_t s, int* kernels) {
   const ShrinkArgs a{p.x, p.ldx, p.down, p.seg, nullptr, p.la, nullptr, nullptr, 0, p.R, (int)p.K};
-  const ExpandArgs b{p.la, p.up, p.seg, p.scale, p.base, p.ldb, p.out, p.ldo, p.R, (int)p.N};
+  const ExpandArgs b{p.la, p.up, p.seg, p.scale, p.base, p.ldb, p.out, p.ldo, p.R, (int)p.N, 0, 0};
   const bool few = few_rows(p.seg, p.R, p.N, p.K);
   *kernels = few ? 1 : 2;
   if (few) return launch_few(a, b, p.out_f32 != 0, s);
@@ -1183,7 +1185,7 @@ hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kerne
     if ((e = launch_shrink(a, s)) != hipSuccess) return e;
   }
   if (p.dx) {
-    const ExpandArgs b{dla, down_t, p.seg, nullptr, p.dx_base, p.ldb, p.dx, p.lddx, p.R, K};
+    const ExpandArgs b{dla, down_t, p.seg, nullptr, p.dx_base, p.ldb, p.dx, p.lddx, p.R, K, 0, 0};
     ++*kernels;
     if ((e = launch_expand(b, p.dx_f32 != 0, s)) != hipSuccess) return e;
   }
