@@ -992,37 +992,62 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
   }
 }
 
-// both weight gradients in one launch: the first up.blocks blocks make d_up
-template <int RG, bool CODES>
-__global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs up, OuterArgs down) {
-  __shared__ v4f red[2][RG * 8 * 64];
-  const int b = blockIdx.x;
-  if (b < up.blocks) outer_block<RG, false, true>(up, b, red);
-  else outer_block<RG, CODES, false>(down, b - up.blocks, red);
+// Both weight gradients and dx in one launch: they need the same operands only,
+// and the products of the one keep the matrix cores busy while the other waits
+// for memory. The first up.blocks blocks make d_up, the next d_down, the rest dx.
+template <int RG, int KS, int NJ, bool CODES, typename T>
+__global__ __launch_bounds__(256) void lora_gradients_kernel(OuterArgs up, OuterArgs down, ExpandArgs dx) {
+  constexpr size_t A = sizeof(v4f) * 2 * RG * 8 * 64, B = sizeof(ExpandLds<KS, NJ, T>);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[A > B ? A : B];
+  auto red = reinterpret_cast<v4f(*)[RG * 8 * 64]>(lds);
+  int b = blockIdx.x;
+  if (b < up.blocks) return outer_block<RG, false, true>(up, b, red);
+  b -= up.blocks;
+  if (b < down.blocks) return outer_block<RG, CODES, false>(down, b, red);
+  b -= down.blocks;
+  expand_block<KS, NJ, T>(dx, b % dx.blocks_x, b / dx.blocks_x, *reinterpret_cast<ExpandLds<KS, NJ, T>*>(lds));
 }
 
 static int outer_blocks(const OuterArgs& p) {
   const int rb = p.R <= 16 ? 16 : (p.R <= 32 ? 32 : 64);
   return (p.C + 127) / 128 * ((p.R + rb - 1) / rb) * p.seg.A * p.P;
 }
-template <bool CODES>
-static hipError_t launch_outer(const OuterArgs& up, const OuterArgs& down, hipStream_t s) {
-  const dim3 grid(up.blocks + down.blocks);
-  const int R = up.blocks ? up.R : down.R;
-  if (R <= 16) hipLaunchKernelGGL((lora_outer_kernel<1, CODES>), grid, dim3(256), 0, s, up, down);
-  else if (R <= 32) hipLaunchKernelGGL((lora_outer_kernel<2, CODES>), grid, dim3(256), 0, s, up, down);
-  else hipLaunchKernelGGL((lora_outer_kernel<4, CODES>), grid, dim3(256), 0, s, up, down);
-  return hipGetLastError();
+// Above rank 32 a block of the weight gradients takes all registers of half a
+// compute unit, which is too few blocks for dx: many rows run better one after
+// the other (8192 rows of rank 64 from codes: 89 + 80 us against 181 us), few,
+// whose blocks all fit at once, better together.
+template <int RG, int KS, int NJ, bool CODES, typename T>
+static int launch_gradients_k(const OuterArgs& up, const OuterArgs& down, ExpandArgs dx, bool want_dx, hipStream_t s) {
+  unsigned blocks = up.blocks + down.blocks, more = 0;
+  bool apart = false;
+  if (want_dx) {
+    expand_tiles(dx, NJ);
+    more = (unsigned)dx.blocks_x * ((dx.C + 64 * NJ - 1) / (64 * NJ));
+    apart = RG == 4 && blocks + more > 512;
+  }
+  if (apart) launch_expand_k<KS, NJ, T>(dx, s);
+  else blocks += more;
+  hipLaunchKernelGGL((lora_gradients_kernel<RG, KS, NJ, CODES, T>), dim3(blocks), dim3(256), 0, s, up, down, dx);
+  return apart ? 2 : 1;
+}
+template <bool CODES, typename T>
+static int launch_gradients(const OuterArgs& up, const OuterArgs& down, const ExpandArgs& dx, bool want_dx, hipStream_t s) {
+  if (dx.R <= 16) return launch_gradients_k<1, 1, 8, CODES, T>(up, down, dx, want_dx, s);
+  if (dx.R <= 32) return launch_gradients_k<2, 1, 8, CODES, T>(up, down, dx, want_dx, s);
+  if (dx.R <= 64) return launch_gradients_k<4, 2, 8, CODES, T>(up, down, dx, want_dx, s);
+  return launch_gradients_k<4, 4, 4, CODES, T>(up, down, dx, want_dx, s);
 }
 
 // Parts an adapter's rows are split into: as many as keep both gradients' blocks
-// in one round on the GPU's 256 compute units, which hold two to four of them by
-// the registers of the rank (a block's
-// start and end cost as much as four of its steps: d_up of rank 64 and 4096
-// channels 28 us in 8 parts, 37 in 16), at least 128 rows each were the rows even.
+// in one round on the GPU's 256 compute units, at least 128 rows each were the
+// rows even. A block's start and end cost as much as four of its steps (d_up of
+// rank 64 and 4096 channels: 28 us in 8 parts, 37 in 16), and beside the blocks of
+// dx, which share the launch up to rank 32, fewer are better: 8192 rows of rank 16
+// with 512 blocks 75 us, with 1024 79 us; 1531 rows of rank 32 with 384 15.4 us, with 768
+// 16.2 us.
 static int outer_parts(int64_t M, int64_t N, int64_t K, int R, int A) {
   const int64_t blocks = ((N + 127) / 128 + (K + 127) / 128) * ((R + 63) / 64) * A;
-  int64_t P = (R <= 16 ? 1024 : (R <= 32 ? 768 : 512)) / blocks;
+  int64_t P = (R <= 16 ? 512 : (R <= 32 ? 384 : 512)) / blocks;
   const int64_t most = (M + 127) / 128;
   if (P > most) P = most;
   return P < 1 ? 1 : (int)P;
@@ -1184,12 +1209,11 @@ hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kerne
     ++*kernels;
     if ((e = launch_shrink(a, s)) != hipSuccess) return e;
   }
-  if (p.dx) {
-    const ExpandArgs b{dla, down_t, p.seg, nullptr, p.dx_base, p.ldb, p.dx, p.lddx, p.R, K, 0, 0};
+  const ExpandArgs ex{dla, down_t, p.seg, nullptr, p.dx_base, p.ldb, p.dx, p.lddx, p.R, K, 0, 0};
+  if (!p.d_up && !p.d_down) {
     ++*kernels;
-    if ((e = launch_expand(b, p.dx_f32 != 0, s)) != hipSuccess) return e;
+    return launch_expand(ex, p.dx_f32 != 0, s);
   }
-  if (!p.d_up && !p.d_down) return e;
   const int rot = codes && p.d_down ? p.rot_group : 0;
   const bool join_up = p.d_up && P > 1, join_down = p.d_down && (P > 1 || rot);
   OuterArgs up{la8, p.dy, p.lddy, p.seg, p.scale, join_up ? part_up : p.d_up, wn, P, !join_up && p.accumulate, p.R, N, 0};
@@ -1197,8 +1221,12 @@ hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kerne
                  p.R, K, 0};
   if (p.d_up) up.blocks = outer_blocks(up);
   if (p.d_down) down.blocks = outer_blocks(down);
-  ++*kernels;
-  if ((e = codes ? launch_outer<true>(up, down, s) : launch_outer<false>(up, down, s)) != hipSuccess) return e;
+  const bool want_dx = p.dx != nullptr, f32 = p.dx_f32 != 0;
+  if (codes && f32) *kernels += launch_gradients<true, float>(up, down, ex, want_dx, s);
+  else if (codes) *kernels += launch_gradients<true, uint16_t>(up, down, ex, want_dx, s);
+  else if (f32) *kernels += launch_gradients<false, float>(up, down, ex, want_dx, s);
+  else *kernels += launch_gradients<false, uint16_t>(up, down, ex, want_dx, s);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   if (join_up || join_down) {
     JoinArgs ju{part_up, P, wn, p.d_up, p.accumulate, 0}, jd{part_down, P, wk, p.d_down, p.accumulate, 0};
     if (join_up) ju.blocks = join_blocks(ju, 0);
