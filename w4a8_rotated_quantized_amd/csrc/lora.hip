@@ -1009,45 +1009,42 @@ __global__ __launch_bounds__(256) void lora_gradients_kernel(OuterArgs up, Outer
 }
 
 static int outer_blocks(const OuterArgs& p) {
-  const int rb = p.R <= 16 ? 16 : (p.R <= 32 ? 32 : 64);
+  const int rb = p.R <= 16 ? 16 : 32;
   return (p.C + 127) / 128 * ((p.R + rb - 1) / rb) * p.seg.A * p.P;
 }
-// Above rank 32 a block of the weight gradients takes all registers of half a
-// compute unit, which is too few blocks for dx: many rows run better one after
-// the other (8192 rows of rank 64 from codes: 89 + 80 us against 181 us), few,
-// whose blocks all fit at once, better together.
+// Ranks above 32 are made 32 at a time, each reading x or dy again (the second
+// time from the caches): the sums of 64 take all registers of half a compute unit,
+// too few blocks for dx beside them (8192 rows of rank 64 from codes: 160 us
+// together against 91 + 81 us of 64 ranks at a time and dx on its own).
 template <int RG, int KS, int NJ, bool CODES, typename T>
-static int launch_gradients_k(const OuterArgs& up, const OuterArgs& down, ExpandArgs dx, bool want_dx, hipStream_t s) {
-  unsigned blocks = up.blocks + down.blocks, more = 0;
-  bool apart = false;
+static void launch_gradients_k(const OuterArgs& up, const OuterArgs& down, ExpandArgs dx, bool want_dx, hipStream_t s) {
+  unsigned blocks = up.blocks + down.blocks;
   if (want_dx) {
     expand_tiles(dx, NJ);
-    more = (unsigned)dx.blocks_x * ((dx.C + 64 * NJ - 1) / (64 * NJ));
-    apart = RG == 4 && blocks + more > 512;
+    blocks += (unsigned)dx.blocks_x * ((dx.C + 64 * NJ - 1) / (64 * NJ));
   }
-  if (apart) launch_expand_k<KS, NJ, T>(dx, s);
-  else blocks += more;
   hipLaunchKernelGGL((lora_gradients_kernel<RG, KS, NJ, CODES, T>), dim3(blocks), dim3(256), 0, s, up, down, dx);
-  return apart ? 2 : 1;
 }
 template <bool CODES, typename T>
-static int launch_gradients(const OuterArgs& up, const OuterArgs& down, const ExpandArgs& dx, bool want_dx, hipStream_t s) {
-  if (dx.R <= 16) return launch_gradients_k<1, 1, 8, CODES, T>(up, down, dx, want_dx, s);
-  if (dx.R <= 32) return launch_gradients_k<2, 1, 8, CODES, T>(up, down, dx, want_dx, s);
-  if (dx.R <= 64) return launch_gradients_k<4, 2, 8, CODES, T>(up, down, dx, want_dx, s);
-  return launch_gradients_k<4, 4, 4, CODES, T>(up, down, dx, want_dx, s);
+static hipError_t launch_gradients(const OuterArgs& up, const OuterArgs& down, const ExpandArgs& dx, bool want_dx,
+                                   hipStream_t s) {
+  if (dx.R <= 16) launch_gradients_k<1, 1, 8, CODES, T>(up, down, dx, want_dx, s);
+  else if (dx.R <= 32) launch_gradients_k<2, 1, 8, CODES, T>(up, down, dx, want_dx, s);
+  else if (dx.R <= 64) launch_gradients_k<2, 2, 8, CODES, T>(up, down, dx, want_dx, s);
+  else launch_gradients_k<2, 4, 4, CODES, T>(up, down, dx, want_dx, s);
+  return hipGetLastError();
 }
 
 // Parts an adapter's rows are split into: as many as keep both gradients' blocks
 // in one round on the GPU's 256 compute units, at least 128 rows each were the
 // rows even. A block's start and end cost as much as four of its steps (d_up of
-// rank 64 and 4096 channels: 28 us in 8 parts, 37 in 16), and beside the blocks of
-// dx, which share the launch up to rank 32, fewer are better: 8192 rows of rank 16
-// with 512 blocks 75 us, with 1024 79 us; 1531 rows of rank 32 with 384 15.4 us, with 768
-// 16.2 us.
+// rank 64 and 4096 channels: 28 us in 8 parts, 37 in 16), and the blocks of dx share
+// the launch: 8192 rows of rank 16 with 512 blocks 75 us, with 1024 79 us; 1531 rows of
+// rank 32 with 384 15.4 us, with 768 16.2 us; 8192 rows of rank 64 from codes with 384 160
+// us, with 768 169 us.
 static int outer_parts(int64_t M, int64_t N, int64_t K, int R, int A) {
-  const int64_t blocks = ((N + 127) / 128 + (K + 127) / 128) * ((R + 63) / 64) * A;
-  int64_t P = (R <= 16 ? 512 : (R <= 32 ? 384 : 512)) / blocks;
+  const int64_t blocks = ((N + 127) / 128 + (K + 127) / 128) * ((R + 31) / 32) * A;
+  int64_t P = (R <= 16 ? 512 : 384) / blocks;
   const int64_t most = (M + 127) / 128;
   if (P > most) P = most;
   return P < 1 ? 1 : (int)P;
@@ -1222,11 +1219,12 @@ hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kerne
   if (p.d_up) up.blocks = outer_blocks(up);
   if (p.d_down) down.blocks = outer_blocks(down);
   const bool want_dx = p.dx != nullptr, f32 = p.dx_f32 != 0;
-  if (codes && f32) *kernels += launch_gradients<true, float>(up, down, ex, want_dx, s);
-  else if (codes) *kernels += launch_gradients<true, uint16_t>(up, down, ex, want_dx, s);
-  else if (f32) *kernels += launch_gradients<false, float>(up, down, ex, want_dx, s);
-  else *kernels += launch_gradients<false, uint16_t>(up, down, ex, want_dx, s);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  ++*kernels;
+  if (codes && f32) e = launch_gradients<true, float>(up, down, ex, want_dx, s);
+  else if (codes) e = launch_gradients<true, uint16_t>(up, down, ex, want_dx, s);
+  else if (f32) e = launch_gradients<false, float>(up, down, ex, want_dx, s);
+  else e = launch_gradients<false, uint16_t>(up, down, ex, want_dx, s);
+  if (e != hipSuccess) return e;
   if (join_up || join_down) {
     JoinArgs ju{part_up, P, wn, p.d_up, p.accumulate, 0}, jd{part_down, P, wk, p.d_down, p.accumulate, 0};
     if (join_up) ju.blocks = join_blocks(ju, 0);
