@@ -347,7 +347,9 @@ static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
   const int rg = (p.R + 15) / 16;
   const unsigned t16 = tile_grid(p.seg, 16), t32 = tile_grid(p.seg, 32);
   const bool many = p.seg.M >= 32 * 256;           // 32-row tiles for every one of the 256 compute units
-  if (p.seg.M <= 256) hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 2, 2>), dim3(t16, rg), dim3(1024), 0, s, p);
+  // 16 ranks a block while every compute unit gets at most one: more of them take part (64 single
+  // rows of rank 64, K = 4096: 3 us less than 64 ranks a block; 256, which make 1024 blocks, 10 us more)
+  if (t16 * rg <= 256) hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 2, 2>), dim3(t16, rg), dim3(1024), 0, s, p);
   else if (rg <= 1) hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 8, 3, 2>), dim3(t16), dim3(512), 0, s, p);
   else if (rg <= 2 && !many) hipLaunchKernelGGL((lora_shrink_kernel<2, 1, 8, 2, 2>), dim3(t16), dim3(512), 0, s, p);
   else if (rg <= 2) hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 5, 2, 2>), dim3(t32), dim3(320), 0, s, p);
