@@ -143,6 +143,35 @@ def test_forward(cr, shape, f32):
     assert not out0[dev(none)].any()
 
 
+# Enough rows for the tall tiles and the wide shrink blocks of each rank
+TALL = [(8200, 8200, 72, 64, 2, 5, "ragged"), (8200, 2056, 200, 24, 2, 5, "gaps"), (8209, 2056, 136, 128, 3, 9, "ragged"),
+        (8300, 520, 264, 16, 2, 70, "ragged")]
+
+
+@pytest.mark.parametrize("shape", TALL)
+def test_forward_many_rows(cr, shape):
+    say(f"lora forward {shape}")
+    t = Case(*shape[:6], mix=shape[6])
+    base_d, base = t.base(t.N, False)
+    want, la_want = oa.lora_forward(t.x, t.down, t.up, t.off, t.ids, t.c, base)
+    out, la = t.fwd(cr, base=base_d)
+    e1, e2 = t.two_products(t.x, t.down, t.up, base, want, False)
+    _near(la, la_want, e1, "lora_act")
+    _near(out, want, e2, "out")
+
+
+def test_no_row_has_an_adapter(cr):
+    t = Case(70, 136, 264, 16, 3, 4, seed=23)
+    base_d, _ = t.base(t.N, False)
+    la = dev(t.g.standard_normal((t.M, t.R)).astype(np.float32))
+    for off, ids in (([0, 20, 20, 50, 70], [-1, 0, 3, -7]), ([0, 0, 0, 0, 0], [0, 1, 2, 0]), ([70, 70, 70, 70, 70], [0, 1, 2, 0])):
+        t.off_d, t.ids_d = dev(np.int32(off)), dev(np.int32(ids))
+        out, la1 = t.fwd(cr, base=base_d)
+        assert torch.equal(out, base_d) and not la1.any()
+        dx, dd, du = t.bwd(cr, la)
+        assert not dx.any() and not dd.any() and not du.any()
+
+
 def test_forward_without_scale_and_with_strided_rows(cr):
     t = Case(77, 264, 136, 24, 3, 6, seed=3, scale=False)
     want, la_want = oa.lora_forward(t.x, t.down, t.up, t.off, t.ids)
@@ -212,6 +241,12 @@ def _weight_bounds(t, dla_err, la, dla, x_abs, dy_abs):
         bd[a] = (dla_err[at] + (n + 2) * U2 * np.abs(dla[at])).T @ x_abs[at]
         bu[a] = abs(t.c64[a]) * (n + 2) * U2 * (dy_abs[at].T @ np.abs(la[at]))
     return bd + 1e-37, bu + 1e-37
+
+
+@pytest.mark.parametrize("shape", [(8200, 264, 2056, 64, 2, 5, "ragged"), (8201, 136, 520, 16, 3, 7, "gaps"),
+                                   (8200, 72, 8200, 32, 2, 70, "ragged")])
+def test_backward_many_rows(cr, shape):
+    test_backward(cr, shape, False)
 
 
 @pytest.mark.parametrize("f32", [False, True])

@@ -595,9 +595,7 @@ static hipError_t launch_expand(const ExpandArgs& p, bool f32, hipStream_t s) {
 
 // ---------------------------------------------------------------------------
 // Both in one launch, for few rows: a block takes 16 rows of one segment and
-// 2048 columns of out and makes lora_act of the rows for itself. The launch
-// that this saves is worth more than the weights of the shrink that the blocks
-// of other columns read again.
+// 2048 columns of out and makes lora_act of the rows for itself (see few_rows).
 // ---------------------------------------------------------------------------
 template <int RG, typename T>
 __global__ __launch_bounds__(1024) void lora_few_kernel(ShrinkArgs sp, ExpandArgs p) {
@@ -650,7 +648,11 @@ __global__ __launch_bounds__(1024) void lora_few_kernel(ShrinkArgs sp, ExpandArg
 }
 
 // Rows x column groups x weights of the shrink: what the blocks read of it, at
-// most 64 MB (64 rows of 64 requests, rank 32, 4096 x 4096: 2 x 16.8 MB).
+// most 64 MB. There both ways take the same time on the GPU (64 rows of rank 32,
+// 8192 x 8192: 20.4 and 20.6 us with the launch) and one launch less on the host
+// (12 against 15.5 us); below, one launch is 1 to 2.5 us shorter (128 rows of rank 16,
+// 4096 x 4096: 16.4 against 18.9 us), above, two are (64 rows of rank 32, 12288 x
+// 12288: 26.6 against 38.5 us).
 static bool few_rows(const LoraSegments& g, int R, int64_t N, int64_t K) {
   return R <= 32 && g.M <= 256 && g.M * ((N + 2047) / 2048) * R * K <= ((int64_t)1 << 25);
 }
