@@ -349,7 +349,9 @@ static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
   const bool many = p.seg.M >= 32 * 256;           // 32-row tiles for every one of the 256 compute units
   // 16 ranks a block while every compute unit gets at most one: more of them take part (64 single
   // rows of rank 64, K = 4096: 3 us less than 64 ranks a block; 256, which make 1024 blocks, 10 us more)
+  // (32 ranks a block by the same rule: 1631 rows of rank 64, K = 6768: 15.8 against 20.2 us)
   if (t16 * rg <= 256) hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, 2, 2>), dim3(t16, rg), dim3(1024), 0, s, p);
+  else if (t16 * ((rg + 1) / 2) <= 256) hipLaunchKernelGGL((lora_shrink_kernel<2, 1, 8, 2, 2>), dim3(t16, (rg + 1) / 2), dim3(512), 0, s, p);
   else if (rg <= 1) hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 8, 3, 2>), dim3(t16), dim3(512), 0, s, p);
   else if (rg <= 2 && !many) hipLaunchKernelGGL((lora_shrink_kernel<2, 1, 8, 2, 2>), dim3(t16), dim3(512), 0, s, p);
   else if (rg <= 2) hipLaunchKernelGGL((lora_shrink_kernel<2, 2, 5, 2, 2>), dim3(t32), dim3(320), 0, s, p);
@@ -683,6 +685,7 @@ struct PrepareArgs {
   uint16_t* la8;
   int M, N, K, R, A;
   int up_blocks, down_blocks;
+  LoraSegments seg;
 };
 
 // rows x cols (at most 64 x 128 or 128 x 64, multiples of 8) of `in` transposed into `out`
@@ -711,9 +714,20 @@ CR_DEV void transpose_tile(const uint16_t* in, int64_t ldi, uint16_t* out, int64
 __global__ __launch_bounds__(256) void lora_prepare_kernel(PrepareArgs p) {
   __shared__ uint16_t lds[128 * 66 > 64 * 130 ? 128 * 66 : 64 * 130];
   int b = blockIdx.x;
+  // with more adapters than segments some have no rows, and nothing reads theirs (2 rows, 25 adapters
+  // of rank 128, N = 4480: 6.2 against 12.6 us)
+  auto unused = [&](int a) {
+    if (p.A <= p.seg.S) return false;
+    for (int s = 0; s < p.seg.S; s += 64) {
+      const int v = s + (threadIdx.x & 63);
+      if (__ballot(v < p.seg.S && seg_adapter(p.seg, v + 1) == a)) return false;
+    }
+    return true;
+  };
   if (b < p.up_blocks) {                           // 64 channels and all ranks of one adapter
     const int per = (p.N + 63) / 64;
     const int a = b / per, n0 = b % per * 64;
+    if (unused(a)) return;
     const int n = p.N - n0 < 64 ? p.N - n0 : 64;
     transpose_tile(p.up + ((int64_t)a * p.N + n0) * p.R, p.R, p.up_t + (int64_t)a * p.R * p.N + n0, p.N, n, p.R, lds);
     return;
@@ -722,6 +736,7 @@ __global__ __launch_bounds__(256) void lora_prepare_kernel(PrepareArgs p) {
   if (b < p.down_blocks) {
     const int per = (p.K + 63) / 64;
     const int a = b / per, k0 = b % per * 64;
+    if (unused(a)) return;
     const int n = p.K - k0 < 64 ? p.K - k0 : 64;
     transpose_tile(p.down + (int64_t)a * p.R * p.K + k0, p.K, p.down_t + ((int64_t)a * p.K + k0) * p.R, p.R, p.R, n, lds);
     return;
@@ -909,35 +924,74 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
         for (int rg = 0; rg < RG; ++rg) acc[rg][j] = mfma16(__builtin_bit_cast(v8bf, uf[rg][q]), vf, acc[rg][j]);
     }
   };
-  int turn = 0;                                    // steps so far, over all segments
-  int64_t before = 0;
-  for (int s0 = 0; s0 < p.seg.S; s0 += 64) {
-    if (s0 > 0) segments(s0);
-    for (uint64_t left = __ballot(len > 0); left; left &= left - 1) {
-      const int src = __builtin_ctzll(left);
-      const int slo = __builtin_amdgcn_readlane(lo, src), slen = __builtin_amdgcn_readlane(len, src);
+  // The wave's steps: every fourth of the adapter's, over all runs of rows. A run
+  // is one segment of the adapter or several that follow one another, as single
+  // rows of one adapter do (95 segments, all but one a row, in 4771 rows of rank 24
+  // and one adapter, N = 608: 22 us for the launch against 50 a segment at a time).
+  int s0 = 0, turn = 0;                            // turn: steps so far
+  int64_t before = 0;                              // rows of the adapter so far
+  uint64_t left = __ballot(len > 0);
+  int mlo = 0, mhi = 0, m00 = 0, count = 0, k = 0;
+  auto advance = [&]() {                           // false behind the last step
+    k += 4;
+    while (k >= count) {
+      while (left == 0) {
+        s0 += 64;
+        if (s0 >= p.seg.S) return false;
+        segments(s0);
+        left = __ballot(len > 0);
+      }
+      int src = __builtin_ctzll(left);
+      const int slo = __builtin_amdgcn_readlane(lo, src);
+      int slen = __builtin_amdgcn_readlane(len, src);
+      for (left &= left - 1; left; left &= left - 1) {
+        src = __builtin_ctzll(left);
+        if (__builtin_amdgcn_readlane(lo, src) != slo + slen) break;
+        slen += __builtin_amdgcn_readlane(len, src);
+      }
       const int64_t x0 = from > before ? from - before : 0;
       const int64_t x1 = to - before < slen ? to - before : slen;
       before += slen;
+      count = k = 0;
       if (x1 <= x0) continue;
-      const int mlo = slo + (int)x0, mhi = slo + (int)x1;
-      const int m00 = mlo & ~31, count = (mhi - m00 + 31) >> 5;
-      int k = (wave - turn) & 3;                   // this wave's steps: k, k + 4, ...
+      mlo = slo + (int)x0;
+      mhi = slo + (int)x1;
+      m00 = mlo & ~31;
+      count = (mhi - m00 + 31) >> 5;
+      k = (wave - turn) & 3;
       turn += count;
-      if (k >= count) continue;
-      wait_vmcnt<0>();                             // the last segment's loads for nothing
-      load_u(m00 + 32 * k);
-      load_v(next, m00 + 32 * k);
-      // one copy of the step's code: a block runs it a few times only, and fetching it counts
-#pragma unroll 1
-      for (; k < count; k += 4)
-        step(m00 + 32 * k, m00 + 32 * (k + 4 < count ? k + 4 : k), mlo, mhi);   // behind the last: itself, for nothing
     }
+    return true;
+  };
+  bool more = advance();
+  if (more) {
+    load_u(m00 + 32 * k);
+    load_v(next, m00 + 32 * k);
+  }
+  // one copy of the step's code: a block runs it a few times only, and fetching it counts
+#pragma unroll 1
+  while (more) {
+    const int m0 = m00 + 32 * k, from_row = mlo, to_row = mhi;
+    more = advance();
+    step(m0, more ? m00 + 32 * k : m0, from_row, to_row);   // behind the last: itself, for nothing
+  }
+  float* out = p.out + part * p.part + (int64_t)a * p.R * p.C;
+  const int cb = c - 8 * i;
+  if (turn == 0) {                                 // no rows: zeros, or what was there
+    if (p.accumulate) return;
+    const int line = UP ? 4 * RG : 32;
+#pragma unroll 1
+    for (int k = threadIdx.x; k < 16 * RG * 32; k += 256) {
+      const int cc = cb + (UP ? k / line : 4 * (k % line)), r = r0 + (UP ? 4 * (k % line) : k / line);
+      if (cc < p.C && r < p.R)
+        *reinterpret_cast<v4f*>(out + (UP ? (int64_t)cc * p.R + r : (int64_t)r * p.C + cc)) = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    return;
   }
   wait_vmcnt<0>();
   __syncthreads();                                 // every wave's u has arrived and been read
 #pragma unroll 1
-  for (int n = 2; n >= 1; n >>= 1) {
+  for (int n = turn > 2 ? 2 : turn > 1 ? 1 : 0; n >= 1; n >>= 1) {   // waves that had no step hold zeros
     if (wave >= n && wave < 2 * n) {
 #pragma unroll
       for (int rg = 0; rg < RG; ++rg)
@@ -979,8 +1033,6 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
     }
   }
   __syncthreads();
-  float* out = p.out + part * p.part + (int64_t)a * p.R * p.C;
-  const int cb = c - 8 * i;
 #pragma unroll 1
   for (int k = threadIdx.x; k < 16 * RG * 32; k += 256) {
     const int row = k / LINE, at = k % LINE;
@@ -1070,10 +1122,16 @@ CR_DEV void join_block(const JoinArgs& p, int b) {
   const int64_t k = ((int64_t)b * 256 + threadIdx.x) * 4;
   if (k >= p.n) return;
   v4f s = *reinterpret_cast<const v4f*>(p.part + k);
-  for (int q = 1; q < p.P; ++q) {
-    const v4f o = *reinterpret_cast<const v4f*>(p.part + q * p.n + k);
+  for (int q = 1; q < p.P; q += 8) {               // eight parts on their way at once (38 parts: 4.4 against 11.6 us)
+    v4f w[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] += o[e];
+    for (int i = 0; i < 8; ++i)
+      w[i] = *reinterpret_cast<const v4f*>(p.part + (q + i < p.P ? q + i : q) * p.n + k);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (q + i < p.P)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += w[i][e];
   }
   v4f* o = reinterpret_cast<v4f*>(p.out + k);
   if (p.accumulate) {
@@ -1101,14 +1159,22 @@ CR_DEV void join_rotate_block(const JoinArgs& p, int b) {
     const float* src = p.part + k0 + 256 * g;
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
-      v4f s = *reinterpret_cast<const v4f*>(src + e);
-      for (int q = 1; q < p.P; ++q) {
-        const v4f o = *reinterpret_cast<const v4f*>(src + q * p.n + e);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[x] += o[x];
-      }
+      const v4f s = *reinterpret_cast<const v4f*>(src + e);
 #pragma unroll
       for (int x = 0; x < 4; ++x) v[g][e + x] = s[x];
+    }
+    for (int q = 1; q < p.P; q += 4) {
+      v4f w[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[i][e] = *reinterpret_cast<const v4f*>(src + (q + i < p.P ? q + i : q) * p.n + 4 * e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (q + i < p.P)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[g][e] += w[i][e >> 2][e & 3];
     }
     const bool cneg = NR == 1024 && chunk_neg(g);
 #pragma unroll
@@ -1202,7 +1268,7 @@ hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kerne
   hipError_t e = hipSuccess;
   *kernels = 1;
   const PrepareArgs pre{dla_wanted ? p.up : nullptr, up_t, p.dx ? p.down : nullptr, down_t,
-                        p.d_up ? p.la : nullptr, la8, M, N, K, p.R, A, 0, 0};
+                        p.d_up ? p.la : nullptr, la8, M, N, K, p.R, A, 0, 0, p.seg};
   if ((e = launch_prepare(pre, s)) != hipSuccess) return e;
   if (dla_wanted) {
     const ShrinkArgs a{p.dy, p.lddy, up_t, p.seg, p.scale, dla, p.d_down ? dla8 : nullptr,
