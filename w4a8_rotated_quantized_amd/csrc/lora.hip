@@ -346,7 +346,9 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
 static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
   const int rg = (p.R + 15) / 16;
   const unsigned t16 = tile_grid(p.seg, 16), t32 = tile_grid(p.seg, 32);
-  const bool many = p.seg.M >= 32 * 256;           // 32-row tiles for every one of the 256 compute units
+  // 32-row tiles where they make a block for every one of the 256 compute units (rank 128, 7569 rows,
+  // K = 952: 12.8 against 14.9 us in 16-row tiles)
+  const bool many = p.seg.M / 32 * ((rg + 3) / 4) >= 256;
   // 16 ranks a block while every compute unit gets at most one: more of them take part (64 single
   // rows of rank 64, K = 4096: 3 us less than 64 ranks a block; 256, which make 1024 blocks, 10 us more)
   // (32 ranks a block by the same rule: 1631 rows of rank 64, K = 6768: 15.8 against 20.2 us)
