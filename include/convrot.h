@@ -544,7 +544,9 @@ cr_status int8_tensorwise_gemm(const void* a_codes, const float* a_scale,
  *   carried as three bf16 terms); out and dx are rounded once. Results do not
  *   depend on timing (no atomics), and a row's result does not depend on the
  *   values of other rows (infinities and NaN stay in their row; in the weight
- *   gradients they stay in their adapter).
+ *   gradients they stay in their adapter). The order of a float32 sum is fixed
+ *   for a call's sizes and segments; another batch around the same rows may
+ *   change its last bits.
  *
  *   x            bf16 [M, K], leading dimension ldx; backward: the same, or the
  *                INT8 codes that convrot_rotate_quantize made of it (SYM_INT8,
@@ -568,7 +570,8 @@ cr_status int8_tensorwise_gemm(const void* a_codes, const float* a_scale,
  *   scale        optional float32 [A] (NULL: 1)
  *   base         optional, of out's type, leading dimension ldb (NULL: 0). It may
  *                be out itself (ldb == ldo): then rows without adapter are left
- *                as they are. Any other overlap is not allowed. dx_base likewise.
+ *                as they are. dx_base likewise. Outputs must not overlap
+ *                inputs or each other in any other way.
  *   out, dx      CR_OUT_BF16 or CR_OUT_F32
  *   lora_act     float32 [M, R] (written by the forward, read by the backward)
  *   dx, d_down, d_up   each may be NULL if not wanted, not all of them; x may be
@@ -618,7 +621,8 @@ cr_status convrot_lora_backward(const void* dy, int64_t lddy, const float* lora_
  *   forward   y = act(z) of z itself, rounded once
  *   backward  dz = dy act'(scale * code), rounded once
  * Shape: rows >= 1, C % 64 == 0, C <= 32768, rows C < 2^34, leading dimensions
- * multiples of 8, not below the row length and below 2^31. One launch each.
+ * multiples of 8, not below the row length and below 2^31. Outputs must not
+ * overlap inputs or each other. One launch each.
  */
 typedef enum cr_act {
   CR_ACT_GELU = 0,

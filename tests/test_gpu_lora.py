@@ -249,6 +249,13 @@ def test_backward_many_rows(cr, shape):
     test_backward(cr, shape, False)
 
 
+@pytest.mark.parametrize("shape", [(1500, 72, 136, 24, 1, 95, "prompt"), (2600, 40, 264, 16, 2, 150, "prompt"),
+                                   (4200, 8, 8, 8, 1, 700, "ragged"), (70, 136, 264, 32, 90, 2, "ragged"),
+                                   (3, 520, 72, 128, 70, 2, "tokens")])
+def test_backward_many_segments_or_adapters(cr, shape):
+    test_backward(cr, shape, True)
+
+
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("shape", SHAPES)
 def test_backward(cr, shape, f32):
@@ -307,6 +314,44 @@ def test_backward_from_codes(cr, shape, rot, tensor):
     bd = np.broadcast_to(g, (t.A, t.R, g.shape[2], rot)).reshape(bd.shape)
     _near(dd, dd_w, bd, "d_down")
     _near(du, du_w, bu, "d_up")
+
+
+@pytest.mark.parametrize("rot", [64, 1024])
+@pytest.mark.parametrize("shape", [(3000, 40, 1024, 16, 1, 2, "ragged"), (40, 72, 1024, 40, 9, 3, "ragged")])
+def test_backward_from_codes_many_parts_or_adapters(cr, shape, rot):
+    test_backward_from_codes(cr, shape, rot, False)
+
+
+def test_adapters_without_rows(cr):
+    """Their gradients are zeros whatever their weights and factors hold, or stay what they were."""
+    t = Case(37, 136, 256, 24, 8, 2, seed=10)
+    t.ids_d.fill_(5)
+    la = dev(t.g.standard_normal((t.M, t.R)).astype(np.float32))
+    codes, scales, _, _ = cr.convrot_rotate_quantize(t.x_d, 256, cr.Q.SYM_INT8, cr.GRAN.ROW)
+    others = [a for a in range(t.A) if a != 5]
+    want = [t.bwd(cr, la, **k) for k in ({}, {"x": codes, "x_scales": scales})]
+    for v in (t.down_d, t.up_d, t.c_d):
+        v[others] = math.inf
+    for k, w in zip(({}, {"x": codes, "x_scales": scales}), want):
+        got = t.bwd(cr, la, **k)
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
+        for d in got[1:]:
+            assert not d[others].any() and d[5].any()
+        a, b = torch.randn_like(got[1]), torch.randn_like(got[2])
+        _, dd, du = t.bwd(cr, la, d_down=a.clone(), d_up=b.clone(), accumulate=True, **k)
+        assert torch.equal(dd, a + got[1]) and torch.equal(du, b + got[2])
+
+
+def test_descending_offsets_end_and_stay_inside(cr):
+    """What they name more than once is unspecified; rows and adapters they do not name are not."""
+    t = Case(64, 72, 64, 8, 3, 300, seed=12)
+    off = np.zeros(301, np.int32)
+    off[1::2] = 48
+    off_d, ids_d = dev(off), dev(np.zeros(300, np.int32))
+    la = torch.zeros((t.M, t.R), dtype=torch.float32, device=DEV)
+    dx, dd, du = cr.convrot_lora_backward(t.dy_d, la, t.x_d, t.down_d, t.up_d, off_d, ids_d)
+    torch.cuda.synchronize()
+    assert dx.shape == (t.M, t.K) and not dd[1:].any() and not du.any()
 
 
 def test_accumulate(cr):

@@ -951,6 +951,8 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
         if (__builtin_amdgcn_readlane(lo, src) != slo + slen) break;
         slen += __builtin_amdgcn_readlane(len, src);
       }
+      // descending offsets could name rows more often than there are
+      if (slen > p.seg.M - before) slen = (int)(p.seg.M - before);
       const int64_t x0 = from > before ? from - before : 0;
       const int64_t x1 = to - before < slen ? to - before : slen;
       before += slen;
