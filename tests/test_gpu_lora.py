@@ -503,6 +503,17 @@ def test_counters(cr):
         assert c["lora"] == launches and c["fallbacks"] == 0
 
 
+def test_counters_of_the_backward(cr):
+    # dla with what is laid out anew, gradients; or layout, dla, gradients, and the parts' sum
+    for M, R, launches in ((20, 32, 2), (300, 32, 3), (300, 40, 4)):
+        t = Case(M, 72, 64, R, 2, 3)
+        la = torch.zeros((M, R), dtype=torch.float32, device=DEV)
+        cr.reset_counters()
+        t.bwd(cr, la)
+        c = cr.get_counters()
+        assert c["lora"] == launches and c["fallbacks"] == 0
+
+
 def test_refusals(cr):
     t = Case(20, 72, 64, 8, 2, 3)
     ok = (t.x_d, t.down_d, t.up_d, t.off_d, t.ids_d)

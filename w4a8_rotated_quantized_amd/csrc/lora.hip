@@ -196,8 +196,15 @@ struct ShrinkLds {
 // spreads the fragment reads over the banks. 8192 rows, 4096 columns: 23.4 us at
 // rank 16 (2.9 TB/s of x), 38 us at rank 64, where the weights, read from L2 for
 // every 32 rows, are twice the bytes of x.
-template <int RG, int TM, int NW, int DX, int DW>
-CR_DEV void shrink_sums(const ShrinkArgs& p, const RowTile& t, int r0, uint8_t* lds) {
+//
+// WT: the weights lie the other way, [A][C][R]. A load then takes the 16 ranks of
+// 32 columns, two lanes a column, and a fragment is gathered two bytes at a
+// time; column 8 g + e of the load lies at position 8 g + (e + 2 g) % 8, which
+// spreads these reads over the banks. Four times the LDS reads, so it is for few
+// rows only, where a launch that transposes first costs more.
+template <int RG, int TM, int NW, int DX, int DW, bool WT>
+CR_DEV void shrink_sums(const ShrinkArgs& p, const RowTile& t, int r0, int bx, uint8_t* lds) {
+  static_assert(!WT || RG == 1, "a load holds the ranks of one group");
   typedef ShrinkLds<RG, TM, NW, DX, DW> L;
   constexpr int NX = L::nx, NWT = L::nw, RED = L::red;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -212,15 +219,21 @@ CR_DEV void shrink_sums(const ShrinkArgs& p, const RowTile& t, int r0, uint8_t* 
   }
 #pragma unroll
   for (int n = 0; n < NWT; ++n) {
-    const int r = r0 + 8 * n + lr;
-    wr[n] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C;
+    if constexpr (WT) {
+      const int r = r0 + 8 * (lane & 1);
+      wr[n] = p.w + (int64_t)t.a * p.C * p.R + (r < p.R ? r : 0);
+    } else {
+      const int r = r0 + 8 * n + lr;
+      wr[n] = p.w + ((int64_t)t.a * p.R + (r < p.R ? r : p.R - 1)) * p.C;
+    }
   }
+  const int wc = (lane >> 4) * 8 + (((lane >> 1) - 2 * (lane >> 4)) & 7);   // WT: the lane's column of a load
   uint8_t* xring = lds + wave * ShrinkLds<RG, TM, NW, DX, DW>::ring;
   uint8_t* wring = xring + DX * NX * 1024;
   const int stages = ((p.C + 63) / 64 - wave + NW - 1) / NW;   // may be 0
   // blocks start at different columns: rows a power of two apart share an L2 channel
   // (rank 64, K = 4096: 21 against 29 us from the cache)
-  const int first = stages ? blockIdx.x % stages : 0;
+  const int first = stages ? bx % stages : 0;
   auto column = [&](int s) { s += first; return ((s < stages ? s : s - stages) * NW + wave) * 64; };
   auto lane_column = [&](int s) {
     const int c = column(s) + lc;
@@ -233,10 +246,15 @@ CR_DEV void shrink_sums(const ShrinkArgs& p, const RowTile& t, int r0, uint8_t* 
       __builtin_amdgcn_global_load_lds((lora_gptr)(xr[n] + c), (lora_lptr)(xring + (slot * NX + n) * 1024), 16, 0, 0);
   };
   auto load_w = [&](int s, int slot) {
-    const int c = lane_column(s);
 #pragma unroll
-    for (int n = 0; n < NWT; ++n)
-      __builtin_amdgcn_global_load_lds((lora_gptr)(wr[n] + c), (lora_lptr)(wring + (slot * NWT + n) * 1024), 16, 0, 0);
+    for (int n = 0; n < NWT; ++n) {
+      int64_t at = lane_column(s);
+      if constexpr (WT) {
+        const int c = column(s) + 32 * n + wc;
+        at = (int64_t)(c < p.C ? c : 0) * p.R;
+      }
+      __builtin_amdgcn_global_load_lds((lora_gptr)(wr[n] + at), (lora_lptr)(wring + (slot * NWT + n) * 1024), 16, 0, 0);
+    }
   };
   v4f acc[RG][TM];
 #pragma unroll
@@ -266,8 +284,17 @@ CR_DEV void shrink_sums(const ShrinkArgs& p, const RowTile& t, int r0, uint8_t* 
       for (int tm = 0; tm < TM; ++tm)
         xf[tm][h] = *reinterpret_cast<const u32x4*>(xring + (xs * NX + 2 * tm) * 1024 + at + ((4 * h + g) ^ sw) * 16);
 #pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
-        wf[rg][h] = *reinterpret_cast<const u32x4*>(wring + (ws * NWT + 2 * rg) * 1024 + at + ((4 * h + g) ^ sw) * 16);
+      for (int rg = 0; rg < RG; ++rg) {
+        if constexpr (WT) {
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(wring + (ws * NWT + h) * 1024) + i;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            wf[rg][h][k] = (uint32_t)src[(8 * g + ((2 * k + 2 * g) & 7)) * 16] |
+                           ((uint32_t)src[(8 * g + ((2 * k + 1 + 2 * g) & 7)) * 16] << 16);
+        } else {
+          wf[rg][h] = *reinterpret_cast<const u32x4*>(wring + (ws * NWT + 2 * rg) * 1024 + at + ((4 * h + g) ^ sw) * 16);
+        }
+      }
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): read before the slots are filled again
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -305,12 +332,11 @@ CR_DEV void shrink_sums(const ShrinkArgs& p, const RowTile& t, int r0, uint8_t* 
 }
 
 // a block: TM x 16 rows of one segment and 16 RG ranks
-template <int RG, int TM, int NW, int DX, int DW>
-__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
+template <int RG, int TM, int NW, int DX, int DW, bool WT>
+CR_DEV void shrink_block(const ShrinkArgs& p, int bx, int by, uint8_t* lds) {
   constexpr int RED = ShrinkLds<RG, TM, NW, DX, DW>::red;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[ShrinkLds<RG, TM, NW, DX, DW>::bytes];
-  const int r0 = blockIdx.y * 16 * RG;
-  const RowTile t = find_tile(p.seg, blockIdx.x, 16 * TM);
+  const int r0 = by * 16 * RG;
+  const RowTile t = find_tile(p.seg, bx, 16 * TM);
   if (t.lo >= t.hi) return;
   if (t.a < 0) {                                  // rows without adapter: zeros
     const int nr = p.R - r0 < 16 * RG ? p.R - r0 : 16 * RG;
@@ -318,7 +344,7 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
       p.la[(int64_t)(t.lo + k / nr) * p.R + r0 + k % nr] = 0.f;
     return;
   }
-  shrink_sums<RG, TM, NW, DX, DW>(p, t, r0, lds);
+  shrink_sums<RG, TM, NW, DX, DW, WT>(p, t, r0, bx, lds);
   const v4f* red = reinterpret_cast<const v4f*>(lds);
   const float cs = p.scale ? p.scale[t.a] : 1.f;
   for (int k = threadIdx.x; k < RED; k += 64 * NW) {
@@ -343,6 +369,12 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
       }
     }
   }
+}
+
+template <int RG, int TM, int NW, int DX, int DW>
+__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(ShrinkArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ShrinkLds<RG, TM, NW, DX, DW>::bytes];
+  shrink_block<RG, TM, NW, DX, DW, false>(p, blockIdx.x, blockIdx.y, lds);
 }
 
 static hipError_t launch_shrink(const ShrinkArgs& p, hipStream_t s) {
@@ -630,7 +662,7 @@ __global__ __launch_bounds__(1024) void lora_few_kernel(ShrinkArgs sp, ExpandArg
   if constexpr (EARLY) w.load_base(b, t.lo);
   v8bf wf[8][1];
   w.load_weights(wf);
-  shrink_sums<RG, 1, NW, DX, DW>(sp, t, 0, lds);
+  shrink_sums<RG, 1, NW, DX, DW, false>(sp, t, 0, blockIdx.x, lds);
   if constexpr (!EARLY) w.load_base(b, t.lo);
   const v4f* red = reinterpret_cast<const v4f*>(lds);
   if (threadIdx.x < 128) {                         // 16 rows x 32 ranks, four ranks a thread
@@ -697,11 +729,12 @@ struct PrepareArgs {
 };
 
 // rows x cols (at most 64 x 128 or 128 x 64, multiples of 8) of `in` transposed into `out`
+template <int THREADS>
 CR_DEV void transpose_tile(const uint16_t* in, int64_t ldi, uint16_t* out, int64_t ldo, int rows, int cols,
                            uint16_t* lds) {
   const int pitch = cols + 2;                      // an odd number of words: columns spread over the banks
   const int c8 = cols / 8, r8 = rows / 8;
-  for (int k = threadIdx.x; k < rows * c8; k += 256) {
+  for (int k = threadIdx.x; k < rows * c8; k += THREADS) {
     const int r = k / c8, c = k % c8 * 8;
     const u32x4 v = *reinterpret_cast<const u32x4*>(in + r * ldi + c);
     uint32_t* d = reinterpret_cast<uint32_t*>(lds + r * pitch + c);
@@ -709,7 +742,7 @@ CR_DEV void transpose_tile(const uint16_t* in, int64_t ldi, uint16_t* out, int64
     for (int e = 0; e < 4; ++e) d[e] = v[e];
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < cols * r8; k += 256) {
+  for (int k = threadIdx.x; k < cols * r8; k += THREADS) {
     const int c = k / r8, r = k % r8 * 8;
     u32x4 v;
 #pragma unroll
@@ -719,9 +752,9 @@ CR_DEV void transpose_tile(const uint16_t* in, int64_t ldi, uint16_t* out, int64
   }
 }
 
-__global__ __launch_bounds__(256) void lora_prepare_kernel(PrepareArgs p) {
-  __shared__ uint16_t lds[128 * 66 > 64 * 130 ? 128 * 66 : 64 * 130];
-  int b = blockIdx.x;
+constexpr int kPrepareLds = 128 * 66 > 64 * 130 ? 128 * 66 : 64 * 130;   // 2-byte words
+template <int THREADS>
+CR_DEV void prepare_block(const PrepareArgs& p, int b, uint16_t* lds) {
   // with more adapters than segments some have no rows, and nothing reads theirs (2 rows, 25 adapters
   // of rank 128, N = 4480: 6.2 against 12.6 us)
   auto unused = [&](int a) {
@@ -737,7 +770,7 @@ __global__ __launch_bounds__(256) void lora_prepare_kernel(PrepareArgs p) {
     const int a = b / per, n0 = b % per * 64;
     if (unused(a)) return;
     const int n = p.N - n0 < 64 ? p.N - n0 : 64;
-    transpose_tile(p.up + ((int64_t)a * p.N + n0) * p.R, p.R, p.up_t + (int64_t)a * p.R * p.N + n0, p.N, n, p.R, lds);
+    transpose_tile<THREADS>(p.up + ((int64_t)a * p.N + n0) * p.R, p.R, p.up_t + (int64_t)a * p.R * p.N + n0, p.N, n, p.R, lds);
     return;
   }
   b -= p.up_blocks;
@@ -746,11 +779,11 @@ __global__ __launch_bounds__(256) void lora_prepare_kernel(PrepareArgs p) {
     const int a = b / per, k0 = b % per * 64;
     if (unused(a)) return;
     const int n = p.K - k0 < 64 ? p.K - k0 : 64;
-    transpose_tile(p.down + (int64_t)a * p.R * p.K + k0, p.K, p.down_t + ((int64_t)a * p.K + k0) * p.R, p.R, p.R, n, lds);
+    transpose_tile<THREADS>(p.down + (int64_t)a * p.R * p.K + k0, p.K, p.down_t + ((int64_t)a * p.K + k0) * p.R, p.R, p.R, n, lds);
     return;
   }
   b -= p.down_blocks;
-  const int64_t k = (int64_t)b * 256 + threadIdx.x;   // one octet of rows and one rank
+  const int64_t k = (int64_t)b * THREADS + threadIdx.x;   // one octet of rows and one rank
   const int64_t m8 = k / p.R;
   const int r = (int)(k % p.R);
   if (m8 * 8 >= p.M) return;
@@ -768,12 +801,45 @@ __global__ __launch_bounds__(256) void lora_prepare_kernel(PrepareArgs p) {
     *reinterpret_cast<u32x4*>(p.la8 + rows8_index(p.M, p.R, term, (int)(m8 * 8), r)) = f[term];
 }
 
-static hipError_t launch_prepare(PrepareArgs p, hipStream_t s) {
+__global__ __launch_bounds__(256) void lora_prepare_kernel(PrepareArgs p) {
+  __shared__ uint16_t lds[kPrepareLds];
+  prepare_block<256>(p, blockIdx.x, lds);
+}
+
+static int64_t prepare_blocks(PrepareArgs& p, int threads) {
   p.up_blocks = p.up ? p.A * ((p.N + 63) / 64) : 0;
   p.down_blocks = p.down ? p.A * ((p.K + 63) / 64) : 0;
-  const int64_t la_blocks = p.la ? ((int64_t)((p.M + 7) / 8) * p.R + 255) / 256 : 0;
-  hipLaunchKernelGGL(lora_prepare_kernel, dim3((unsigned)(p.up_blocks + p.down_blocks + la_blocks)), dim3(256), 0, s, p);
+  return p.up_blocks + p.down_blocks + (p.la ? ((int64_t)((p.M + 7) / 8) * p.R + threads - 1) / threads : 0);
+}
+static hipError_t launch_prepare(PrepareArgs p, hipStream_t s) {
+  const unsigned blocks = (unsigned)prepare_blocks(p, 256);
+  hipLaunchKernelGGL(lora_prepare_kernel, dim3(blocks), dim3(256), 0, s, p);
   return hipGetLastError();
+}
+
+// prepare and dla in one launch: dla takes up as it lies, and what is left of
+// prepare nobody needs before the next launch. A whole call, this way against the
+// two launches: 300 rows, 2560 x 4096, rank 8, 21.0 against 24.0 us; 1531 rows, 2560 x 2560,
+// rank 32, 24.5 against 26.7; 2 rows, 12288 x 12288, rank 32, 18.8 against 21.0. Each
+// block takes most of a compute unit's LDS, and ranks above 32 are gathered from
+// lines that several blocks read: 512 rows, 4096 x 9216, rank 64 took 31.5 against
+// 29.0 us, 1531 rows of it, two rounds of dla's blocks, 42.2 against 36.3 us.
+__global__ __launch_bounds__(1024) void lora_first_kernel(ShrinkArgs a, PrepareArgs p, int tiles, int shrink_blocks) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ShrinkLds<1, 1, 16, 2, 2>::bytes];
+  static_assert(sizeof(lds) >= kPrepareLds * 2, "");
+  const int b = blockIdx.x;
+  if (b < shrink_blocks) shrink_block<1, 1, 16, 2, 2, true>(a, b % tiles, b / tiles, lds);
+  else prepare_block<1024>(p, b - shrink_blocks, reinterpret_cast<uint16_t*>(lds));
+}
+// false: too many blocks, nothing launched (up: [A][N][R])
+static bool launch_first(ShrinkArgs a, const uint16_t* up, PrepareArgs p, hipStream_t s, hipError_t* e) {
+  a.w = up;
+  p.up = nullptr;
+  const int64_t tiles = tile_grid(a.seg, 16), shrink = tiles * ((a.R + 15) / 16), blocks = shrink + prepare_blocks(p, 1024);
+  if (a.R > 32 || shrink > 256 || blocks > 512) return false;
+  hipLaunchKernelGGL(lora_first_kernel, dim3((unsigned)blocks), dim3(1024), 0, s, a, p, (int)tiles, (int)shrink);
+  *e = hipGetLastError();
+  return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -1282,12 +1348,16 @@ hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t s, int* kerne
   *kernels = 1;
   const PrepareArgs pre{dla_wanted ? p.up : nullptr, up_t, p.dx ? p.down : nullptr, down_t,
                         p.d_up ? p.la : nullptr, la8, M, N, K, p.R, A, 0, 0, p.seg};
-  if ((e = launch_prepare(pre, s)) != hipSuccess) return e;
-  if (dla_wanted) {
-    const ShrinkArgs a{p.dy, p.lddy, up_t, p.seg, p.scale, dla, p.d_down ? dla8 : nullptr,
-                       codes ? p.x_scales : nullptr, p.x_row_scales, p.R, N};
-    ++*kernels;
-    if ((e = launch_shrink(a, s)) != hipSuccess) return e;
+  const ShrinkArgs a{p.dy, p.lddy, up_t, p.seg, p.scale, dla, p.d_down ? dla8 : nullptr,
+                     codes ? p.x_scales : nullptr, p.x_row_scales, p.R, N};
+  if (dla_wanted && launch_first(a, p.up, pre, s, &e)) {
+    if (e != hipSuccess) return e;
+  } else {
+    if ((e = launch_prepare(pre, s)) != hipSuccess) return e;
+    if (dla_wanted) {
+      ++*kernels;
+      if ((e = launch_shrink(a, s)) != hipSuccess) return e;
+    }
   }
   const ExpandArgs ex{dla, down_t, p.seg, nullptr, p.dx_base, p.ldb, p.dx, p.lddx, p.R, K, 0, 0};
   if (!p.d_up && !p.d_down) {
