@@ -251,7 +251,7 @@ def test_backward_many_rows(cr, shape):
 
 @pytest.mark.parametrize("shape", [(1500, 72, 136, 24, 1, 95, "prompt"), (2600, 40, 264, 16, 2, 150, "prompt"),
                                    (4200, 8, 8, 8, 1, 700, "ragged"), (70, 136, 264, 32, 90, 2, "ragged"),
-                                   (3, 520, 72, 128, 70, 2, "tokens")])
+                                   (3, 520, 72, 128, 70, 2, "tokens"), (70, 136, 264, 16, 110, 2, "ragged")])
 def test_backward_many_segments_or_adapters(cr, shape):
     test_backward(cr, shape, True)
 

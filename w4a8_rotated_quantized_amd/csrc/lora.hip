@@ -200,8 +200,8 @@ struct ShrinkLds {
 // WT: the weights lie the other way, [A][C][R]. A load then takes the 16 ranks of
 // 32 columns, two lanes a column, and a fragment is gathered two bytes at a
 // time; column 8 g + e of the load lies at position 8 g + (e + 2 g) % 8, which
-// spreads these reads over the banks. Four times the LDS reads, so it is for few
-// rows only, where a launch that transposes first costs more.
+// spreads these reads over the banks. Four times the LDS reads, so it is for
+// few ranks only, where a launch that transposes first costs more.
 template <int RG, int TM, int NW, int DX, int DW, bool WT>
 CR_DEV void shrink_sums(const ShrinkArgs& p, const RowTile& t, int r0, int bx, uint8_t* lds) {
   static_assert(!WT || RG == 1, "a load holds the ranks of one group");
@@ -820,26 +820,37 @@ static hipError_t launch_prepare(PrepareArgs p, hipStream_t s) {
 // prepare and dla in one launch: dla takes up as it lies, and what is left of
 // prepare nobody needs before the next launch. A whole call, this way against the
 // two launches: 300 rows, 2560 x 4096, rank 8, 21.0 against 24.0 us; 1531 rows, 2560 x 2560,
-// rank 32, 24.5 against 26.7; 2 rows, 12288 x 12288, rank 32, 18.8 against 21.0. Each
-// block takes most of a compute unit's LDS, and ranks above 32 are gathered from
-// lines that several blocks read: 512 rows, 4096 x 9216, rank 64 took 31.5 against
-// 29.0 us, 1531 rows of it, two rounds of dla's blocks, 42.2 against 36.3 us.
-__global__ __launch_bounds__(1024) void lora_first_kernel(ShrinkArgs a, PrepareArgs p, int tiles, int shrink_blocks) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[ShrinkLds<1, 1, 16, 2, 2>::bytes];
+// rank 32, 24.5 against 26.7; 2 rows, 12288 x 12288, rank 32, 18.8 against 21.0; 8192 rows,
+// 4096 x 4096, rank 16, 102.9 against 105.0; 7031 rows, 768 x 7256, rank 16, 69 against 75.
+// Ranks above 32 are gathered from lines that several blocks read: 512 rows, 4096 x
+// 9216, rank 64 took 31.5 against 29.0 us, 1531 rows of it, two rounds of dla's
+// blocks, 42.2 against 36.3 us. The blocks of prepare take as much LDS as those of
+// dla, two at most on a compute unit, so there have to be few.
+template <int NW, int DX, int DW>
+__global__ __launch_bounds__(64 * NW) void lora_first_kernel(ShrinkArgs a, PrepareArgs p, int tiles, int shrink_blocks) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ShrinkLds<1, 1, NW, DX, DW>::bytes];
   static_assert(sizeof(lds) >= kPrepareLds * 2, "");
   const int b = blockIdx.x;
-  if (b < shrink_blocks) shrink_block<1, 1, 16, 2, 2, true>(a, b % tiles, b / tiles, lds);
-  else prepare_block<1024>(p, b - shrink_blocks, reinterpret_cast<uint16_t*>(lds));
+  if (b < shrink_blocks) shrink_block<1, 1, NW, DX, DW, true>(a, b % tiles, b / tiles, lds);
+  else prepare_block<64 * NW>(p, b - shrink_blocks, reinterpret_cast<uint16_t*>(lds));
 }
-// false: too many blocks, nothing launched (up: [A][N][R])
+template <int NW, int DX, int DW>
+static bool launch_first_k(const ShrinkArgs& a, PrepareArgs p, int64_t tiles, int64_t shrink, hipStream_t s, hipError_t* e) {
+  const int64_t prepare = prepare_blocks(p, 64 * NW);
+  if (prepare > 512) return false;
+  hipLaunchKernelGGL((lora_first_kernel<NW, DX, DW>), dim3((unsigned)(shrink + prepare)), dim3(64 * NW), 0, s, a, p,
+                     (int)tiles, (int)shrink);
+  *e = hipGetLastError();
+  return true;
+}
+// false: not for these sizes, nothing launched (up: [A][N][R])
 static bool launch_first(ShrinkArgs a, const uint16_t* up, PrepareArgs p, hipStream_t s, hipError_t* e) {
   a.w = up;
   p.up = nullptr;
-  const int64_t tiles = tile_grid(a.seg, 16), shrink = tiles * ((a.R + 15) / 16), blocks = shrink + prepare_blocks(p, 1024);
-  if (a.R > 32 || shrink > 256 || blocks > 512) return false;
-  hipLaunchKernelGGL(lora_first_kernel, dim3((unsigned)blocks), dim3(1024), 0, s, a, p, (int)tiles, (int)shrink);
-  *e = hipGetLastError();
-  return true;
+  const int64_t tiles = tile_grid(a.seg, 16), shrink = tiles * ((a.R + 15) / 16);
+  if (a.R <= 32 && shrink <= 256) return launch_first_k<16, 2, 2>(a, p, tiles, shrink, s, e);
+  if (a.R <= 16) return launch_first_k<8, 3, 2>(a, p, tiles, shrink, s, e);
+  return false;
 }
 
 // ---------------------------------------------------------------------------
