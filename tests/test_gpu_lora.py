@@ -160,6 +160,14 @@ def test_forward_many_rows(cr, shape):
     _near(out, want, e2, "out")
 
 
+# expand in tiles of 32, 32 and 64 rows
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("shape", [(1000, 4104, 72, 64, 3, 7, "ragged"), (700, 4104, 72, 128, 2, 3, "gaps"),
+                                   (2000, 4104, 72, 40, 2, 90, "ragged")])
+def test_forward_middle_tiles(cr, shape, f32):
+    test_forward(cr, shape, f32)
+
+
 def test_no_row_has_an_adapter(cr):
     t = Case(70, 136, 264, 16, 3, 4, seed=23)
     base_d, _ = t.base(t.N, False)

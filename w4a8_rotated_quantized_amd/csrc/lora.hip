@@ -611,10 +611,14 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
 }
 
 // Tall tiles read the weights less often, short ones end sooner: the tallest
-// that still give every one of the 256 compute units two blocks.
+// that still give every one of the 256 compute units two blocks, or one of 64 or
+// 32 rows (1531 x 9216 float32 of rank 64: 22.2 us in 64 rows, 32.9 in 16; 2488 x 2280
+// of rank 128: 16.0 and 19.8; 2438 x 2816 of rank 64: 13.9 us in 32 rows, 16.6 in 16).
 static void expand_tiles(ExpandArgs& p, int NJ) {
   const int64_t columns = (p.C + 64 * NJ - 1) / (64 * NJ);
-  p.rows = p.seg.M / 256 * columns >= 512 ? 256 : (p.seg.M / 64 * columns >= 512 ? 64 : 16);
+  p.rows = p.seg.M / 256 * columns >= 512 ? 256
+           : p.seg.M / 64 * columns >= 256 ? 64
+           : p.seg.M / 32 * columns >= 256 ? 32 : 16;
   p.blocks_x = (int)tile_grid(p.seg, p.rows);
 }
 template <int KS, int NJ, typename T>
