@@ -558,15 +558,15 @@ cr_status int8_tensorwise_gemm(const void* a_codes, const float* a_scale,
  *                The gradient is summed in the rotated basis and rotated back.
  *   down, up     bf16 [A, R, K] and [A, N, R] of A = n_adapters; R a multiple of
  *                8 from 8 to 128 (pad smaller ranks with zeros)
- *   seg_offsets  int32 [S + 1], not descending; seg_adapter int32 [S]. Empty
+ *   seg_offsets  int32 [S + 1], ascending; seg_adapter int32 [S]. Empty
  *                segments are fine. Segments may share an adapter. Rows before
  *                the first offset or behind the last, and segments whose
  *                adapter lies outside 0 .. A-1, have no adapter: their lora_act
  *                is 0, their out is base (their dx dx_base) and they add nothing
  *                to the gradients. Offsets are read on the device and clamped to
- *                the batch, so no row outside it is touched whatever they hold;
- *                descending offsets leave the results of the rows concerned
- *                unspecified.
+ *                the batch, and one below an earlier one counts as that earlier
+ *                one: whatever they hold, every row of the batch is in one
+ *                segment at most and no row outside it is touched.
  *   scale        optional float32 [A] (NULL: 1)
  *   base         optional, of out's type, leading dimension ldb (NULL: 0). It may
  *                be out itself (ldb == ldo): then rows without adapter are left

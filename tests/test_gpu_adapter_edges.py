@@ -1,0 +1,75 @@
+"""Calls of the adapter and checkpoint entry points at the edges of what their
+documentation allows: offsets in any order, tensors that are freed right after
+a call on another stream, infinite weights, codes of a smoothed input, loops
+with several stages per wave, the far tails of the activations.
+
+Bounds are those of test_gpu_lora.py and test_gpu_act.py unless a test derives
+its own."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from oracle import adapters as oa  # noqa: E402
+from tests.gpu_helpers import DEV, dev, say  # noqa: E402
+from tests.test_gpu_lora import Case, _near, _weight_bounds, cr  # noqa: E402, F401
+
+
+def _descending(kind, M, S, g):
+    if kind == "up and down":                      # 48 of 64 rows named again and again
+        off = np.zeros(S + 1, np.int64)
+        off[1::2] = 3 * M // 4
+    elif kind == "falling":
+        off = np.linspace(3 * M // 4, 0, S + 1).astype(np.int64)
+    else:
+        off = g.integers(-M // 4, 3 * M // 4, S + 1)
+    return off
+
+
+@pytest.mark.parametrize("kind", ["up and down", "falling", "any"])
+@pytest.mark.parametrize("M,N,K,R,A,S", [(64, 72, 64, 8, 3, 300), (40, 136, 72, 40, 2, 9), (700, 264, 136, 24, 3, 130),
+                                         (300, 72, 256, 64, 1, 66)])
+def test_offsets_in_any_order(cr, M, N, K, R, A, S, kind):
+    """An offset below an earlier one counts as that earlier one. Every row is
+    written, rows that no segment names are base and reach no gradient."""
+    say(f"offsets {kind} {M} {N} {K} {R} {A} {S}")
+    t = Case(M, N, K, R, A, S, seed=31)
+    t.off, t.ids = _descending(kind, M, S, t.g), t.g.integers(0, A, S)
+    t.off_d, t.ids_d = dev(t.off.astype(np.int32)), dev(t.ids.astype(np.int32))
+    off = np.maximum.accumulate(np.clip(t.off, 0, M))
+    t.rows = oa.row_adapters(off, t.ids, M, A)
+    none = t.rows < 0
+    assert none[3 * M // 4 + 1:].all()
+    la32 = t.g.standard_normal((M, R)).astype(np.float32)
+    la_d, none_d = dev(la32), dev(none)
+    for v in (t.x_d, t.dy_d, la_d):
+        v[none_d] = float("nan")
+    for v in (t.x, t.dy, la32):
+        v[none] = 0
+    base_d, base = t.base(N, True)
+    out, la = t.fwd(cr, base=base_d, out_type=cr.OUT.F32, out=torch.full((M, N), float("nan"), device=DEV),
+                    lora_act=torch.full((M, R), float("nan"), device=DEV))
+    want, la_want = oa.lora_forward(t.x, t.down, t.up, off, t.ids, t.c, base)
+    e1, e2 = t.two_products(t.x, t.down, t.up, base, want, True)
+    _near(la, la_want, e1, "lora_act")
+    _near(out, want, e2, "out")
+    assert torch.equal(out[none_d], base_d[none_d]) and not la[none_d].any()
+    base_d, base = t.base(K, True, seed=2)
+    dx, dd, du = t.bwd(cr, la_d, dx_base=base_d, dx_type=cr.OUT.F32, dx=torch.full((M, K), float("nan"), device=DEV))
+    dx_w, dd_w, du_w, dla = oa.lora_backward(t.dy, la32, t.x, t.down, t.up, off, t.ids, t.c, base)
+    c_up = t.c64[:, None, None] * t.up.transpose(0, 2, 1)
+    keep, t.c64 = t.c64, np.ones(A)
+    e1, e2 = t.two_products(t.dy, c_up, t.down.transpose(0, 2, 1), base, dx_w, True)
+    t.c64 = keep
+    _near(dx, dx_w, e2, "dx")
+    assert torch.equal(dx[none_d], base_d[none_d])
+    bd, bu = _weight_bounds(t, e1, la32, dla, np.abs(t.x), np.abs(t.dy))
+    _near(dd, dd_w, bd, "d_down")
+    _near(du, du_w, bu, "d_up")
+    # the same call with the offsets written out: the same bits
+    t.off_d = dev(off.astype(np.int32))
+    fwd = t.fwd(cr, base=t.base(N, True)[0], out_type=cr.OUT.F32)
+    bwd = t.bwd(cr, la_d, dx_base=base_d, dx_type=cr.OUT.F32)
+    for a, b in zip((out, la, dx, dd, du), fwd + bwd):
+        assert torch.equal(a, b)

@@ -35,8 +35,11 @@ CR_DEV v4f mfma16(v8bf a, v8bf b, v4f c) { return __builtin_amdgcn_mfma_f32_16x1
 // Boundary v (0 .. S + 2) of the S + 2 stretches that cover all M rows: the
 // rows before the first segment, the S segments, and the rows behind the last
 // one. Every value lies in [0, M] whatever the offsets hold, so no tile leaves
-// the batch. The load is unconditional, its index clamped: loads of several
-// boundaries are then under way together.
+// the batch. An offset below an earlier one counts as that earlier one: both
+// users take the running maximum of these values, so every row lies in exactly
+// one stretch and M / T + S + 2 tiles of T rows are enough for any offsets. The
+// load is unconditional, its index clamped: loads of several boundaries are
+// then under way together.
 CR_DEV int seg_bound(const LoraSegments& g, int v) {
   const int at = v - 1;
   int o = g.off[at < 0 ? 0 : (at > g.S ? g.S : at)];
@@ -64,21 +67,49 @@ CR_DEV int wave_scan(int x) {
   return x;
 }
 
+// running maximum over the wave's lanes of values from 0 on
+CR_DEV int wave_scan_max(int x) {
+  auto with = [&](int o) { x = x > o ? x : o; };
+  with(__builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));   // the same steps
+  with(__builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));
+  return x;
+}
+
+// Rows [lo, hi) of the lane's stretch v and the running maximum behind the
+// wave's last one; top: that of the stretches before.
+struct Stretch {
+  int lo, hi, top;
+};
+CR_DEV Stretch seg_rows(const LoraSegments& g, int v, int top) {
+  const int start = seg_bound(g, v), end = seg_bound(g, v + 1);
+  Stretch r;
+  r.lo = wave_scan_max(start > top ? start : top);
+  r.hi = end > r.lo ? end : r.lo;
+  r.top = __builtin_amdgcn_readlane(r.hi, 63);
+  return r;
+}
+
 // Tile t of T rows (a power of two), counted through the stretches: each wave scans the tile
 // counts of 64 stretches at a time. All 64 lanes take part; the result is
 // the same in all of them.
 CR_DEV RowTile find_tile(const LoraSegments& g, int t, int T) {
   const int lane = threadIdx.x & 63;
+  int top = 0;
   for (int v0 = 0; v0 < g.S + 2; v0 += 64) {
     const int v = v0 + lane;
-    const int lo = seg_bound(g, v), end = seg_bound(g, v + 1), a = seg_adapter(g, v);
-    const int hi = end > lo && v < g.S + 2 ? end : lo;
-    const int n = (hi - lo + T - 1) >> __builtin_ctz(T);
+    const int a = seg_adapter(g, v);
+    const Stretch st = seg_rows(g, v, top);        // behind the last stretch: M to M
+    top = st.top;
+    const int n = (st.hi - st.lo + T - 1) >> __builtin_ctz(T);
     const int upto = wave_scan(n);
     const int total = __builtin_amdgcn_readlane(upto, 63);
     if (t < total) {
       const int src = __builtin_ctzll(__ballot(upto > t));
-      const int slo = __builtin_amdgcn_readlane(lo, src), shi = __builtin_amdgcn_readlane(hi, src);
+      const int slo = __builtin_amdgcn_readlane(st.lo, src), shi = __builtin_amdgcn_readlane(st.hi, src);
       const int skip = t - (__builtin_amdgcn_readlane(upto, src) - __builtin_amdgcn_readlane(n, src));
       RowTile r;
       r.lo = slo + skip * T;
@@ -931,12 +962,14 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
   const float cs = p.scale ? p.scale[a] : 1.f;
   // lane's segment of the 64 that start at s0: its first row and its rows, 0 if
   // it is not of this adapter
-  int lo, len;
+  int lo, len, top = 0;                           // top: where the segments before these end
   auto segments = [&](int s0) {
     const int s = s0 + lane;
-    const int hi = seg_bound(p.seg, s + 2), of = seg_adapter(p.seg, s + 1);
-    lo = seg_bound(p.seg, s + 1);
-    len = s < p.seg.S && hi > lo && of == a ? hi - lo : 0;
+    const int of = seg_adapter(p.seg, s + 1);
+    const Stretch st = seg_rows(p.seg, s + 1, s0 ? top : 0);
+    top = st.top;
+    lo = st.lo;
+    len = s < p.seg.S && of == a ? st.hi - st.lo : 0;
   };
   segments(0);
   int64_t from = 0, to = (int64_t)1 << 62;        // this part of the adapter's rows, counted through its segments
@@ -1038,8 +1071,6 @@ CR_DEV void outer_block(const OuterArgs& p, int b, v4f (*red)[RG * 8 * 64]) {
         if (__builtin_amdgcn_readlane(lo, src) != slo + slen) break;
         slen += __builtin_amdgcn_readlane(len, src);
       }
-      // descending offsets could name rows more often than there are
-      if (slen > p.seg.M - before) slen = (int)(p.seg.M - before);
       const int64_t x0 = from > before ? from - before : 0;
       const int64_t x1 = to - before < slen ? to - before : slen;
       before += slen;
