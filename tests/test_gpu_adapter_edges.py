@@ -73,3 +73,64 @@ def test_offsets_in_any_order(cr, M, N, K, R, A, S, kind):
     bwd = t.bwd(cr, la_d, dx_base=base_d, dx_type=cr.OUT.F32)
     for a, b in zip((out, la, dx, dd, du), fwd + bwd):
         assert torch.equal(a, b)
+
+
+def test_inputs_freed_while_another_stream_reads_them(cr):
+    """A call on a given stream keeps the memory of its tensors: what the
+    caller frees right after it is not given out again before the call ends."""
+    t = Case(300, 136, 256, 16, 2, 5, seed=33)
+    la_d = dev(t.g.standard_normal((t.M, t.R)).astype(np.float32))
+    codes, scales, _, _ = cr.convrot_rotate_quantize(t.x_d, 256, cr.Q.SYM_INT8, cr.GRAN.ROW)
+    base, dx_base = t.base(t.N, False)[0], t.base(t.K, False, seed=2)[0]
+    z = t.dy_d[:, :128].contiguous()
+    _, zc, zs = cr.convrot_act_checkpoint(z, cr.ACT.GELU)
+    adapters = (t.down_d, t.up_d, t.off_d, t.ids_d, t.c_d)
+    calls = (
+        ("forward", lambda s, x, b, *a: cr.convrot_lora_forward(x, *a, base=b, stream=s), (t.x_d, base, *adapters)),
+        ("backward", lambda s, dy, la, x, xs, b, ws, *a: cr.convrot_lora_backward(
+            dy, la, x, *a, x_scales=xs, dx_base=b, workspace=ws, stream=s),
+         (t.dy_d, la_d, codes, scales, dx_base,
+          torch.zeros(cr.convrot_lora_backward_workspace_size(t.M, t.N, t.K, t.R, t.A), dtype=torch.uint8, device=DEV),
+          *adapters)),
+        ("checkpoint", lambda s, v: cr.convrot_act_checkpoint(v, cr.ACT.GELU, stream=s), (z,)),
+        ("slope", lambda s, *v: (cr.convrot_act_backward(*v, cr.ACT.GELU, stream=s),), (z, zc, zs)))
+    for name, call, args in calls:
+        say(f"freed inputs: {name}")
+        want = call(None, *args)
+        held = [v.clone() for v in args]
+        torch.cuda.synchronize()
+        other = torch.cuda.Stream()
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(50_000_000)          # the call waits behind it
+        got = call(other, *held)
+        freed = {v.data_ptr() for v in held}
+        del held
+        fresh = [torch.full_like(v, 3) for v in args]
+        waiting = not other.query()
+        assert not waiting or not freed & {v.data_ptr() for v in fresh}, name
+        torch.cuda.synchronize()
+        assert waiting, "the other stream ended before the memory was asked for"
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), name
+
+
+def test_captured_on_a_given_stream(cr):
+    t = Case(300, 136, 256, 16, 2, 5, seed=34)
+    z = t.dy_d[:, :128].contiguous()
+    def all_of_them(s):
+        out, la = t.fwd(cr, stream=s)
+        y, codes, scales = cr.convrot_act_checkpoint(z, cr.ACT.GELU_TANH, stream=s)
+        return (out, la, *t.bwd(cr, la, stream=s), y, cr.convrot_act_backward(y, codes, scales, cr.ACT.GELU_TANH, stream=s))
+    want = all_of_them(None)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = all_of_them(side)
+    for _ in range(3):
+        for v in held:
+            v.fill_(5)
+        again = all_of_them(None)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(held, again, want):
+            assert torch.equal(a, c) and torch.equal(b, c)

@@ -437,6 +437,15 @@ def _on(index, stream):
     return torch.cuda.stream(stream)
 
 
+def _hold(stream, *tensors):
+    """Tensors of a call on a given stream: memory of theirs that is freed while
+    the call still runs is not given out again before it has ended."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 # handle of a GPU's current stream, without the stream object around it
 _current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -490,6 +499,7 @@ def convrot_lora_forward(x, down, up, seg_offsets, seg_adapter, scale=None, base
             pl = lora_act.data_ptr()
         else:
             pl = _tensor(lora_act, "lora_act", _F32, index, (M, R))
+        _hold(stream, x, down, up, seg_offsets, seg_adapter, scale, base, out, lora_act)
         st = lib.convrot_lora_forward(px, ldx, pd, pu, R, A, po, pa, S, ps, pb, ldb, py, out_type, ldo, pl, M, N, K,
                                       _current_stream_handle(index))
     _check(st, "convrot_lora_forward")
@@ -556,6 +566,11 @@ def convrot_lora_backward(dy, lora_act, x, down, up, seg_offsets, seg_adapter, s
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
         elif workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous on GPU {index}")
+        _hold(stream, dy, down, up, seg_offsets, seg_adapter, scale, workspace)
+        if want_weights:
+            _hold(stream, lora_act, x, x_scales, d_down, d_up)
+        if want_dx:
+            _hold(stream, dx_base, dx)
         st = lib.convrot_lora_backward(pdy, lddy, pl, px, ldx, pxs, gran, rot_group, pd, pu, R, A, po, pa, S, ps,
                                        pb, ldb, pdx, dx_type, lddx, pgd, pgu, int(bool(accumulate)), M, N, K,
                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -596,6 +611,7 @@ def convrot_act_checkpoint(z, act, y=None, codes=None, scales=None, stream=None)
             ps = scales.data_ptr()
         else:
             ps = _tensor(scales, "scales", _F32, index, (rows, W // 64))
+        _hold(stream, z, y, codes, scales)
         st = lib.convrot_act_checkpoint(pz, ldz, rows, C, act, py, ldy, pc, ps, _current_stream_handle(index))
     _check(st, "convrot_act_checkpoint")
     return y, codes, scales
@@ -618,6 +634,7 @@ def convrot_act_backward(dy, codes, scales, act, dz=None, stream=None):
             pz = dz.data_ptr()
         else:
             pz, lddz = _rows(dz, "dz", _BF16, index, rows, W)
+        _hold(stream, dy, codes, scales, dz)
         st = lib.convrot_act_backward(pdy, lddy, pc, ps, rows, C, act, pz, lddz, _current_stream_handle(index))
     _check(st, "convrot_act_backward")
     return dz
