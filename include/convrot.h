@@ -556,6 +556,10 @@ cr_status int8_tensorwise_gemm(const void* a_codes, const float* a_scale,
  *                256 or 1024; K % 256 == 0, K % rot_group == 0, ldx % 16 == 0).
  *                x_scales NULL: x is bf16 and x_gran, rot_group are ignored.
  *                The gradient is summed in the rotated basis and rotated back.
+ *                Codes made with `smooth` stand for x * smooth, which they do not
+ *                tell: d_down is then sum_m dla[m, :]^T (x * smooth)[m, :], and its
+ *                column k has to be divided by smooth[k] for the gradient of down
+ *                (before it is added to anything: not with accumulate).
  *   down, up     bf16 [A, R, K] and [A, N, R] of A = n_adapters; R a multiple of
  *                8 from 8 to 128 (pad smaller ranks with zeros)
  *   seg_offsets  int32 [S + 1], ascending; seg_adapter int32 [S]. Empty

@@ -1,0 +1,30 @@
+"""What the adapter calls cannot check on their operands stands in their
+documentation, in the header and in the binding alike."""
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PKG = os.path.join(ROOT, "w4a8_rotated_quantized_amd")
+
+
+def _header():
+    with open(os.path.join(ROOT, "include", "convrot.h")) as f:
+        text = f.read()
+    lo = text.index("convrot_lora_forward / convrot_lora_backward - ")
+    return " ".join(text[lo:text.index("convrot_act_checkpoint / convrot_act_backward - ")].replace("\n *", " ").split())
+
+
+@pytest.fixture(scope="module")
+def cr():
+    pytest.importorskip("torch")
+    if not os.path.exists(os.path.join(PKG, "libconvrot.so")):
+        pytest.skip("libconvrot.so not built")
+    import w4a8_rotated_quantized_amd as m
+    return m
+
+
+def test_codes_of_a_smoothed_input(cr):
+    assert "Codes made with `smooth` stand for x * smooth" in _header()
+    assert "divided by smooth[k]" in _header()
+    assert "smooth stand for x * smooth" in " ".join(cr.convrot_lora_backward.__doc__.split())

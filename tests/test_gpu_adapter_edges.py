@@ -12,8 +12,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from oracle import adapters as oa  # noqa: E402
-from tests.gpu_helpers import DEV, dev, say  # noqa: E402
-from tests.test_gpu_lora import Case, _near, _weight_bounds, cr  # noqa: E402, F401
+from tests.gpu_helpers import DEV, dev, host, rel_l2, say  # noqa: E402
+from tests.test_gpu_lora import U2, Case, _near, _weight_bounds, cr  # noqa: E402, F401
 
 
 def _descending(kind, M, S, g):
@@ -134,3 +134,33 @@ def test_captured_on_a_given_stream(cr):
         torch.cuda.synchronize()
         for a, b, c in zip(held, again, want):
             assert torch.equal(a, c) and torch.equal(b, c)
+
+
+def test_codes_of_a_smoothed_input(cr):
+    """Codes made with `smooth` stand for x * smooth: the call gives that
+    input's d_down, and dividing its columns by smooth gives the gradient."""
+    t = Case(200, 136, 512, 16, 2, 4, seed=35)
+    la32 = t.g.standard_normal((t.M, t.R)).astype(np.float32)
+    smooth = np.exp2(t.g.integers(-3, 4, t.K)).astype(np.float32)      # powers of two: x * smooth and the division are exact
+    codes, scales, _, _ = cr.convrot_rotate_quantize(t.x_d, 256, cr.Q.SYM_INT8, cr.GRAN.ROW, smooth=dev(smooth))
+    _, dd, _ = t.bwd(cr, dev(la32), x=codes, x_scales=scales, want_dx=False)
+    x_hat = oa.restore_input(host(codes), host(scales), 256)
+    _, want, _, dla = oa.lora_backward(t.dy, la32, x_hat / smooth, t.down, t.up, t.off, t.ids, t.c)
+    # what the sums and the rotation (8 steps, two roundings each) of rotated codes may be off by
+    rotated = np.abs(host(codes).astype(np.float64) * host(scales).astype(np.float64)[:, None])
+    c_up = t.c64[:, None, None] * t.up.transpose(0, 2, 1)
+    e1 = np.zeros((t.M, t.R))
+    for a in range(t.A):
+        at = t.rows == a
+        e1[at] = (t.N + 16) * U2 * (np.abs(t.dy[at]) @ np.abs(c_up[a]).T)
+    bd, _ = _weight_bounds(t, e1, la32, dla, rotated, np.abs(t.dy))
+    for a in range(t.A):
+        at = t.rows == a
+        bd[a] += 16 * U2 * (np.abs(dla[at]).T @ rotated[at])
+    g = bd.reshape(t.A, t.R, -1, 256).sum(-1, keepdims=True) / 16
+    bd = np.broadcast_to(g, (t.A, t.R, g.shape[2], 256)).reshape(bd.shape)
+    _near(dd / dev(smooth), want, bd / smooth, "d_down / smooth")
+    # and that is the gradient of x itself up to the codes' 8 bits: a row of four to six sigma has a step
+    # of 1/21 sigma at most, an error of step / sqrt 12, 1.4 percent of sigma (x * smooth: of its largest columns)
+    _, true, _, _ = oa.lora_backward(t.dy, la32, t.x, t.down, t.up, t.off, t.ids, t.c)
+    assert rel_l2(host(dd), true * smooth) <= 0.05

@@ -521,8 +521,10 @@ def convrot_lora_backward(dy, lora_act, x, down, up, seg_offsets, seg_adapter, s
 
     x is the forward's input: bf16 [M, K], or as an 8-bit checkpoint the int8
     codes [M, K] that convrot_rotate_quantize (SYM_INT8, per row or per tensor,
-    rot_group) made of it, with x_scales float32 [M] or [1]. x and lora_act are
-    not read with want_weights=False and may be None then."""
+    rot_group) made of it, with x_scales float32 [M] or [1]. Codes made with
+    smooth stand for x * smooth: divide d_down by smooth then (and do not
+    accumulate into it). x and lora_act are not read with want_weights=False
+    and may be None then."""
     index = _gpu(dy, "dy")
     A, R, N, K, S, (pd, pu, po, pa, ps) = _adapters(index, dy, down, up, seg_offsets, seg_adapter, scale)
     M, dt, dev = dy.shape[0], _out_dtype(dx_type), dy.device
