@@ -544,7 +544,10 @@ cr_status int8_tensorwise_gemm(const void* a_codes, const float* a_scale,
  *   carried as three bf16 terms); out and dx are rounded once. Results do not
  *   depend on timing (no atomics), and a row's result does not depend on the
  *   values of other rows (infinities and NaN stay in their row; in the weight
- *   gradients they stay in their adapter). The order of a float32 sum is fixed
+ *   gradients they stay in their adapter). Where an infinite bf16 value meets a
+ *   float32 factor (up in out, down in dx, dy in d_up, x in d_down) the sums it
+ *   enters are infinite or NaN: a factor whose lower terms are zero gives
+ *   0 * infinity there. The order of a float32 sum is fixed
  *   for a call's sizes and segments; another batch around the same rows may
  *   change its last bits.
  *

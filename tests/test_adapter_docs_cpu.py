@@ -28,3 +28,9 @@ def test_codes_of_a_smoothed_input(cr):
     assert "Codes made with `smooth` stand for x * smooth" in _header()
     assert "divided by smooth[k]" in _header()
     assert "smooth stand for x * smooth" in " ".join(cr.convrot_lora_backward.__doc__.split())
+
+
+def test_infinite_bf16_values():
+    text = _header()
+    assert "an infinite bf16 value meets a float32 factor (up in out, down in dx, dy in d_up, x in d_down)" in text
+    assert "are infinite or NaN" in text

@@ -164,3 +164,54 @@ def test_codes_of_a_smoothed_input(cr):
     # of 1/21 sigma at most, an error of step / sqrt 12, 1.4 percent of sigma (x * smooth: of its largest columns)
     _, true, _, _ = oa.lora_backward(t.dy, la32, t.x, t.down, t.up, t.off, t.ids, t.c)
     assert rel_l2(host(dd), true * smooth) <= 0.05
+
+
+def test_infinite_weights_and_gradients(cr):
+    """An infinite bf16 value makes exactly the sums it enters infinite or NaN:
+    which of the two is open where it meets a float32 factor, and an infinity
+    where a bf16 one meets bf16. All other values keep their bits."""
+    t = Case(90, 136, 264, 16, 2, 3, seed=36, scale=False)
+    t.off_d, t.ids_d = dev(np.int32([0, 30, 60, 90])), dev(np.int32([0, 1, -1]))
+    la_d = dev(np.where(t.g.random((t.M, t.R)) < 0.5, 1.0, t.g.standard_normal((t.M, t.R))).astype(np.float32))
+    out, la = t.fwd(cr)
+    dx, dd, du = t.bwd(cr, la_d)
+    def only(got, was, at, what):
+        """got is not finite exactly where `at` says, and was's bits elsewhere"""
+        m = torch.zeros(got.shape, dtype=torch.bool, device=DEV)
+        m[at] = True
+        assert not torch.isfinite(got[m]).any() and torch.equal(got[~m], was[~m]), what
+    rows0, every = slice(0, 30), slice(None)
+    keep = t.up_d[0, 70, 3].clone()
+    t.up_d[0, 70, 3] = float("inf")                # enters column 70 of out and rank 3 of dla
+    out2, la2 = t.fwd(cr)
+    dx2, dd2, du2 = t.bwd(cr, la_d)
+    only(out2, out, (rows0, 70), "out, up")
+    only(dx2, dx, (rows0, every), "dx, up")
+    only(dd2, dd, (0, 3), "d_down, up")
+    assert torch.equal(la2, la) and torch.equal(du2, du)
+    t.up_d[0, 70, 3] = keep
+    keep = t.down_d[0, 5, 200].clone()
+    t.down_d[0, 5, 200] = float("inf")             # enters rank 5 of lora_act and column 200 of dx
+    out2, la2 = t.fwd(cr)
+    dx2, dd2, du2 = t.bwd(cr, la_d)
+    only(la2, la, (rows0, 5), "lora_act, down")
+    assert torch.isinf(la2[:30, 5]).all()
+    only(out2, out, (rows0, every), "out, down")
+    only(dx2, dx, (rows0, 200), "dx, down")
+    assert torch.equal(dd2, dd) and torch.equal(du2, du)
+    t.down_d[0, 5, 200] = keep
+    keep = t.dy_d[40, 9].clone()
+    t.dy_d[40, 9] = float("-inf")                  # enters row 40 of dx and column 9 of adapter 1's d_up
+    dx2, dd2, du2 = t.bwd(cr, la_d)
+    only(dx2, dx, (40, every), "dx, dy")
+    only(dd2, dd, (1, every), "d_down, dy")
+    only(du2, du, (1, 9), "d_up, dy")
+    t.dy_d[40, 9] = keep
+    t.x_d[40, 11] = float("inf")                   # enters row 40 of lora_act and column 11 of adapter 1's d_down
+    out2, la2 = t.fwd(cr)
+    dx2, dd2, du2 = t.bwd(cr, la_d)
+    only(la2, la, (40, every), "lora_act, x")
+    assert torch.isinf(la2[40]).all()
+    only(out2, out, (40, every), "out, x")
+    only(dd2, dd, (1, every, 11), "d_down, x")
+    assert torch.equal(dx2, dx) and torch.equal(du2, du)

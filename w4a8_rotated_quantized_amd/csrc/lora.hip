@@ -137,7 +137,9 @@ CR_DEV v8bf load8(const uint16_t* p, bool ok) {
 }
 
 // f = hi + mid + lo, each a bf16 value: truncation leaves remainders that are
-// exact in float32. An infinity or NaN goes into hi alone.
+// exact in float32. An infinity or NaN goes into hi alone. An infinite partner
+// of a finite f meets mid and lo too, often zeros: the sum is NaN then where the
+// product alone were infinite, not finite in either case.
 struct Split {
   uint32_t hi, mid, lo;   // bf16 bits in the upper half
 };
