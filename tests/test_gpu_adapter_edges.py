@@ -215,3 +215,23 @@ def test_infinite_weights_and_gradients(cr):
     only(out2, out, (40, every), "out, x")
     only(dd2, dd, (1, every, 11), "d_down, x")
     assert torch.equal(dx2, dx) and torch.equal(du2, du)
+
+
+def test_gated_slope_of_the_largest_values(cr):
+    """silu' reaches 1.1: u silu'(g) beyond float32's largest value must not
+    make dg infinite while dy u silu'(g) has a value."""
+    g = np.repeat(np.float32([1.5, 2.375, 3.0, -1.25, 20.0, 0.5]), 64).reshape(6, 64)
+    top = np.float32(3.3895313892515355e38)        # the largest bf16 value
+    u = np.full((6, 64), top, np.float32)
+    u[3:, ::2] = -top
+    for dy in (2.0 ** -7, 0.5, -2.0 ** -60):
+        z = torch.from_numpy(np.concatenate([g, u], 1)).to(torch.bfloat16).to(DEV)
+        y, codes, scales = cr.convrot_act_checkpoint(z, cr.ACT.SWIGLU)
+        dy_d = torch.full((6, 64), dy, dtype=torch.bfloat16, device=DEV)
+        dz = host(cr.convrot_act_backward(dy_d, codes, scales, cr.ACT.SWIGLU).float()).astype(np.float64)
+        kept = oa.restore_checkpoint(host(codes), host(scales))
+        want = oa.act_backward(np.full((6, 64), dy), kept, "swiglu")
+        assert np.isfinite(dz).all()
+        # half a bf16 step, and the float32 roundings that test_gpu_act.py allows a slope
+        k = np.concatenate([kept[:, :64], kept[:, :64]], 1)
+        assert np.all(np.abs(dz - want) <= np.abs(want) * (2.0 ** -8 + 64 * 2.0 ** -24 * (1 + np.abs(k)) ** 2))

@@ -208,7 +208,8 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActArgs p, RowDiv d) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const Sigmoid s = sigmoid(v[e]);
-      dg[e] = dy[e] * (u[e] * (s.p * (1.f + v[e] * s.q)));
+      // halved on the way, exactly: the slope reaches 1.1, and u times it could overflow where dg does not
+      dg[e] = 2.f * (dy[e] * (u[e] * (0.5f * (s.p * (1.f + v[e] * s.q)))));
       du[e] = dy[e] * (v[e] * s.p);
     }
     *reinterpret_cast<u32x4*>(out) = pack8(dg);
