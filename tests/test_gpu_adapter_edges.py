@@ -12,6 +12,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from oracle import adapters as oa  # noqa: E402
+import tests.test_gpu_lora as lora_tests  # noqa: E402
 from tests.gpu_helpers import DEV, dev, host, rel_l2, say  # noqa: E402
 from tests.test_gpu_lora import U2, Case, _near, _weight_bounds, cr  # noqa: E402, F401
 
@@ -235,3 +236,53 @@ def test_gated_slope_of_the_largest_values(cr):
         # half a bf16 step, and the float32 roundings that test_gpu_act.py allows a slope
         k = np.concatenate([kept[:, :64], kept[:, :64]], 1)
         assert np.all(np.abs(dz - want) <= np.abs(want) * (2.0 ** -8 + 64 * 2.0 ** -24 * (1 + np.abs(k)) ** 2))
+
+
+# Sizes that give every wave of the first product several stages of 64 columns, so that the slots of its
+# rings are used again and the start column wraps, for each of its variants: waves a block, rows and ranks
+# of a block, stages in flight. M, the sum's length, R, A, S
+RINGS = [(300, 5000, 16, 2, 5), (800, 5000, 64, 2, 5),                     # 16 waves, 16 rows, 16 ranks, 2 stages
+         (2000, 2056, 32, 2, 5), (5000, 2056, 32, 3, 70),                  # 8 waves, 32 ranks, 2 stages
+         (4300, 2056, 16, 2, 5), (4500, 1544, 8, 2, 9),                    # 8 waves, 16 ranks, 3 stages of x and 2 of the weights
+         (8300, 1608, 32, 2, 7), (8192, 2560, 24, 3, 5),                   # 5 waves, 32 rows, 32 ranks, 2 stages
+         (2100, 2056, 64, 2, 5), (1300, 2056, 120, 3, 5),                  # 8 waves, 64 ranks, 1 stage
+         (8300, 2056, 64, 2, 5), (4200, 1608, 120, 2, 9),                  # 6 waves, 32 rows, 64 ranks, 1 stage
+         (48, 5000, 16, 2, 3), (130, 4104, 24, 2, 9)]                      # both products in one launch
+
+
+@pytest.mark.parametrize("M,C,R,A,S", RINGS)
+def test_long_rows_forward(cr, M, C, R, A, S):
+    _forward(cr, (M, 72, C, R, A, S), False)
+
+
+@pytest.mark.parametrize("M,C,R,A,S", RINGS)
+def test_long_rows_backward(cr, M, C, R, A, S):
+    """dla is the same product over dy; up to rank 16, and up to 32 with few rows, it reads up as it lies."""
+    lora_tests.test_backward(cr, (M, C, 72, R, A, S, "ragged"), False)
+
+
+def _forward(cr, shape, f32):
+    say(f"lora forward {shape} f32={f32}")
+    t = Case(*shape, seed=37)
+    base_d, base = t.base(t.N, f32)
+    want, la_want = oa.lora_forward(t.x, t.down, t.up, t.off, t.ids, t.c, base)
+    out, la = t.fwd(cr, base=base_d, out_type=cr.OUT.F32 if f32 else cr.OUT.BF16)
+    e1, e2 = t.two_products(t.x, t.down, t.up, base, want, f32)
+    _near(la, la_want, e1, "lora_act")
+    _near(out, want, e2, "out")
+
+
+# the second product in tiles of 256 rows: ranks of one, two and four register steps
+TALL = [(8200, 8200, 16, 2, 5), (8256, 7696, 64, 3, 9), (8300, 4104, 128, 2, 7)]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,C,R,A,S", TALL)
+def test_tall_tiles_forward(cr, M, C, R, A, S, f32):
+    _forward(cr, (M, C, 72, R, A, S), f32)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,C,R,A,S", TALL)
+def test_tall_tiles_backward(cr, M, C, R, A, S, f32):
+    lora_tests.test_backward(cr, (M, 72, C, R, A, S, "ragged"), f32)
