@@ -11,9 +11,11 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from oracle import adapters as oa  # noqa: E402
+import tests.test_gpu_act as act_tests  # noqa: E402
 import tests.test_gpu_lora as lora_tests  # noqa: E402
-from tests.gpu_helpers import DEV, dev, host, rel_l2, say  # noqa: E402
+import workloads as wl  # noqa: E402
+from oracle import adapters as oa  # noqa: E402
+from tests.gpu_helpers import DEV, bf16_dev, bf16_to_f32, dev, host, rel_l2, say  # noqa: E402
 from tests.test_gpu_lora import U2, Case, _near, _weight_bounds, cr  # noqa: E402, F401
 
 
@@ -286,3 +288,57 @@ def test_tall_tiles_forward(cr, M, C, R, A, S, f32):
 @pytest.mark.parametrize("M,C,R,A,S", TALL)
 def test_tall_tiles_backward(cr, M, C, R, A, S, f32):
     lora_tests.test_backward(cr, (M, 72, C, R, A, S, "ragged"), f32)
+
+
+def _bf16_values():
+    v = bf16_to_f32(np.arange(1 << 16, dtype=np.uint32).astype(np.uint16))
+    return np.sort(v[np.isfinite(v) & ((np.abs(v) > 3.9e-37) | (v == 0))])
+
+
+@pytest.mark.parametrize("act", act_tests.ACTS)
+def test_value_of_every_bf16_number(cr, act):
+    """The bound of ordinary values holds for all: in the negative tail, down to
+    float32's smallest normal value, the relative precision is kept, and beyond
+    it the result is that close to the tiny one, never positive."""
+    v = _bf16_values()
+    v = np.concatenate([v, np.zeros(-len(v) % 128, np.float32)]).reshape(-1, 128)
+    z = np.concatenate([v, np.ones_like(v)], 1) if act == "swiglu" else v
+    y, _, _ = cr.convrot_act_checkpoint(bf16_dev(wl.bf16_bits_from_f32(z)), act_tests._act(cr, act))
+    got, z64 = act_tests._f32(y), z.astype(np.float64)
+    want = oa.act_value(z64, act)
+    assert np.all(np.abs(got - want) <= act_tests._value_bound(z64, want, act))
+    assert np.all(got[v < 0] <= 0) and np.all(got[v > 0] >= 0)
+
+
+@pytest.mark.parametrize("act", act_tests.ACTS)
+def test_slope_of_the_tails(cr, act):
+    """Groups of one value each, so that the codes stand for it to a float32
+    rounding, from 1/8 to 256 either way.
+
+    GELU_TANH: p + z p q a (1 + 3 b z^2) with p = sigma(2 t): 2 t is off by four
+    roundings, p by |2 t| times that and by four of its own, the second part by six
+    more: 64 (1 + |2 t|) roundings of either part cover it. Below float32's normal
+    values p keeps 2^-149, which the second part multiplies by less than 2^10
+    before p is 0."""
+    v = _bf16_values()
+    v = v[(np.abs(v) >= 0.125) & (np.abs(v) <= 256)]
+    z = np.repeat(v, 64).reshape(-1, 64)
+    if act == "swiglu":
+        z = np.concatenate([z, np.ones_like(z)], 1)
+    _, codes, scales = cr.convrot_act_checkpoint(bf16_dev(wl.bf16_bits_from_f32(z)), act_tests._act(cr, act))
+    kept = oa.restore_checkpoint(host(codes), host(scales))
+    assert np.all(np.abs(kept - z) <= 2.0 ** -22 * np.abs(z))
+    ones = np.ones((len(v), 64))
+    got = act_tests._f32(cr.convrot_act_backward(dev(ones.astype(np.float32)).bfloat16(), codes, scales,
+                                                 act_tests._act(cr, act)))
+    want = oa.act_backward(ones, kept, act)
+    if act == "gelu_tanh":
+        a, b = 2 * np.sqrt(2 / np.pi), 0.044715
+        t2 = a * (kept + b * kept ** 3)
+        with np.errstate(over="ignore"):
+            p, q = 1 / (1 + np.exp(-t2)), 1 / (1 + np.exp(t2))
+        bound = 2.0 ** -8 * np.abs(want) + 2.0 ** -126 + 64 * 2.0 ** -24 * (1 + np.abs(t2)) * (
+            p + np.abs(kept) * p * q * a * (1 + 3 * b * kept * kept))
+    else:
+        bound = act_tests._slope_bound(ones, kept, want, act)
+    assert np.all(np.abs(got - want) <= bound)
