@@ -725,12 +725,14 @@ __global__ __launch_bounds__(1024) void lora_few_kernel(ShrinkArgs sp, ExpandArg
   if (w.c0 < p.C) w.add_rows(wf, la3, 0, reinterpret_cast<float*>(lds) + wave * 16 * Wave::PITCH, b, t.lo);
 }
 
-// Rows x column groups x weights of the shrink: what the blocks read of it, at
-// most 64 MB. There both ways take the same time on the GPU (64 rows of rank 32,
-// 8192 x 8192: 20.4 and 20.6 us with the launch) and one launch less on the host
-// (12 against 15.5 us); below, one launch is 1 to 2.5 us shorter (128 rows of rank 16,
-// 4096 x 4096: 16.4 against 18.9 us), above, two are (64 rows of rank 32, 12288 x
-// 12288: 26.6 against 38.5 us).
+// Rows x column groups x weights of the shrink: what the blocks would read of it
+// if every row were a tile, at most 64 MiB. GPU time of one launch and of two (host
+// calls take 12 and 15.5 us): at the bound, 64 single rows of rank 32, 4096 -> 8192,
+// 13.1 and 14.8 us, 128 of rank 16 17.3 and 18.0; below, 128 of rank 16, 4096 -> 4096,
+// 10.2 and 13.2; above, 96 of rank 32, 4096 -> 8192 (96 MiB), 22.4 and 19.2, 64 of rank
+// 32, 12288 -> 12288, 35.7 and 22.9 (8192 -> 8192, 128 MiB, still 16.3 and 17.4). Long
+// segments read less than this counts, in fewer blocks: 256 rows of one adapter,
+// rank 32, 4096 -> 4096 (128 MiB as counted), 11.9 and 10.8 us.
 static bool few_rows(const LoraSegments& g, int R, int64_t N, int64_t K) {
   return R <= 32 && g.M <= 256 && g.M * ((N + 2047) / 2048) * R * K <= ((int64_t)1 << 25);
 }
