@@ -34,3 +34,9 @@ def test_infinite_bf16_values():
     text = _header()
     assert "an infinite bf16 value meets a float32 factor (up in out, down in dx, dy in d_up, x in d_down)" in text
     assert "are infinite or NaN" in text
+
+
+def test_autograd_records_nothing(cr):
+    for call, back in ((cr.convrot_lora_forward, "convrot_lora_backward"), (cr.convrot_act_checkpoint, "convrot_act_backward")):
+        text = " ".join(call.__doc__.split())
+        assert "Not recorded by autograd" in text and back in text

@@ -396,6 +396,9 @@ def int8_tensorwise_gemm(a_codes, a_scale, w, w_scale, M, N, K, bias=None, out_t
 
 # ---------------------------------------------------------------------------
 # batched low-rank adapters and 8-bit activation checkpoints
+#
+# As everywhere in this binding, autograd records nothing: outputs require no
+# gradient whatever the inputs do. The backward calls give the gradients.
 # ---------------------------------------------------------------------------
 _OUT_DTYPE = {OUT.BF16: torch.bfloat16, OUT.F32: torch.float32}
 _BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
@@ -482,7 +485,8 @@ def convrot_lora_forward(x, down, up, seg_offsets, seg_adapter, scale=None, base
     the output's type (None: zero), which may be `out` itself. Rows of x, base
     and out may lie further apart than their length. Returns (out, lora_act):
     lora_act float32 [M, R] is what convrot_lora_backward reads. Outputs are
-    allocated when not given."""
+    allocated when not given. Not recorded by autograd: the gradients come from
+    convrot_lora_backward."""
     index = _gpu(x, "x")
     A, R, N, K, S, (pd, pu, po, pa, ps) = _adapters(index, x, down, up, seg_offsets, seg_adapter, scale)
     M, dt = x.shape[0], _out_dtype(out_type)
@@ -590,7 +594,8 @@ def _act_width(t, act, what):
 def convrot_act_checkpoint(z, act, y=None, codes=None, scales=None, stream=None):
     """y = act(z) (ACT.GELU, ACT.GELU_TANH: z bf16 [rows, C]; ACT.SWIGLU: z
     bf16 [rows, 2C], gate then linear half), with z kept as int8 codes and one
-    float32 scale per row and 64 columns. Returns (y, codes, scales)."""
+    float32 scale per row and 64 columns. Returns (y, codes, scales). Not
+    recorded by autograd: the gradient comes from convrot_act_backward."""
     index = _gpu(z, "z")
     rows, W = _act_width(z, act, "z")
     C = W // 2 if act == ACT.SWIGLU else W
