@@ -342,3 +342,29 @@ def test_slope_of_the_tails(cr, act):
     else:
         bound = act_tests._slope_bound(ones, kept, want, act)
     assert np.all(np.abs(got - want) <= bound)
+
+
+def test_misaligned_operands_are_named(cr):
+    """Views that start between multiples of 16 bytes are refused, by name."""
+    t = Case(20, 72, 64, 8, 2, 3, seed=38)
+    la = torch.zeros((20, 8), device=DEV)
+    shifted = lambda v: torch.cat([v.flatten()[:1], v.flatten()])[1:].view(v.shape)
+    def refused(name, call):
+        with pytest.raises(cr.ConvRotError, match=rf"\({name}: not at a multiple of 16 bytes\): invalid argument") as e:
+            call()
+        assert e.value.status == 1
+    fwd = dict(x=t.x_d, down=t.down_d, up=t.up_d, seg_offsets=t.off_d, seg_adapter=t.ids_d, scale=t.c_d)
+    for k in fwd:
+        refused(k, lambda: cr.convrot_lora_forward(**{**fwd, k: shifted(fwd[k])}))
+    bwd = dict(fwd, dy=t.dy_d, lora_act=la)
+    for k in bwd:
+        refused(k, lambda: cr.convrot_lora_backward(**{**bwd, k: shifted(bwd[k])}))
+    z = t.dy_d[:, :64].contiguous()
+    y, codes, scales = cr.convrot_act_checkpoint(z, cr.ACT.GELU)
+    refused("z", lambda: cr.convrot_act_checkpoint(shifted(z), cr.ACT.GELU))
+    back = dict(dy=y, codes=codes, scales=scales)
+    for k in back:
+        refused(k, lambda: cr.convrot_act_backward(**{**back, k: shifted(back[k])}, act=cr.ACT.GELU))
+    refused("x, scale", lambda: cr.convrot_lora_forward(**{**fwd, "x": shifted(t.x_d), "scale": shifted(t.c_d)}))
+    # what is not read is not named
+    cr.convrot_lora_backward(**{**bwd, "x": shifted(t.x_d), "lora_act": shifted(la)}, want_weights=False)

@@ -454,6 +454,12 @@ _current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _refused(status, where, **tensors):
+    """Raises for a call that was not accepted, naming addresses that the library does not take."""
+    off = [k for k, t in tensors.items() if t is not None and t.data_ptr() % 16]
+    _check(status, f"{where} ({', '.join(off)}: not at a multiple of 16 bytes)" if off else where)
+
+
 def _out_dtype(out_type):
     if out_type not in _OUT_DTYPE:
         raise ValueError("the output type is OUT.BF16 or OUT.F32")
@@ -506,7 +512,9 @@ def convrot_lora_forward(x, down, up, seg_offsets, seg_adapter, scale=None, base
         _hold(stream, x, down, up, seg_offsets, seg_adapter, scale, base, out, lora_act)
         st = lib.convrot_lora_forward(px, ldx, pd, pu, R, A, po, pa, S, ps, pb, ldb, py, out_type, ldo, pl, M, N, K,
                                       _current_stream_handle(index))
-    _check(st, "convrot_lora_forward")
+    if st:
+        _refused(st, "convrot_lora_forward", x=x, down=down, up=up, seg_offsets=seg_offsets, seg_adapter=seg_adapter,
+                 scale=scale, base=base, out=out, lora_act=lora_act)
     return out, lora_act
 
 
@@ -581,7 +589,13 @@ def convrot_lora_backward(dy, lora_act, x, down, up, seg_offsets, seg_adapter, s
                                        pb, ldb, pdx, dx_type, lddx, pgd, pgu, int(bool(accumulate)), M, N, K,
                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                        _current_stream_handle(index))
-    _check(st, "convrot_lora_backward")
+    if st:
+        read = dict(dy=dy, down=down, up=up, seg_offsets=seg_offsets, seg_adapter=seg_adapter, scale=scale, workspace=workspace)
+        if want_weights:
+            read.update(x=x, x_scales=x_scales, lora_act=lora_act, d_down=d_down, d_up=d_up)
+        if want_dx:
+            read.update(dx_base=dx_base, dx=dx)
+        _refused(st, "convrot_lora_backward", **read)
     return (dx if want_dx else None), (d_down if want_weights else None), (d_up if want_weights else None)
 
 
@@ -620,7 +634,8 @@ def convrot_act_checkpoint(z, act, y=None, codes=None, scales=None, stream=None)
             ps = _tensor(scales, "scales", _F32, index, (rows, W // 64))
         _hold(stream, z, y, codes, scales)
         st = lib.convrot_act_checkpoint(pz, ldz, rows, C, act, py, ldy, pc, ps, _current_stream_handle(index))
-    _check(st, "convrot_act_checkpoint")
+    if st:
+        _refused(st, "convrot_act_checkpoint", z=z, y=y, codes=codes, scales=scales)
     return y, codes, scales
 
 
@@ -643,5 +658,6 @@ def convrot_act_backward(dy, codes, scales, act, dz=None, stream=None):
             pz, lddz = _rows(dz, "dz", _BF16, index, rows, W)
         _hold(stream, dy, codes, scales, dz)
         st = lib.convrot_act_backward(pdy, lddy, pc, ps, rows, C, act, pz, lddz, _current_stream_handle(index))
-    _check(st, "convrot_act_backward")
+    if st:
+        _refused(st, "convrot_act_backward", dy=dy, codes=codes, scales=scales, dz=dz)
     return dz
