@@ -1,7 +1,8 @@
 """Calls of the adapter and checkpoint entry points at the edges of what their
 documentation allows: offsets in any order, tensors that are freed right after
 a call on another stream, infinite weights, codes of a smoothed input, loops
-with several stages per wave, the far tails of the activations.
+with several stages per wave, the far tails of the activations, addresses
+beyond 32 bits, gradients in place.
 
 Bounds are those of test_gpu_lora.py and test_gpu_act.py unless a test derives
 its own."""
@@ -368,3 +369,86 @@ def test_misaligned_operands_are_named(cr):
     refused("x, scale", lambda: cr.convrot_lora_forward(**{**fwd, "x": shifted(t.x_d), "scale": shifted(t.c_d)}))
     # what is not read is not named
     cr.convrot_lora_backward(**{**bwd, "x": shifted(t.x_d), "lora_act": shifted(la)}, want_weights=False)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N,K,R,A,S", [(37, 72, 264, 16, 2, 5), (700, 136, 520, 40, 3, 9), (2100, 72, 4104, 24, 2, 7)])
+def test_backward_in_place(cr, M, N, K, R, A, S, f32):
+    """dx may be dx_base itself: the same bits, rows without adapter as they were."""
+    t = Case(M, N, K, R, A, S, mix="gaps", seed=39)
+    kind = cr.OUT.F32 if f32 else cr.OUT.BF16
+    la = dev(t.g.standard_normal((M, R)).astype(np.float32))
+    base = t.base(K, f32)[0]
+    want = t.bwd(cr, la, dx_base=base, dx_type=kind)
+    own = base.clone()
+    got = t.bwd(cr, la, dx_base=own, dx=own, dx_type=kind)
+    assert got[0] is own
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    none = dev(t.rows < 0)
+    assert none.any() and torch.equal(own[none], base[none])
+
+
+def _far(v, ld):
+    """v in rows ld elements apart"""
+    wide = torch.empty((v.shape[0], ld), dtype=v.dtype, device=DEV)
+    wide[:, :v.shape[1]] = v
+    return wide[:, :v.shape[1]]
+
+
+def test_rows_beyond_32_bits(cr):
+    """Rows up to 2^31 elements and more behind the first one: the bits of dense rows."""
+    t = Case(1100, 264, 136, 24, 2, 5, seed=40)
+    ld = 1 << 21                                   # the last row starts at 1.07 * 2^31 elements
+    la = dev(t.g.standard_normal((t.M, t.R)).astype(np.float32))
+    base, dx_base = t.base(t.N, False)[0], t.base(t.K, False, seed=2)[0]
+    want, want_b = t.fwd(cr, base=base), t.bwd(cr, la, dx_base=dx_base)
+    x, dy, y = t.x_d, t.dy_d, torch.empty((t.M, ld), dtype=torch.bfloat16, device=DEV)
+    t.x_d, t.dy_d = _far(x, ld), _far(dy, ld)
+    got = t.fwd(cr, base=_far(base, ld), out=y[:, :t.N])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    got = t.bwd(cr, la, dx_base=_far(dx_base, ld), dx=y[:, :t.K])
+    for a, b in zip(got, want_b):
+        assert torch.equal(a, b)
+    for act in (cr.ACT.GELU, cr.ACT.SWIGLU):
+        z, d = x[:, :128].contiguous(), dy[:, :64 if act == cr.ACT.SWIGLU else 128].contiguous()
+        want = cr.convrot_act_checkpoint(z, act)
+        got = cr.convrot_act_checkpoint(_far(z, ld), act, y=y[:, :d.shape[1]])
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        dz = cr.convrot_act_backward(d, want[1], want[2], act)
+        assert torch.equal(cr.convrot_act_backward(_far(d, ld), want[1], want[2], act, dz=y[:, :128]), dz)
+
+
+def test_adapters_beyond_32_bits(cr):
+    """down of 2^31 values and more: the last adapter's rows get its weights."""
+    A, R, K, N, M = 4096, 128, 4104, 8, 70
+    g = np.random.default_rng(41)
+    put = lambda *shape: torch.from_numpy(g.standard_normal(shape).astype(np.float32)).to(DEV).bfloat16()
+    x, d, u = put(M, K), put(2, R, K), put(2, N, R)
+    off, one = dev(np.int32([0, 40, 70])), torch.zeros((A, N, R), dtype=torch.bfloat16, device=DEV)
+    want = cr.convrot_lora_forward(x, d, u, off, dev(np.int32([1, 0])))
+    down = torch.empty((A, R, K), dtype=torch.bfloat16, device=DEV)
+    assert down.numel() > 2 ** 31
+    down[A - 1], one[A - 1] = d[1], u[1]
+    down[7], one[7] = d[0], u[0]
+    got = cr.convrot_lora_forward(x, down, one, off, dev(np.int32([A - 1, 7])))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act", ["gelu_tanh", "swiglu"])
+def test_codes_beyond_32_bits(cr, act):
+    """2^31 codes and more: the last rows are those of a call of their own."""
+    rows, C = (530_000, 4096) if act == "gelu_tanh" else (270_000, 4096)
+    kind = act_tests._act(cr, act)
+    W = 2 * C if act == "swiglu" else C
+    z = torch.empty((rows, W), dtype=torch.bfloat16, device=DEV).normal_()
+    assert z.numel() > 2 ** 31
+    y, codes, scales = cr.convrot_act_checkpoint(z, kind)
+    last = slice(rows - 3, rows)
+    for a, b in zip((y, codes, scales), cr.convrot_act_checkpoint(z[last], kind)):
+        assert torch.equal(a[last], b)
+    dz = cr.convrot_act_backward(y, codes, scales, kind)
+    assert torch.equal(dz[last], cr.convrot_act_backward(y[last], codes[last], scales[last], kind))
