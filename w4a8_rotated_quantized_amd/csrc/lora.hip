@@ -227,7 +227,8 @@ struct ShrinkLds {
 // same bytes from L2 2.6 times slower: 15.5 against 5.9 us for 256 x 512 KB).
 // Within a row's 128 bytes, chunk q lies at position q ^ (row % 8), which
 // spreads the fragment reads over the banks. 8192 rows, 4096 columns: 23.4 us at
-// rank 16 (2.9 TB/s of x), 38 us at rank 64, where the weights, read from L2 for
+// rank 16 (2.9 TB/s of x), 38 us at rank 64 (1.8 TB/s), where nothing is behind
+// the one stage of the rings that is waited for, and the weights, read from L2 for
 // every 32 rows, are twice the bytes of x.
 //
 // WT: the weights lie the other way, [A][C][R]. A load then takes the 16 ranks of
