@@ -214,16 +214,15 @@ def _encode(x, rot):
     v = v.view(rows, tiles * 4, BLOCK)
     top = v.abs().amax(-1)
     power = torch.frexp(top)[1] - 3                               # floor(log2 top) - 2
-    byte = (power + 127).clamp(0, 254)
-    r = v * torch.ldexp(torch.ones_like(top), 127 - byte)[:, :, None]
+    half = int(math.log(rot, 4) + 0.5) if rot else 0              # 1 / sqrt(rot) = 2^-half
+    byte = (power + 127 - half).clamp(0, 254)
+    r = v * torch.ldexp(torch.ones_like(top), 127 - byte - half)[:, :, None]
     a = r.abs()
     # nearest of 0, .5, 1, 1.5, 2, 3, 4, 6; halves to the even code
     code = ((a > 0.25).int() + (a >= 0.75).int() + (a > 1.25).int() + (a >= 1.75).int() + (a > 2.5).int()
             + (a >= 3.5).int() + (a > 5).int())
     code = code + 8 * (r < 0).int()
-    if rot:
-        byte = byte - int(math.log(rot, 4) + 0.5)                 # 1 / sqrt(rot) is a power of two
-    byte = torch.where(top > 0, byte.clamp(0), torch.zeros_like(byte))
+    byte = torch.where(top > 0, byte, torch.zeros_like(byte))
     code = code.view(rows, tiles, TILE)
     packed = (code[:, :, 0::2] + 16 * code[:, :, 1::2]).to(torch.uint8)
     return packed.permute(1, 0, 2).contiguous(), byte.to(torch.uint8).view(rows, tiles, 4).permute(1, 0, 2).contiguous()
