@@ -120,7 +120,7 @@ cr_status convrot_device_check(void);
 
 /* Dispatch counters: kernel launches per entry point (index = order of the
  * entry points below: 0 rotate_quantize, 1 pack, 2 w4a4, 3 w4a8, 4 int8,
- * 5 lora_forward / lora_backward, 6 act_checkpoint / act_backward)
+ * 5 lora_forward / lora_backward, 6 act_checkpoint / act_backward, 7 mxfp4_*)
  * and the count of non-native fallbacks, which is always 0 because no
  * fallback exists. Process-wide, thread-safe. */
 typedef struct cr_counters {
@@ -641,6 +641,62 @@ cr_status convrot_act_checkpoint(const void* z, int64_t ldz, int64_t rows, int64
                                  void* y, int64_t ldy, void* codes, float* scales, hipStream_t stream);
 cr_status convrot_act_backward(const void* dy, int64_t lddy, const void* codes, const float* scales,
                                int64_t rows, int64_t C, cr_act act, void* dz, int64_t lddz, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * mxfp4_quantize / mxfp4_dequantize / mxfp4_gemm - the rotated 4-bit linear in
+ * microscaled floating point: the number format that gfx950's matrix cores take
+ * as it is, beside the INT4 formats above.
+ *
+ * Cites: "Qwen-Image-Edit-2511 - INT4 tensorwise W4A4" page, intro (the same
+ * rotation offline on the weights and online on the activations, dynamic
+ * quantization) and "Qwen-Image-Edit-2511 INT4 (ComfyUI Optimized)", Key
+ * Technical Optimizations (quantize once, then a scaled matmul); OCP
+ * Microscaling Formats (MX) v1.0 for the format.
+ *
+ *   Format: 32 consecutive columns of a row share a power of two 2^(b - 127) (E8M0
+ *   byte b); a code is E2M1: bit 3 the sign, 0..7 for 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   The value is 2^(b - 127) times that of the code.
+ *   Quantization: with A the largest magnitude of the 32 values (of the
+ *   orthonormally rotated ones), b = max(floor(log2 A) - 2 + 127, 0); codes are
+ *   v 2^(127 - b) rounded half to even, values beyond 6 as 6. 32 zeros: b = 0
+ *   and codes 0. A block that holds an infinity or NaN: b = 255 and codes 0,
+ *   which stands for NaN in all 32 places.
+ *   Layout, for activations and weights alike: tiles of 128 columns,
+ *     codes   uint8 [ceil(K/128)][rows][64], two a byte, the even column in the
+ *             low nibble
+ *     scales  uint8 [ceil(K/128)][rows][4], the bytes b of the tile's four blocks
+ *   The columns from K to the end of the last tile have b = 0 and codes 0.
+ *   From rows x K codes in rows of K/2 bytes with rows of K/32 scale bytes (K a multiple of
+ *   128) the layout is a transposition of [rows][K/128] to [K/128][rows].
+ *
+ *   mxfp4_quantize    x bf16 [rows, K], leading dimension ldx; rot_group 0 (none),
+ *                     16, 64, 256 or 1024: each group of rot_group columns is
+ *                     rotated first (float32, in the butterfly order above). With
+ *                     non-finite values under a rotation the group is NaN.
+ *   mxfp4_dequantize  out [rows, K] bf16 or float32, leading dimension ldo: the values
+ *                     of the codes, rotated back (float32, same butterflies, times
+ *                     1/sqrt(rot_group)) and rounded once
+ *   mxfp4_gemm        out[m, n] = sum_k a[m, k] w[n, k] + bias[n]; a and w of the
+ *                     same K and rotation. Products and scales are exact, sums
+ *                     float32 in an order fixed by the sizes; out is rounded once.
+ *                     out CR_OUT_BF16 or CR_OUT_F32, leading dimension ldc; bias
+ *                     optional bf16 [N].
+ *   The gradient of the linear: dx = dy W is mxfp4_gemm of dy and of W^T quantized
+ *   along N (each quantized along what is summed), or a product with the weights
+ *   that mxfp4_dequantize gives back; dx comes out in the rotated basis when W's
+ *   rotation is left in.
+ * Shape: 1 <= rows, M < 2^26; 32 <= K <= 32768, K % 32 == 0 and K % rot_group == 0;
+ * mxfp4_gemm: 1 <= N < 2^26, N % 8 == 0, ceil(M/64) ceil(N/64) < 2^31; leading dimensions
+ * multiples of 8, not below the row length and below 2^31. Outputs must not overlap
+ * inputs. One launch each, no workspace.
+ */
+cr_status mxfp4_quantize(const void* x, int64_t ldx, int64_t rows, int64_t K, int rot_group,
+                         void* codes, void* scales, hipStream_t stream);
+cr_status mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, int rot_group,
+                           void* out, cr_out out_type, int64_t ldo, hipStream_t stream);
+cr_status mxfp4_gemm(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
+                     const void* bias, void* out, cr_out out_type, int64_t ldc,
+                     int64_t M, int64_t N, int64_t K, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -22,6 +22,7 @@ __all__ = [
     "int8_tensorwise_gemm", "convrot_rq_workspace_size", "w4_packed_bytes",
     "ACT", "convrot_lora_forward", "convrot_lora_backward", "convrot_lora_backward_workspace_size",
     "convrot_act_checkpoint", "convrot_act_backward",
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm",
     "get_counters", "reset_counters", "device_check", "status_string",
 ]
 
@@ -107,6 +108,9 @@ _SIGS = {
                                    _vp, _i64, _vp, _i, _i64, _vp, _vp, _i, _i64, _i64, _i64, _vp, _sz, _vp]),
     "convrot_act_checkpoint": (_i, [_vp, _i64, _i64, _i64, _i, _vp, _i64, _vp, _vp, _vp]),
     "convrot_act_backward": (_i, [_vp, _i64, _vp, _vp, _i64, _i64, _i, _vp, _i64, _vp]),
+    "mxfp4_quantize": (_i, [_vp, _i64, _i64, _i64, _i, _vp, _vp, _vp]),
+    "mxfp4_dequantize": (_i, [_vp, _vp, _i64, _i64, _i, _vp, _i, _i64, _vp]),
+    "mxfp4_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i64, _i64, _i64, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -151,7 +155,7 @@ def get_counters():
     lib.convrot_get_counters(ctypes.byref(c))
     return {"rotate_quantize": c.launches[0], "pack": c.launches[1], "w4a4": c.launches[2],
             "w4a8": c.launches[3], "int8": c.launches[4], "lora": c.launches[5], "act": c.launches[6],
-            "fallbacks": c.fallbacks}
+            "mxfp4": c.launches[7], "fallbacks": c.fallbacks}
 
 
 def reset_counters():
@@ -661,3 +665,97 @@ def convrot_act_backward(dy, codes, scales, act, dz=None, stream=None):
     if st:
         _refused(st, "convrot_act_backward", dy=dy, codes=codes, scales=scales, dz=dz)
     return dz
+
+
+# ---------------------------------------------------------------------------
+# the rotated 4-bit linear in microscaled floating point
+#
+# Operands of either side: codes uint8 [ceil(K/128), rows, 64] (E2M1, two a
+# byte) and scales uint8 [ceil(K/128), rows, 4] (a power of two per 32 columns).
+# ---------------------------------------------------------------------------
+_U8 = torch.uint8
+
+
+def _mx_pair(codes, scales, what, index):
+    """Checks codes and scales of one operand: (tiles, rows, address, address)."""
+    if codes.dim() != 3 or codes.shape[2] != 64:
+        raise ValueError(f"{what} codes are uint8 [ceil(K/128), rows, 64]")
+    tiles, rows = codes.shape[:2]
+    return (tiles, rows, _tensor(codes, f"{what} codes", _U8, index, (tiles, rows, 64)),
+            _tensor(scales, f"{what} scales", _U8, index, (tiles, rows, 4)))
+
+
+def mxfp4_quantize(x, rot_group=0, codes=None, scales=None, stream=None):
+    """x: bf16 [rows, K] (rows may lie further apart; K a multiple of 32 and of
+    rot_group) -> (codes, scales) in microscaled 4-bit floating point: codes uint8
+    [ceil(K/128), rows, 64], scales uint8 [ceil(K/128), rows, 4]. rot_group: 0
+    (none), 16, 64, 256 or 1024 columns rotated first. Weights and activations of
+    one product take the same rot_group."""
+    index = _gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x is [rows, K]")
+    rows, K = x.shape
+    px, ldx = _rows(x, "x", _BF16, index, rows, K)
+    tiles = -(-K // 128)
+    with _on(index, stream):
+        if codes is None:
+            codes = torch.empty((tiles, rows, 64), dtype=_U8, device=x.device)
+            pc = codes.data_ptr()
+        else:
+            pc = _tensor(codes, "codes", _U8, index, (tiles, rows, 64))
+        if scales is None:
+            scales = torch.empty((tiles, rows, 4), dtype=_U8, device=x.device)
+            ps = scales.data_ptr()
+        else:
+            ps = _tensor(scales, "scales", _U8, index, (tiles, rows, 4))
+        _hold(stream, x, codes, scales)
+        st = lib.mxfp4_quantize(px, ldx, rows, K, rot_group, pc, ps, _current_stream_handle(index))
+    if st:
+        _refused(st, "mxfp4_quantize", x=x, codes=codes, scales=scales)
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, K, rot_group=0, out_type=OUT.BF16, out=None, stream=None):
+    """The values that the codes of mxfp4_quantize stand for, [rows, K] in
+    out_type, rotated back by rot_group (0: left in the basis of the codes)."""
+    index = _gpu(codes, "codes")
+    tiles, rows, pc, ps = _mx_pair(codes, scales, "the", index)
+    if tiles != -(-K // 128):
+        raise ValueError("K does not fit the codes' tiles")
+    dt = _out_dtype(out_type)
+    with _on(index, stream):
+        if out is None:
+            out, ldo = torch.empty((rows, K), dtype=dt, device=codes.device), K
+            po = out.data_ptr()
+        else:
+            po, ldo = _rows(out, "out", dt, index, rows, K)
+        _hold(stream, codes, scales, out)
+        st = lib.mxfp4_dequantize(pc, ps, rows, K, rot_group, po, out_type, ldo, _current_stream_handle(index))
+    if st:
+        _refused(st, "mxfp4_dequantize", codes=codes, scales=scales, out=out)
+    return out
+
+
+def mxfp4_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, out_type=OUT.BF16, out=None, stream=None):
+    """a w^T + bias of two operands of mxfp4_quantize, a [M, K] (activations) and
+    w [N, K] (weights, N a multiple of 8), quantized with the same rot_group.
+    bias: bf16 [N]. Returns [M, N] in out_type; rows of a given out may lie
+    further apart. Not recorded by autograd."""
+    index = _gpu(a_codes, "a_codes")
+    tiles, M, pa, pas = _mx_pair(a_codes, a_scales, "a", index)
+    w_tiles, N, pw, pws = _mx_pair(w_codes, w_scales, "w", index)
+    if tiles != w_tiles:
+        raise ValueError("a and w have different K")
+    pb = None if bias is None else _tensor(bias, "bias", _BF16, index, (N,))
+    dt = _out_dtype(out_type)
+    with _on(index, stream):
+        if out is None:
+            out, ldc = torch.empty((M, N), dtype=dt, device=a_codes.device), N
+            po = out.data_ptr()
+        else:
+            po, ldc = _rows(out, "out", dt, index, M, N)
+        _hold(stream, a_codes, a_scales, w_codes, w_scales, bias, out)
+        st = lib.mxfp4_gemm(pa, pas, pw, pws, pb, po, out_type, ldc, M, N, tiles * 128, _current_stream_handle(index))
+    if st:
+        _refused(st, "mxfp4_gemm", a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out)
+    return out

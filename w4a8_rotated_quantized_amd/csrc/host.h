@@ -10,7 +10,7 @@
 namespace cr {
 
 // index of a counter in cr_counters.launches
-enum HostEntry { HE_RQ = 0, HE_PACK = 1, HE_W4A4 = 2, HE_W4A8 = 3, HE_INT8 = 4, HE_LORA = 5, HE_ACT = 6 };
+enum HostEntry { HE_RQ = 0, HE_PACK = 1, HE_W4A4 = 2, HE_W4A8 = 3, HE_INT8 = 4, HE_LORA = 5, HE_ACT = 6, HE_MX = 7 };
 
 cr_status host_device_check();
 // names the call for the launch log: its sizes and format arguments
