@@ -120,7 +120,8 @@ cr_status convrot_device_check(void);
 
 /* Dispatch counters: kernel launches per entry point (index = order of the
  * entry points below: 0 rotate_quantize, 1 pack, 2 w4a4, 3 w4a8, 4 int8,
- * 5 lora_forward / lora_backward, 6 act_checkpoint / act_backward, 7 mxfp4_*)
+ * 5 lora_forward / lora_backward / adamw_*, 6 act_checkpoint / act_backward /
+ * layer_norm_*, 7 mxfp4_*)
  * and the count of non-native fallbacks, which is always 0 because no
  * fallback exists. Process-wide, thread-safe. */
 typedef struct cr_counters {
@@ -697,6 +698,121 @@ cr_status mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, 
 cr_status mxfp4_gemm(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
                      const void* bias, void* out, cr_out out_type, int64_t ldc,
                      int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * convrot_layer_norm_forward / convrot_layer_norm_backward - the norm in front
+ * of the quantized projections, with one weight and bias or one pair per
+ * sequence of the batch (the adaLN modulation that the modulation layers produce),
+ * and its gradients.
+ *
+ * Cites: "Qwen-Image-Edit-2511 - INT4 tensorwise W4A4" page, intro (the
+ * adaLN modulation layers of the block).
+ *
+ *   rows m of sequence s are [seg_offsets[s], seg_offsets[s+1]):
+ *     mean[m] = sum_c x[m, c] / C,  rstd[m] = 1 / sqrt(sum_c (x[m, c] - mean[m])^2 / C + eps)
+ *     xh[m, c] = (x[m, c] - mean[m]) rstd[m]
+ *     y[m, c] = xh[m, c] (weight[s, c] + one_plus) + bias[s, c]
+ *   backward, for the gradient dy of y, with g = dy (weight[s] + one_plus):
+ *     dx[m, c] = dx_base[m, c] + rstd[m] (g[m, c] - sum_c g / C - xh[m, c] sum_c (g xh) / C)
+ *     d_weight[s, c] = sum_m dy[m, c] xh[m, c],  d_bias[s, c] = sum_m dy[m, c]    over the rows of s
+ *   All of it in float32; y and dx are rounded once. No atomics on values: the rows'
+ *   sums are split into parts that are added in order, fixed by the sizes and offsets.
+ *   A row's y and dx do not depend on other rows; what is not finite in a row
+ *   reaches d_weight and d_bias of its sequence only.
+ *
+ *   x            bf16 or float32 (x_type) [rows, C], leading dimension ldx
+ *   weight, bias bf16 or float32 (affine_type, both the same) [S, C]; each may be
+ *                NULL (weight: 1 whatever one_plus is, bias: 0)
+ *   one_plus     0, or 1: the weight is given without its 1 (adaLN's scale)
+ *   seg_offsets  int32 [S + 1] on the device, ascending; NULL with S = 1: all rows
+ *                are one sequence. Empty sequences are fine. One below an earlier one
+ *                counts as that earlier one. Rows before the first or behind the last
+ *                offset are in no sequence: their places in y, mean, rstd and dx are left
+ *                as they are, and nothing of them is read.
+ *   y, dx        CR_OUT_BF16 or CR_OUT_F32, leading dimensions ldy, lddx
+ *   mean, rstd   float32 [rows], written by the forward and read by the backward
+ *   dy           bf16 or float32 (dy_type), leading dimension lddy
+ *   dx_base      optional, of dx's type (the gradient that reaches x past the norm);
+ *                may be dx itself (ldb == lddx). Other overlaps are not allowed.
+ *   dx, d_weight, d_bias   each may be NULL if not wanted, not all of them. d_weight and
+ *                d_bias are float32 [S, C], written whole (zeros for empty sequences),
+ *                or added to with accumulate != 0.
+ *   workspace    convrot_layer_norm_backward_workspace_size(...) bytes (0 where the call
+ *                refuses the sizes), needed for d_weight and d_bias; any contents. Calls
+ *                that share one must be ordered on one stream.
+ * Shape: 1 <= rows < 2^26, C a multiple of 8 from 8 to 16384, 1 <= S <= 4096, leading
+ * dimensions multiples of 8, not below C and below 2^31. Forward one launch,
+ * backward one or two.
+ */
+cr_status convrot_layer_norm_forward(const void* x, cr_out x_type, int64_t ldx, const void* weight, const void* bias,
+                                     cr_out affine_type, int one_plus, const int32_t* seg_offsets, int S, double eps,
+                                     void* y, cr_out y_type, int64_t ldy, float* mean, float* rstd,
+                                     int64_t rows, int64_t C, hipStream_t stream);
+
+size_t convrot_layer_norm_backward_workspace_size(int64_t rows, int64_t C, int S);
+
+cr_status convrot_layer_norm_backward(const void* dy, cr_out dy_type, int64_t lddy, const void* x, cr_out x_type,
+                                      int64_t ldx, const float* mean, const float* rstd, const void* weight,
+                                      cr_out affine_type, int one_plus, const int32_t* seg_offsets, int S,
+                                      const void* dx_base, int64_t ldb, void* dx, cr_out dx_type, int64_t lddx,
+                                      float* d_weight, float* d_bias, int accumulate, int64_t rows, int64_t C,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * convrot_adamw_step / convrot_adamw_moments - an optimizer step over many
+ * tensors at once (the adapters that convrot_lora_backward gives the gradients
+ * of), with its moments in float32 or in 8 bits.
+ *
+ *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *   copy = p rounded to bf16. Each operation rounds once to float32; the constants are
+ *   computed in float64 and rounded.
+ *
+ *   tensors      HOST array of `count` entries, read before the call returns:
+ *     param      float32 [n], updated
+ *     grad       bf16 or float32 (grad_type) [n]
+ *     exp_avg, exp_avg_sq   the moments m and v, updated. state_bits 32: float32 [n].
+ *                8: int8 [n] and uint8 [n] codes with
+ *     avg_scales, sq_scales   float32 [ceil(n / 256)], one scale for 256 consecutive elements
+ *                (4-byte aligned; not read for 32 bits):
+ *                m = s (c / 127) |c / 127|,  sqrt(v) = s (c / 255)^2, s the largest
+ *                magnitude among the 256. New codes are floor(most sqrt(|value| / s) + u) with
+ *                most = 127 or 255 and u in [0, 1) from the hash below (so a code is right
+ *                on average), at least 1 where sqrt(v) > 0, signed like m. All zeros: s = 0. Where
+ *                an infinity or NaN is among the 256, s is NaN and the codes 0.
+ *     copy       bf16 [n] or NULL: receives the new param
+ *     n          elements, 0 (skipped) to 2^31 - 1
+ *                The tensors must not overlap.
+ *   hash         with 32-bit arithmetic mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15;
+ *                x *= 0xBB67AE85; x ^= x >> 16. Element i of tensor j (both from 0):
+ *                h = mix(mix(i) ^ mix(seed + 0x9E3779B9 (j + 1))); u is (h & 0xFFFF) / 2^16 for
+ *                m and (h >> 16) / 2^16 for sqrt(v). Give every step another seed.
+ *   grad_scale   optional device float32 [1] (a gradient norm's clip, a loss scale's
+ *                inverse), read by the kernels; 4-byte aligned
+ *   lr, step and seed are taken by value: a captured graph replays those of the capture.
+ *   convrot_adamw_moments: m and v of 8-bit entries as float32, entry after entry
+ *                in exp_avg_out and exp_avg_sq_out [sum of n] (param, grad and copy of the
+ *                entries are not read).
+ * 1 <= count <= 65536, step >= 1, lr, eps and weight_decay >= 0, 0 <= beta < 1. One launch for
+ * up to 48 entries, in the list's order; entries of a list may hold the same tensor
+ * only once.
+ */
+typedef struct cr_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* avg_scales;
+  float* sq_scales;
+  void* copy;
+  int64_t n;
+} cr_adamw_tensor;
+
+cr_status convrot_adamw_step(const cr_adamw_tensor* tensors, int count, cr_out grad_type, int state_bits,
+                             double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                             const float* grad_scale, uint32_t seed, hipStream_t stream);
+cr_status convrot_adamw_moments(const cr_adamw_tensor* tensors, int count, float* exp_avg_out, float* exp_avg_sq_out,
+                                hipStream_t stream);
 
 #ifdef __cplusplus
 }

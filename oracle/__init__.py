@@ -22,10 +22,11 @@ Modules, in the order the path runs:
   linear    - epilogues and the composed reference linears
   adapters  - batched low-rank adapters with gradients, 8-bit activation checkpoints
   mx        - microscaled 4-bit floating point: quantization, layout, product
+  training  - layer norm and its gradients, the AdamW step
 
 Every function states the passage it follows, or, where the pages are silent,
 the reading taken and why. The pins that tie this oracle to the mathematics
 and to the pages (closed forms, invariants, brute force on tiny inputs,
 constructed rounding ties) live in tests/test_oracle_*.py.
 """
-from . import hadamard, quant, pack, gemm, linear, adapters, mx  # noqa: F401
+from . import hadamard, quant, pack, gemm, linear, adapters, mx, training  # noqa: F401

@@ -8,6 +8,7 @@ ConvRotError with the library's status text.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -23,6 +24,8 @@ __all__ = [
     "ACT", "convrot_lora_forward", "convrot_lora_backward", "convrot_lora_backward_workspace_size",
     "convrot_act_checkpoint", "convrot_act_backward",
     "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm",
+    "convrot_layer_norm_forward", "convrot_layer_norm_backward", "convrot_layer_norm_backward_workspace_size",
+    "convrot_adamw_step", "convrot_adamw_moments",
     "get_counters", "reset_counters", "device_check", "status_string",
 ]
 
@@ -111,6 +114,13 @@ _SIGS = {
     "mxfp4_quantize": (_i, [_vp, _i64, _i64, _i64, _i, _vp, _vp, _vp]),
     "mxfp4_dequantize": (_i, [_vp, _vp, _i64, _i64, _i, _vp, _i, _i64, _vp]),
     "mxfp4_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i64, _i64, _i64, _i64, _vp]),
+    "convrot_layer_norm_forward": (_i, [_vp, _i, _i64, _vp, _vp, _i, _i, _vp, _i, ctypes.c_double, _vp, _i, _i64, _vp, _vp,
+                                        _i64, _i64, _vp]),
+    "convrot_layer_norm_backward_workspace_size": (_sz, [_i64, _i64, _i]),
+    "convrot_layer_norm_backward": (_i, [_vp, _i, _i64, _vp, _i, _i64, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _i64, _vp, _i,
+                                         _i64, _vp, _vp, _i, _i64, _i64, _vp, _sz, _vp]),
+    "convrot_adamw_step": (_i, [_vp, _i, _i, _i, *[ctypes.c_double] * 5, _i64, _vp, ctypes.c_uint32, _vp]),
+    "convrot_adamw_moments": (_i, [_vp, _i, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -759,3 +769,220 @@ def mxfp4_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, out_type=OUT.BF1
     if st:
         _refused(st, "mxfp4_gemm", a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out)
     return out
+
+
+# ---------------------------------------------------------------------------
+# layer norm and its gradients
+# ---------------------------------------------------------------------------
+def _float_type(t, what):
+    """OUT number of a bf16 or float32 tensor."""
+    if t.dtype is _BF16:
+        return OUT.BF16
+    if t.dtype is _F32:
+        return OUT.F32
+    raise ValueError(f"{what} must be bfloat16 or float32")
+
+
+def _affine(weight, bias, seg_offsets, index, C):
+    """Checks weight, bias ([C], or [S, C] with seg_offsets [S + 1]): (S, type, addresses of the three)."""
+    S, po = 1, None
+    if seg_offsets is not None:
+        if seg_offsets.dim() != 1:
+            raise ValueError("seg_offsets is int32 [S + 1]")
+        S = seg_offsets.shape[0] - 1
+        po = _tensor(seg_offsets, "seg_offsets", _I32, index, (S + 1,))
+    shape = (C,) if seg_offsets is None else (S, C)
+    first = weight if weight is not None else bias
+    kind = OUT.F32 if first is None else _float_type(first, "weight and bias")
+    pw = None if weight is None else _tensor(weight, "weight", _OUT_DTYPE[kind], index, shape)
+    pb = None if bias is None else _tensor(bias, "bias", _OUT_DTYPE[kind], index, shape)
+    return S, kind, pw, pb, po
+
+
+def convrot_layer_norm_forward(x, weight=None, bias=None, seg_offsets=None, eps=1e-6, one_plus=False, out_type=OUT.BF16,
+                               out=None, mean=None, rstd=None, stream=None):
+    """y = (x - mean) rstd (weight + one_plus) + bias over the last dimension of x
+    [M, C] (bf16 or float32; C a multiple of 8). weight, bias: [C], or [S, C]
+    with seg_offsets int32 [S + 1], a pair for the rows seg_offsets[s] ..
+    seg_offsets[s+1] of each sequence (adaLN: one_plus=True with the scales as weight). Rows in no
+    sequence are left as they are in the given outputs. Returns (y in out_type, mean, rstd):
+    mean and rstd float32 [M] are what convrot_layer_norm_backward reads. Not
+    recorded by autograd."""
+    index = _gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x is [M, C]")
+    M, C = x.shape
+    x_type, dt = _float_type(x, "x"), _out_dtype(out_type)
+    px, ldx = _rows(x, "x", x.dtype, index, M, C)
+    S, kind, pw, pb, po = _affine(weight, bias, seg_offsets, index, C)
+    with _on(index, stream):
+        if out is None:
+            out, ldy = torch.empty((M, C), dtype=dt, device=x.device), C
+            py = out.data_ptr()
+        else:
+            py, ldy = _rows(out, "out", dt, index, M, C)
+        mean = torch.empty((M,), dtype=_F32, device=x.device) if mean is None else mean
+        rstd = torch.empty((M,), dtype=_F32, device=x.device) if rstd is None else rstd
+        pm, pr = _tensor(mean, "mean", _F32, index, (M,)), _tensor(rstd, "rstd", _F32, index, (M,))
+        _hold(stream, x, weight, bias, seg_offsets, out, mean, rstd)
+        st = lib.convrot_layer_norm_forward(px, x_type, ldx, pw, pb, kind, int(bool(one_plus)), po, S, eps, py, out_type, ldy,
+                                            pm, pr, M, C, _current_stream_handle(index))
+    if st:
+        _refused(st, "convrot_layer_norm_forward", x=x, weight=weight, bias=bias, seg_offsets=seg_offsets, out=out, mean=mean,
+                 rstd=rstd)
+    return out, mean, rstd
+
+
+def convrot_layer_norm_backward_workspace_size(M, C, S) -> int:
+    return lib.convrot_layer_norm_backward_workspace_size(M, C, S)
+
+
+def convrot_layer_norm_backward(dy, x, mean, rstd, weight=None, seg_offsets=None, one_plus=False, dx_base=None,
+                                dx_type=OUT.BF16, dx=None, d_weight=None, d_bias=None, want_dx=True, want_weights=True,
+                                accumulate=False, workspace=None, stream=None):
+    """Gradients of convrot_layer_norm_forward for dy [M, C] (bf16 or float32).
+    Returns (dx, d_weight, d_bias): dx = dx_base + the input's gradient in
+    dx_type (None with want_dx=False), d_weight and d_bias float32 shaped like the
+    weight, [C] or [S, C] (None with want_weights=False; accumulate=True adds to the
+    given ones)."""
+    index = _gpu(dy, "dy")
+    if dy.dim() != 2:
+        raise ValueError("dy is [M, C]")
+    M, C = dy.shape
+    dev, dt = dy.device, _out_dtype(dx_type)
+    if not want_dx and not want_weights:
+        raise ValueError("nothing is wanted")
+    dy_type, x_type = _float_type(dy, "dy"), _float_type(x, "x")
+    pdy, lddy = _rows(dy, "dy", dy.dtype, index, M, C)
+    px, ldx = _rows(x, "x", x.dtype, index, M, C)
+    pm, pr = _tensor(mean, "mean", _F32, index, (M,)), _tensor(rstd, "rstd", _F32, index, (M,))
+    S, kind, pw, _, po = _affine(weight, None, seg_offsets, index, C)
+    shape = (C,) if seg_offsets is None else (S, C)
+    pb = pdx = pgw = pgb = None
+    ldb = lddx = C
+    if accumulate and want_weights and (d_weight is None or d_bias is None):
+        raise ValueError("accumulate adds to given d_weight and d_bias")
+    if want_dx and dx_base is not None:
+        pb, ldb = _rows(dx_base, "dx_base", dt, index, M, C)
+    with _on(index, stream):
+        if want_dx and dx is None:
+            dx = torch.empty((M, C), dtype=dt, device=dev)
+            pdx = dx.data_ptr()
+        elif want_dx:
+            pdx, lddx = _rows(dx, "dx", dt, index, M, C)
+        pws, wsb = None, 0
+        if want_weights:
+            d_weight = torch.empty(shape, dtype=_F32, device=dev) if d_weight is None else d_weight
+            d_bias = torch.empty(shape, dtype=_F32, device=dev) if d_bias is None else d_bias
+            pgw, pgb = _tensor(d_weight, "d_weight", _F32, index, shape), _tensor(d_bias, "d_bias", _F32, index, shape)
+            if workspace is None:
+                need = lib.convrot_layer_norm_backward_workspace_size(M, C, S)
+                workspace = torch.empty(max(need, 16), dtype=_U8, device=dev)
+            elif workspace.get_device() != index or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be contiguous on GPU {index}")
+            pws, wsb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            _hold(stream, d_weight, d_bias, workspace)
+        if want_dx:
+            _hold(stream, dx_base, dx)
+        _hold(stream, dy, x, mean, rstd, weight, seg_offsets)
+        st = lib.convrot_layer_norm_backward(pdy, dy_type, lddy, px, x_type, ldx, pm, pr, pw, kind, int(bool(one_plus)), po, S,
+                                             pb, ldb, pdx, dx_type, lddx, pgw, pgb, int(bool(accumulate)), M, C, pws, wsb,
+                                             _current_stream_handle(index))
+    if st:
+        read = dict(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, seg_offsets=seg_offsets)
+        if want_weights:
+            read.update(d_weight=d_weight, d_bias=d_bias, workspace=workspace)
+        if want_dx:
+            read.update(dx_base=dx_base, dx=dx)
+        _refused(st, "convrot_layer_norm_backward", **read)
+    return (dx if want_dx else None), (d_weight if want_weights else None), (d_bias if want_weights else None)
+
+
+# ---------------------------------------------------------------------------
+# optimizer step over many tensors
+# ---------------------------------------------------------------------------
+def _list(tensors, what, dtype, index, sizes):
+    """Addresses of a list of dense tensors; dtype, GPU, sizes and contiguity checked list-wise."""
+    if len(tensors) != len(sizes) or [t.numel() for t in tensors] != sizes:
+        raise ValueError(f"{what} must hold one tensor for each of params, of its size")
+    if {t.dtype for t in tensors} != {dtype} or {t.get_device() for t in tensors} != {index} or not all(
+            [t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{what} must be contiguous {dtype} tensors on GPU {index}")
+    return [t.data_ptr() for t in tensors]
+
+
+def _table(*columns):
+    """The entries of cr_adamw_tensor, 8 words each, from its eight columns (None: null)."""
+    n = len(columns[-1])
+    flat = array.array("q", bytes(64 * n))
+    for i, c in enumerate(columns):
+        if c is not None:
+            flat[i::8] = array.array("q", c)
+    return flat
+
+
+def _moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, index, sizes):
+    """Addresses of the moments and their scales (None, None for float32 moments)."""
+    if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
+        raise ValueError("8-bit moments have exp_avg_scales and exp_avg_sq_scales")
+    if exp_avg_scales is None:
+        return (_list(exp_avgs, "exp_avgs", _F32, index, sizes), _list(exp_avg_sqs, "exp_avg_sqs", _F32, index, sizes),
+                None, None)
+    blocks = [-(-n // 256) for n in sizes]
+    return (_list(exp_avgs, "exp_avgs", _I8, index, sizes), _list(exp_avg_sqs, "exp_avg_sqs", _U8, index, sizes),
+            _list(exp_avg_scales, "exp_avg_scales", _F32, index, blocks),
+            _list(exp_avg_sq_scales, "exp_avg_sq_scales", _F32, index, blocks))
+
+
+def convrot_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
+                       copies=None, grad_scale=None, exp_avg_scales=None, exp_avg_sq_scales=None, seed=0, stream=None):
+    """One AdamW step over lists of tensors, in place: params float32, grads bf16
+    or float32 (all of one type), exp_avgs and exp_avg_sqs float32, or int8 and
+    uint8 with exp_avg_scales and exp_avg_sq_scales float32 [ceil(n / 256)] (the
+    8-bit moments; start them as zeros; give each step another seed). copies:
+    bf16 tensors that receive the new params. grad_scale: float32 [1] on the GPU, multiplies
+    the gradients. step counts from 1. A tensor may stand in the lists once."""
+    if not params:
+        raise ValueError("params is empty")
+    index = _gpu(params[0], "params")
+    sizes = [t.numel() for t in params]
+    pp = _list(params, "params", _F32, index, sizes)
+    grad_type = _float_type(grads[0], "grads") if len(grads) else OUT.F32
+    pg = _list(grads, "grads", _OUT_DTYPE[grad_type], index, sizes)
+    pm, pv, pms, pvs = _moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, index, sizes)
+    pc = None if copies is None else _list(copies, "copies", _BF16, index, sizes)
+    pgs = None if grad_scale is None else _tensor(grad_scale, "grad_scale", _F32, index, (1,))
+    table = _table(pp, pg, pm, pv, pms, pvs, pc, sizes)
+    with _on(index, stream):
+        for held in (params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales, (grad_scale,)):
+            if stream is not None and held is not None:
+                _hold(stream, *held)
+        st = lib.convrot_adamw_step(table.buffer_info()[0], len(sizes), grad_type, 32 if pms is None else 8, lr, beta1, beta2,
+                                    eps, weight_decay, step, pgs, seed & 0xFFFFFFFF, _current_stream_handle(index))
+    _check(st, "convrot_adamw_step")
+
+
+def convrot_adamw_moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, exp_avg_out=None, exp_avg_sq_out=None,
+                          stream=None):
+    """8-bit moments of convrot_adamw_step as float32 (for a checkpoint, or to go on
+    with float32 moments): (m, v), one tensor after another in two flat tensors."""
+    if not exp_avgs:
+        raise ValueError("exp_avgs is empty")
+    index = _gpu(exp_avgs[0], "exp_avgs")
+    sizes = [t.numel() for t in exp_avgs]
+    if exp_avg_scales is None or exp_avg_sq_scales is None:
+        raise ValueError("8-bit moments have exp_avg_scales and exp_avg_sq_scales")
+    pm, pv, pms, pvs = _moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, index, sizes)
+    total = sum(sizes)
+    table = _table(None, None, pm, pv, pms, pvs, None, sizes)
+    with _on(index, stream):
+        dev = exp_avgs[0].device
+        exp_avg_out = torch.empty((total,), dtype=_F32, device=dev) if exp_avg_out is None else exp_avg_out
+        exp_avg_sq_out = torch.empty((total,), dtype=_F32, device=dev) if exp_avg_sq_out is None else exp_avg_sq_out
+        po = _tensor(exp_avg_out, "exp_avg_out", _F32, index, (total,))
+        pq = _tensor(exp_avg_sq_out, "exp_avg_sq_out", _F32, index, (total,))
+        for held in (exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, (exp_avg_out, exp_avg_sq_out)):
+            _hold(stream, *held)
+        st = lib.convrot_adamw_moments(table.buffer_info()[0], len(sizes), po, pq, _current_stream_handle(index))
+    _check(st, "convrot_adamw_moments")
+    return exp_avg_out, exp_avg_sq_out

@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
 SOURCES = ["rq.hip", "pack.hip", "merge.hip", "gemm_w4a4.hip", "gemm_int.hip", "gemm_w4a8.hip", "gemm_f6.hip", "abi.cpp",
-           "lora.hip", "act.hip", "adapter_abi.cpp", "mx.hip", "gemm_mx.hip", "block_abi.cpp"]
+           "lora.hip", "act.hip", "adapter_abi.cpp", "mx.hip", "gemm_mx.hip", "norm.hip", "adamw.hip", "block_abi.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,0 +1,405 @@
+// Layer norm of rows with one weight and bias, or one pair per sequence of
+// the batch (adaLN modulation), and its gradients (gfx950).
+//
+//   mean = sum x / C,  rstd = 1 / sqrt(sum (x - mean)^2 / C + eps)
+//   xh = (x - mean) rstd,  y = xh w + b
+//   g = dy w,  dx = base + rstd (g - sum g / C - xh sum (g xh) / C)
+//   dw = sum over the sequence's rows of dy xh,  db = the same of dy
+// Both sums of a row run over the values held in registers: x is read once,
+// and the variance is that of the differences, which x^2 - mean^2 would lose.
+//
+// A row is shared by W waves (1, 4 or 8), each lane holding eight consecutive
+// columns at a time, V times. The memory rate bounds both directions, so a wave
+// keeps a whole row's loads in flight at once.
+#include "block.h"
+#include "common.h"
+
+namespace cr {
+
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+CR_DEV uint32_t pair_of(float lo, float hi) { return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi}); }
+
+// eight consecutive values as they lie in memory
+template <bool F32>
+struct Eight {
+  u32x4 w[F32 ? 2 : 1];
+  CR_DEV void load(const void* base, int64_t at) {
+    if constexpr (F32) {
+      const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + at);
+      w[0] = s[0];
+      w[1] = s[1];
+    } else {
+      w[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at);
+    }
+  }
+  CR_DEV float get(int e) const {
+    if constexpr (F32) return __uint_as_float(w[e >> 2][e & 3]);
+    else return (e & 1) ? bf16_hi(w[0][e >> 1]) : bf16_lo(w[0][e >> 1]);
+  }
+};
+
+template <bool F32>
+CR_DEV void store8(void* base, int64_t at, const float (&v)[8]) {
+  if constexpr (F32) {
+    v4f* d = reinterpret_cast<v4f*>(static_cast<float*>(base) + at);
+    d[0] = v4f{v[0], v[1], v[2], v[3]};
+    d[1] = v4f{v[4], v[5], v[6], v[7]};
+  } else {
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at) =
+        u32x4{pair_of(v[0], v[1]), pair_of(v[2], v[3]), pair_of(v[4], v[5]), pair_of(v[6], v[7])};
+  }
+}
+
+// weights and biases are bf16 or float32 by a run-time flag: they come from L2
+CR_DEV void load_affine(const void* base, int f32, int64_t at, float (&v)[8]) {
+  if (f32) {
+    const v4f* s = reinterpret_cast<const v4f*>(static_cast<const float*>(base) + at);
+    const v4f a = s[0], b = s[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  } else {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+  }
+}
+
+CR_DEV float wave_sum(float v) {
+  v += dpp_f<DPP_QUAD_1032>(v);
+  v += dpp_f<DPP_QUAD_2301>(v);
+  v += dpp_f<DPP_HALF_MIRROR>(v);
+  v += dpp_f<DPP_ROW_ROR8>(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
+// the sum over the W waves of a row, in a fixed order; `slot` alternates so that one barrier is enough
+template <int W>
+CR_DEV float row_sum(float v, float* lds, int wave, int slot) {
+  v = wave_sum(v);
+  if constexpr (W > 1) {
+    float* at = lds + slot * W;
+    if ((threadIdx.x & 63) == 0) at[wave] = v;
+    __syncthreads();
+    v = at[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += at[w];
+  }
+  return v;
+}
+
+// The sequence of a row among S offsets off[0..S], by one wave: the first s whose
+// end off[s + 1] lies behind the row, 64 at a time; S: none. An offset below an
+// earlier one so counts as that earlier one, and off[s + 1] > row for the s found.
+CR_DEV int sequence_of(const int32_t* off, int S, int64_t row, int l) {
+  for (int at = 0; at < S; at += 64) {
+    const uint64_t behind = __ballot(at + l < S && off[1 + min(at + l, S - 1)] > row);
+    if (behind) return at + __builtin_ctzll(behind);
+  }
+  return S;
+}
+
+// Forward. W == 1: four rows a block, a wave each; otherwise a row a block.
+template <int W, int V, bool XF, bool YF>
+__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(NormForward p) {
+  __shared__ float lds[2 * W];
+  const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  if (row >= p.rows) return;
+  int s = 0;
+  if (p.off) {
+    s = sequence_of(p.off, p.S, row, l);
+    if (s >= p.S || row < p.off[0]) return;           // in no sequence: left as it is
+  }
+  const int lane = W == 1 ? l : threadIdx.x;
+  Eight<XF> x[V];
+  const int64_t at = row * p.ldx;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * W * 64 + lane) * 8;
+    if (c < p.C) x[v].load(p.x, at + c);
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if ((v * W * 64 + lane) * 8 < p.C)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += x[v].get(e);
+  const float mean = row_sum<W>(sum, lds, wave, 0) * p.inv_c;
+  float sq = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if ((v * W * 64 + lane) * 8 < p.C)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = x[v].get(e) - mean;
+        sq = __builtin_fmaf(d, d, sq);
+      }
+  const float rstd = 1.f / sqrtf(row_sum<W>(sq, lds, wave, 1) * p.inv_c + p.eps);
+  if (lane == 0) {
+    p.mean[row] = mean;
+    p.rstd[row] = rstd;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * W * 64 + lane) * 8;
+    if (c >= p.C) continue;
+    float y[8], w[8], b[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (x[v].get(e) - mean) * rstd;
+    if (p.w) {
+      load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= w[e] + p.plus;
+    }
+    if (p.b) {
+      load_affine(p.b, p.w_f32, (int64_t)s * p.C + c, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] += b[e];
+    }
+    store8<YF>(p.y, row * p.ldy + c, y);
+  }
+}
+
+// Backward. The rows are cut into p.parts stretches of p.part_rows, a block each. It
+// walks its rows with the sums for dw and db of its columns in registers and
+// writes them out where a sequence ends: part q's share of sequence s goes to
+// slot q + s of the workspace, which no other pair has, as both only grow along the
+// rows. The last launch adds a sequence's slots in order.
+// W == 1: four waves take the block's rows in turn, each with sums of its own,
+// added through LDS before they are written.
+template <int W, int V, bool XF, bool DF>
+__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(NormBackward p) {
+  constexpr int RPB = W == 1 ? 4 : 1;
+  __shared__ float lds[4 * W];
+  __shared__ float4 join[W == 1 ? 3 * 64 * 4 : 1];
+  const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = W == 1 ? l : threadIdx.x;
+  int64_t row = (int64_t)blockIdx.x * p.part_rows;
+  const int64_t end = imin64(row + p.part_rows, p.rows);
+  if (p.off && row < p.off[0]) row = p.off[0];         // rows in no sequence: nothing is read or written
+  int slot = 0;
+  while (row < end) {
+    const int s = p.off ? sequence_of(p.off, p.S, row, l) : 0;
+    if (s >= p.S) return;
+    const int64_t stop = p.off ? imin64(end, p.off[s + 1]) : end;
+    float dw[V][8], db[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[v][e] = db[v][e] = 0.f;
+
+    for (int64_t r = row + (W == 1 ? wave : 0); r < stop; r += RPB) {
+      Eight<XF> x[V];
+      Eight<DF> dy[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * W * 64 + lane) * 8;
+        if (c < p.C) {
+          x[v].load(p.x, r * p.ldx + c);
+          dy[v].load(p.dy, r * p.lddy + c);
+        }
+      }
+      const float mean = p.mean[r], rstd = p.rstd[r];
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * W * 64 + lane) * 8;
+        if (c >= p.C) continue;
+        float w[8];
+        if (p.w) load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = dy[v].get(e), xh = (x[v].get(e) - mean) * rstd;
+          const float g = p.w ? d * (w[e] + p.plus) : d;
+          a += g;
+          b = __builtin_fmaf(g, xh, b);
+          dw[v][e] = __builtin_fmaf(d, xh, dw[v][e]);
+          db[v][e] += d;
+        }
+      }
+      if (p.dx) {
+        a = row_sum<W>(a, lds, wave, slot) * p.inv_c;
+        b = row_sum<W>(b, lds, wave, slot + 1) * p.inv_c;
+        slot ^= 2;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int c = (v * W * 64 + lane) * 8;
+          if (c >= p.C) continue;
+          float w[8], o[8];
+          if (p.w) load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float d = dy[v].get(e), xh = (x[v].get(e) - mean) * rstd;
+            const float g = p.w ? d * (w[e] + p.plus) : d;
+            o[e] = rstd * (g - a - xh * b);
+          }
+          if (p.base) {
+            float t[8];
+            load_affine(p.base, p.dx_f32, r * p.ldb + c, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += t[e];
+          }
+          if (p.dx_f32) store8<true>(p.dx, r * p.lddx + c, o);
+          else store8<false>(p.dx, r * p.lddx + c, o);
+        }
+      }
+    }
+    if (p.parts_w) {
+      const int64_t at = ((int64_t)blockIdx.x + s) * p.C;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * W * 64 + lane) * 8;
+        if constexpr (W == 1) {
+          __syncthreads();
+          if (wave) {
+            float4* to = join + (wave - 1) * 64 * 4;
+            to[l] = float4{dw[v][0], dw[v][1], dw[v][2], dw[v][3]};
+            to[64 + l] = float4{dw[v][4], dw[v][5], dw[v][6], dw[v][7]};
+            to[128 + l] = float4{db[v][0], db[v][1], db[v][2], db[v][3]};
+            to[192 + l] = float4{db[v][4], db[v][5], db[v][6], db[v][7]};
+          }
+          __syncthreads();
+          if (wave == 0) {
+#pragma unroll
+            for (int o = 0; o < 3; ++o)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 t = join[o * 256 + q * 64 + l];
+                float* d = (q < 2 ? dw[v] : db[v]) + (q & 1) * 4;
+                d[0] += t.x;
+                d[1] += t.y;
+                d[2] += t.z;
+                d[3] += t.w;
+              }
+          }
+        }
+        if (c < p.C && (W > 1 || wave == 0)) {
+          store8<true>(p.parts_w, at + c, dw[v]);
+          store8<true>(p.parts_b, at + c, db[v]);
+        }
+      }
+    }
+    row = stop;
+  }
+}
+
+// dw and db of sequence blockIdx.y: the slots of the parts that hold its rows, in order.
+// 256 threads: 32 columns x 8 shares of the slots.
+__global__ __launch_bounds__(256) void norm_join_kernel(NormBackward p) {
+  __shared__ float lds[8][32];
+  const int s = blockIdx.y;
+  const int col = threadIdx.x & 31, share = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + col;
+  int64_t lo = 0, hi = p.rows;
+  if (p.off) {
+    // the sequence begins at the largest offset up to off[s]
+    __shared__ int begin;
+    if (threadIdx.x == 0) begin = 0;
+    __syncthreads();
+    int m = 0;
+    for (int i = threadIdx.x; i <= s; i += 256) m = max(m, p.off[i]);
+    atomicMax(&begin, m);
+    __syncthreads();
+    lo = begin;
+    hi = imin64(p.off[s + 1], p.rows);
+  }
+  const float* from = blockIdx.z ? p.parts_b : p.parts_w;
+  float* to = blockIdx.z ? p.db : p.dw;
+  if (!to) return;
+  float sum = 0.f;
+  if (lo < hi && c < p.C) {
+    const int first = (int)(lo / p.part_rows), last = (int)((hi - 1) / p.part_rows);
+    const int n = last - first + 1, per = (n + 7) / 8;
+    const int q1 = min(first + (share + 1) * per, last + 1);
+    for (int q = first + share * per; q < q1; ++q) sum += from[((int64_t)q + s) * p.C + c];
+  }
+  lds[share][col] = sum;
+  __syncthreads();
+  if (share == 0 && c < p.C) {
+#pragma unroll
+    for (int o = 1; o < 8; ++o) sum += lds[o][col];
+    float* d = to + (int64_t)s * p.C + c;
+    *d = p.accumulate ? *d + sum : sum;
+  }
+}
+
+// waves of a row and column groups of a lane: up to 32 values a lane (64 forward), the fewest waves for that
+template <bool XF, bool YF>
+static hipError_t forward_xy(const NormForward& p, hipStream_t s) {
+  const int chunks = (p.C + 7) / 8;
+  const dim3 four((unsigned)((p.rows + 3) / 4)), one((unsigned)p.rows);
+#define CR_NF(W, V) hipLaunchKernelGGL((norm_forward_kernel<W, V, XF, YF>), W == 1 ? four : one, dim3(W == 1 ? 256 : W * 64), 0, s, p)
+  if (chunks <= 64) CR_NF(1, 1);
+  else if (chunks <= 128) CR_NF(1, 2);
+  else if (chunks <= 256) CR_NF(1, 4);
+  else if (chunks <= 512) CR_NF(1, 8);
+  else if (chunks <= 1024) CR_NF(4, 4);
+  else CR_NF(4, 8);
+#undef CR_NF
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_forward(const NormForward& p, hipStream_t s) {
+  if (p.x_f32) return p.y_f32 ? forward_xy<true, true>(p, s) : forward_xy<true, false>(p, s);
+  return p.y_f32 ? forward_xy<false, true>(p, s) : forward_xy<false, false>(p, s);
+}
+
+// parts of the backward pass: about two blocks a compute unit, whole rounds of a block's waves
+int norm_parts(int64_t rows, int64_t C, int* part_rows) {
+  const int step = C <= 2048 ? 4 : 1;
+  int64_t per = (rows + 511) / 512;
+  per = (per + step - 1) / step * step;
+  *part_rows = (int)per;
+  return (int)((rows + per - 1) / per);
+}
+
+size_t norm_backward_ws_bytes(int64_t rows, int64_t C, int S) {
+  int per;
+  const int parts = norm_parts(rows, C, &per);
+  return (size_t)2 * (size_t)(parts + S) * (size_t)C * sizeof(float);
+}
+
+template <bool XF, bool DF>
+static void backward_xd(const NormBackward& p, hipStream_t s) {
+  const int chunks = (p.C + 7) / 8;
+  const dim3 grid((unsigned)p.parts);
+#define CR_NB(W, V) hipLaunchKernelGGL((norm_backward_kernel<W, V, XF, DF>), grid, dim3(W == 1 ? 256 : W * 64), 0, s, p)
+  if (chunks <= 64) CR_NB(1, 1);
+  else if (chunks <= 128) CR_NB(1, 2);
+  else if (chunks <= 256) CR_NB(1, 4);
+  else if (chunks <= 512) CR_NB(4, 2);
+  else if (chunks <= 1024) CR_NB(4, 4);
+  else CR_NB(8, 4);
+#undef CR_NB
+}
+
+hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int* kernels) {
+  int per;
+  p.parts = norm_parts(p.rows, p.C, &per);
+  p.part_rows = per;
+  if (p.dw || p.db) {
+    p.parts_w = reinterpret_cast<float*>(ws);
+    p.parts_b = p.parts_w + (size_t)(p.parts + p.S) * p.C;
+  }
+  if (p.x_f32) {
+    if (p.dy_f32) backward_xd<true, true>(p, s);
+    else backward_xd<true, false>(p, s);
+  } else {
+    if (p.dy_f32) backward_xd<false, true>(p, s);
+    else backward_xd<false, false>(p, s);
+  }
+  *kernels = 1;
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !p.parts_w) return e;
+  hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((p.C + 31) / 32), (unsigned)p.S, 2), dim3(256), 0, s, p);
+  *kernels = 2;
+  return hipGetLastError();
+}
+
+}  // namespace cr
