@@ -765,7 +765,8 @@ cr_status convrot_layer_norm_backward(const void* dy, cr_out dy_type, int64_t ld
  *
  *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- *   copy = p rounded to bf16. Each operation rounds once to float32; the constants are
+ *   copy = p rounded to bf16. Each operation on m, v and g rounds once to float32 (the
+ *   update's quotient is within two units in its last place); the constants are
  *   computed in float64 and rounded.
  *
  *   tensors      HOST array of `count` entries, read before the call returns:

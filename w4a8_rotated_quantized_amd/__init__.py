@@ -4,11 +4,11 @@ Argument marshalling only: every step of the path runs in the HIP kernels
 behind the C ABI declared in include/convrot.h. PyTorch provides device
 memory and the current stream. There is no fallback: if the library is
 missing this module raises at import, and every non-OK status raises
-ConvRotError with the library's status text.
+ConvRotError with the library's status text. The calls go through ctypes, or
+through the native module where the host's time counts.
 """
 from __future__ import annotations
 
-import array
 import contextlib
 import ctypes
 import os
@@ -32,12 +32,14 @@ __all__ = [
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libconvrot.so")
 
-if not os.path.exists(LIB_PATH):
+if not all(os.path.exists(os.path.join(_HERE, f)) for f in ("libconvrot.so", "_native.so")):
     raise ImportError(
-        f"{LIB_PATH} is not built; run __graft_entry__.build() "
+        f"{LIB_PATH} and _native.so are not built; run __graft_entry__.build() "
         "(hipcc --offload-arch=gfx950). There is no non-HIP fallback.")
 
 lib = ctypes.CDLL(LIB_PATH)
+
+from . import _native  # noqa: E402  (links against the library loaded above)
 
 
 class Q:
@@ -678,72 +680,52 @@ def convrot_act_backward(dy, codes, scales, act, dz=None, stream=None):
 
 
 # ---------------------------------------------------------------------------
+# The entry points below check their tensors and allocate their outputs in the
+# native module (csrc/binding.cpp): their small sizes are bound by the host. A call
+# that the library refuses comes back as its status.
+# ---------------------------------------------------------------------------
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _run(call, first, what, stream, args, held):
+    """call(*args, stream handle) on the GPU of `first` and the given stream
+    (default: that GPU's current one). held(result): the tensors of the call."""
+    index = _gpu(first, what)
+    if stream is None and index == _current_device():
+        return call(*args, _current_stream_handle(index))
+    with _on(index, stream):
+        result = call(*args, _current_stream_handle(index))
+    if type(result) is not int or result == 0:
+        _hold(stream, *held(result))
+    return result
+
+
+# ---------------------------------------------------------------------------
 # the rotated 4-bit linear in microscaled floating point
 #
 # Operands of either side: codes uint8 [ceil(K/128), rows, 64] (E2M1, two a
 # byte) and scales uint8 [ceil(K/128), rows, 4] (a power of two per 32 columns).
 # ---------------------------------------------------------------------------
-_U8 = torch.uint8
-
-
-def _mx_pair(codes, scales, what, index):
-    """Checks codes and scales of one operand: (tiles, rows, address, address)."""
-    if codes.dim() != 3 or codes.shape[2] != 64:
-        raise ValueError(f"{what} codes are uint8 [ceil(K/128), rows, 64]")
-    tiles, rows = codes.shape[:2]
-    return (tiles, rows, _tensor(codes, f"{what} codes", _U8, index, (tiles, rows, 64)),
-            _tensor(scales, f"{what} scales", _U8, index, (tiles, rows, 4)))
-
-
 def mxfp4_quantize(x, rot_group=0, codes=None, scales=None, stream=None):
     """x: bf16 [rows, K] (rows may lie further apart; K a multiple of 32 and of
     rot_group) -> (codes, scales) in microscaled 4-bit floating point: codes uint8
     [ceil(K/128), rows, 64], scales uint8 [ceil(K/128), rows, 4]. rot_group: 0
     (none), 16, 64, 256 or 1024 columns rotated first. Weights and activations of
     one product take the same rot_group."""
-    index = _gpu(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x is [rows, K]")
-    rows, K = x.shape
-    px, ldx = _rows(x, "x", _BF16, index, rows, K)
-    tiles = -(-K // 128)
-    with _on(index, stream):
-        if codes is None:
-            codes = torch.empty((tiles, rows, 64), dtype=_U8, device=x.device)
-            pc = codes.data_ptr()
-        else:
-            pc = _tensor(codes, "codes", _U8, index, (tiles, rows, 64))
-        if scales is None:
-            scales = torch.empty((tiles, rows, 4), dtype=_U8, device=x.device)
-            ps = scales.data_ptr()
-        else:
-            ps = _tensor(scales, "scales", _U8, index, (tiles, rows, 4))
-        _hold(stream, x, codes, scales)
-        st = lib.mxfp4_quantize(px, ldx, rows, K, rot_group, pc, ps, _current_stream_handle(index))
-    if st:
-        _refused(st, "mxfp4_quantize", x=x, codes=codes, scales=scales)
-    return codes, scales
+    r = _run(_native.mxfp4_quantize, x, "x", stream, (x, rot_group, codes, scales), lambda r: (x, *r))
+    if type(r) is int:
+        _refused(r, "mxfp4_quantize", x=x, codes=codes, scales=scales)
+    return r
 
 
 def mxfp4_dequantize(codes, scales, K, rot_group=0, out_type=OUT.BF16, out=None, stream=None):
     """The values that the codes of mxfp4_quantize stand for, [rows, K] in
     out_type, rotated back by rot_group (0: left in the basis of the codes)."""
-    index = _gpu(codes, "codes")
-    tiles, rows, pc, ps = _mx_pair(codes, scales, "the", index)
-    if tiles != -(-K // 128):
-        raise ValueError("K does not fit the codes' tiles")
-    dt = _out_dtype(out_type)
-    with _on(index, stream):
-        if out is None:
-            out, ldo = torch.empty((rows, K), dtype=dt, device=codes.device), K
-            po = out.data_ptr()
-        else:
-            po, ldo = _rows(out, "out", dt, index, rows, K)
-        _hold(stream, codes, scales, out)
-        st = lib.mxfp4_dequantize(pc, ps, rows, K, rot_group, po, out_type, ldo, _current_stream_handle(index))
-    if st:
-        _refused(st, "mxfp4_dequantize", codes=codes, scales=scales, out=out)
-    return out
+    r = _run(_native.mxfp4_dequantize, codes, "codes", stream, (codes, scales, K, rot_group, out_type, out),
+             lambda r: (codes, scales, r))
+    if type(r) is int:
+        _refused(r, "mxfp4_dequantize", codes=codes, scales=scales, out=out)
+    return r
 
 
 def mxfp4_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, out_type=OUT.BF16, out=None, stream=None):
@@ -751,86 +733,32 @@ def mxfp4_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, out_type=OUT.BF1
     w [N, K] (weights, N a multiple of 8), quantized with the same rot_group.
     bias: bf16 [N]. Returns [M, N] in out_type; rows of a given out may lie
     further apart. Not recorded by autograd."""
-    index = _gpu(a_codes, "a_codes")
-    tiles, M, pa, pas = _mx_pair(a_codes, a_scales, "a", index)
-    w_tiles, N, pw, pws = _mx_pair(w_codes, w_scales, "w", index)
-    if tiles != w_tiles:
-        raise ValueError("a and w have different K")
-    pb = None if bias is None else _tensor(bias, "bias", _BF16, index, (N,))
-    dt = _out_dtype(out_type)
-    with _on(index, stream):
-        if out is None:
-            out, ldc = torch.empty((M, N), dtype=dt, device=a_codes.device), N
-            po = out.data_ptr()
-        else:
-            po, ldc = _rows(out, "out", dt, index, M, N)
-        _hold(stream, a_codes, a_scales, w_codes, w_scales, bias, out)
-        st = lib.mxfp4_gemm(pa, pas, pw, pws, pb, po, out_type, ldc, M, N, tiles * 128, _current_stream_handle(index))
-    if st:
-        _refused(st, "mxfp4_gemm", a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out)
-    return out
+    r = _run(_native.mxfp4_gemm, a_codes, "a_codes", stream, (a_codes, a_scales, w_codes, w_scales, bias, out_type, out),
+             lambda r: (a_codes, a_scales, w_codes, w_scales, bias, r))
+    if type(r) is int:
+        _refused(r, "mxfp4_gemm", a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out)
+    return r
 
 
 # ---------------------------------------------------------------------------
 # layer norm and its gradients
 # ---------------------------------------------------------------------------
-def _float_type(t, what):
-    """OUT number of a bf16 or float32 tensor."""
-    if t.dtype is _BF16:
-        return OUT.BF16
-    if t.dtype is _F32:
-        return OUT.F32
-    raise ValueError(f"{what} must be bfloat16 or float32")
-
-
-def _affine(weight, bias, seg_offsets, index, C):
-    """Checks weight, bias ([C], or [S, C] with seg_offsets [S + 1]): (S, type, addresses of the three)."""
-    S, po = 1, None
-    if seg_offsets is not None:
-        if seg_offsets.dim() != 1:
-            raise ValueError("seg_offsets is int32 [S + 1]")
-        S = seg_offsets.shape[0] - 1
-        po = _tensor(seg_offsets, "seg_offsets", _I32, index, (S + 1,))
-    shape = (C,) if seg_offsets is None else (S, C)
-    first = weight if weight is not None else bias
-    kind = OUT.F32 if first is None else _float_type(first, "weight and bias")
-    pw = None if weight is None else _tensor(weight, "weight", _OUT_DTYPE[kind], index, shape)
-    pb = None if bias is None else _tensor(bias, "bias", _OUT_DTYPE[kind], index, shape)
-    return S, kind, pw, pb, po
-
-
 def convrot_layer_norm_forward(x, weight=None, bias=None, seg_offsets=None, eps=1e-6, one_plus=False, out_type=OUT.BF16,
                                out=None, mean=None, rstd=None, stream=None):
     """y = (x - mean) rstd (weight + one_plus) + bias over the last dimension of x
     [M, C] (bf16 or float32; C a multiple of 8). weight, bias: [C], or [S, C]
     with seg_offsets int32 [S + 1], a pair for the rows seg_offsets[s] ..
-    seg_offsets[s+1] of each sequence (adaLN: one_plus=True with the scales as weight). Rows in no
-    sequence are left as they are in the given outputs. Returns (y in out_type, mean, rstd):
-    mean and rstd float32 [M] are what convrot_layer_norm_backward reads. Not
-    recorded by autograd."""
-    index = _gpu(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x is [M, C]")
-    M, C = x.shape
-    x_type, dt = _float_type(x, "x"), _out_dtype(out_type)
-    px, ldx = _rows(x, "x", x.dtype, index, M, C)
-    S, kind, pw, pb, po = _affine(weight, bias, seg_offsets, index, C)
-    with _on(index, stream):
-        if out is None:
-            out, ldy = torch.empty((M, C), dtype=dt, device=x.device), C
-            py = out.data_ptr()
-        else:
-            py, ldy = _rows(out, "out", dt, index, M, C)
-        mean = torch.empty((M,), dtype=_F32, device=x.device) if mean is None else mean
-        rstd = torch.empty((M,), dtype=_F32, device=x.device) if rstd is None else rstd
-        pm, pr = _tensor(mean, "mean", _F32, index, (M,)), _tensor(rstd, "rstd", _F32, index, (M,))
-        _hold(stream, x, weight, bias, seg_offsets, out, mean, rstd)
-        st = lib.convrot_layer_norm_forward(px, x_type, ldx, pw, pb, kind, int(bool(one_plus)), po, S, eps, py, out_type, ldy,
-                                            pm, pr, M, C, _current_stream_handle(index))
-    if st:
-        _refused(st, "convrot_layer_norm_forward", x=x, weight=weight, bias=bias, seg_offsets=seg_offsets, out=out, mean=mean,
+    seg_offsets[s+1] of each sequence (adaLN: one_plus=True with the scales as
+    weight). Rows in no sequence are left as they are in the given outputs. Returns
+    (y in out_type, mean, rstd): mean and rstd float32 [M] are what
+    convrot_layer_norm_backward reads. Not recorded by autograd."""
+    r = _run(_native.layer_norm_forward, x, "x", stream,
+             (x, weight, bias, seg_offsets, eps, one_plus, out_type, out, mean, rstd),
+             lambda r: (x, weight, bias, seg_offsets, *r))
+    if type(r) is int:
+        _refused(r, "convrot_layer_norm_forward", x=x, weight=weight, bias=bias, seg_offsets=seg_offsets, out=out, mean=mean,
                  rstd=rstd)
-    return out, mean, rstd
+    return r
 
 
 def convrot_layer_norm_backward_workspace_size(M, C, S) -> int:
@@ -843,95 +771,27 @@ def convrot_layer_norm_backward(dy, x, mean, rstd, weight=None, seg_offsets=None
     """Gradients of convrot_layer_norm_forward for dy [M, C] (bf16 or float32).
     Returns (dx, d_weight, d_bias): dx = dx_base + the input's gradient in
     dx_type (None with want_dx=False), d_weight and d_bias float32 shaped like the
-    weight, [C] or [S, C] (None with want_weights=False; accumulate=True adds to the
-    given ones)."""
-    index = _gpu(dy, "dy")
-    if dy.dim() != 2:
-        raise ValueError("dy is [M, C]")
-    M, C = dy.shape
-    dev, dt = dy.device, _out_dtype(dx_type)
-    if not want_dx and not want_weights:
-        raise ValueError("nothing is wanted")
-    dy_type, x_type = _float_type(dy, "dy"), _float_type(x, "x")
-    pdy, lddy = _rows(dy, "dy", dy.dtype, index, M, C)
-    px, ldx = _rows(x, "x", x.dtype, index, M, C)
-    pm, pr = _tensor(mean, "mean", _F32, index, (M,)), _tensor(rstd, "rstd", _F32, index, (M,))
-    S, kind, pw, _, po = _affine(weight, None, seg_offsets, index, C)
-    shape = (C,) if seg_offsets is None else (S, C)
-    pb = pdx = pgw = pgb = None
-    ldb = lddx = C
-    if accumulate and want_weights and (d_weight is None or d_bias is None):
-        raise ValueError("accumulate adds to given d_weight and d_bias")
-    if want_dx and dx_base is not None:
-        pb, ldb = _rows(dx_base, "dx_base", dt, index, M, C)
-    with _on(index, stream):
-        if want_dx and dx is None:
-            dx = torch.empty((M, C), dtype=dt, device=dev)
-            pdx = dx.data_ptr()
-        elif want_dx:
-            pdx, lddx = _rows(dx, "dx", dt, index, M, C)
-        pws, wsb = None, 0
-        if want_weights:
-            d_weight = torch.empty(shape, dtype=_F32, device=dev) if d_weight is None else d_weight
-            d_bias = torch.empty(shape, dtype=_F32, device=dev) if d_bias is None else d_bias
-            pgw, pgb = _tensor(d_weight, "d_weight", _F32, index, shape), _tensor(d_bias, "d_bias", _F32, index, shape)
-            if workspace is None:
-                need = lib.convrot_layer_norm_backward_workspace_size(M, C, S)
-                workspace = torch.empty(max(need, 16), dtype=_U8, device=dev)
-            elif workspace.get_device() != index or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be contiguous on GPU {index}")
-            pws, wsb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-            _hold(stream, d_weight, d_bias, workspace)
-        if want_dx:
-            _hold(stream, dx_base, dx)
-        _hold(stream, dy, x, mean, rstd, weight, seg_offsets)
-        st = lib.convrot_layer_norm_backward(pdy, dy_type, lddy, px, x_type, ldx, pm, pr, pw, kind, int(bool(one_plus)), po, S,
-                                             pb, ldb, pdx, dx_type, lddx, pgw, pgb, int(bool(accumulate)), M, C, pws, wsb,
-                                             _current_stream_handle(index))
-    if st:
+    weight, [C] or [S, C] (None with want_weights=False; accumulate=True adds to
+    the given ones)."""
+    r = _run(_native.layer_norm_backward, dy, "dy", stream,
+             (dy, x, mean, rstd, weight, seg_offsets, one_plus, dx_base, dx_type, dx, d_weight, d_bias, want_dx, want_weights,
+              accumulate, workspace),
+             lambda r: (dy, x, mean, rstd, weight, seg_offsets, dx_base, *r))
+    if type(r) is int:
         read = dict(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, seg_offsets=seg_offsets)
         if want_weights:
             read.update(d_weight=d_weight, d_bias=d_bias, workspace=workspace)
         if want_dx:
             read.update(dx_base=dx_base, dx=dx)
-        _refused(st, "convrot_layer_norm_backward", **read)
-    return (dx if want_dx else None), (d_weight if want_weights else None), (d_bias if want_weights else None)
+        _refused(r, "convrot_layer_norm_backward", **read)
+    return r[:3]
 
 
 # ---------------------------------------------------------------------------
 # optimizer step over many tensors
 # ---------------------------------------------------------------------------
-def _list(tensors, what, dtype, index, sizes):
-    """Addresses of a list of dense tensors; dtype, GPU, sizes and contiguity checked list-wise."""
-    if len(tensors) != len(sizes) or [t.numel() for t in tensors] != sizes:
-        raise ValueError(f"{what} must hold one tensor for each of params, of its size")
-    if {t.dtype for t in tensors} != {dtype} or {t.get_device() for t in tensors} != {index} or not all(
-            [t.is_contiguous() for t in tensors]):
-        raise ValueError(f"{what} must be contiguous {dtype} tensors on GPU {index}")
-    return [t.data_ptr() for t in tensors]
-
-
-def _table(*columns):
-    """The entries of cr_adamw_tensor, 8 words each, from its eight columns (None: null)."""
-    n = len(columns[-1])
-    flat = array.array("q", bytes(64 * n))
-    for i, c in enumerate(columns):
-        if c is not None:
-            flat[i::8] = array.array("q", c)
-    return flat
-
-
-def _moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, index, sizes):
-    """Addresses of the moments and their scales (None, None for float32 moments)."""
-    if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
-        raise ValueError("8-bit moments have exp_avg_scales and exp_avg_sq_scales")
-    if exp_avg_scales is None:
-        return (_list(exp_avgs, "exp_avgs", _F32, index, sizes), _list(exp_avg_sqs, "exp_avg_sqs", _F32, index, sizes),
-                None, None)
-    blocks = [-(-n // 256) for n in sizes]
-    return (_list(exp_avgs, "exp_avgs", _I8, index, sizes), _list(exp_avg_sqs, "exp_avg_sqs", _U8, index, sizes),
-            _list(exp_avg_scales, "exp_avg_scales", _F32, index, blocks),
-            _list(exp_avg_sq_scales, "exp_avg_sq_scales", _F32, index, blocks))
+def _listed(*lists):
+    return [t for held in lists if held is not None for t in held]
 
 
 def convrot_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
@@ -940,49 +800,27 @@ def convrot_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1=0.9
     or float32 (all of one type), exp_avgs and exp_avg_sqs float32, or int8 and
     uint8 with exp_avg_scales and exp_avg_sq_scales float32 [ceil(n / 256)] (the
     8-bit moments; start them as zeros; give each step another seed). copies:
-    bf16 tensors that receive the new params. grad_scale: float32 [1] on the GPU, multiplies
-    the gradients. step counts from 1. A tensor may stand in the lists once."""
-    if not params:
+    bf16 tensors that receive the new params. grad_scale: float32 [1] on the GPU,
+    multiplies the gradients. step counts from 1. A tensor may stand in the lists
+    once."""
+    if not len(params):
         raise ValueError("params is empty")
-    index = _gpu(params[0], "params")
-    sizes = [t.numel() for t in params]
-    pp = _list(params, "params", _F32, index, sizes)
-    grad_type = _float_type(grads[0], "grads") if len(grads) else OUT.F32
-    pg = _list(grads, "grads", _OUT_DTYPE[grad_type], index, sizes)
-    pm, pv, pms, pvs = _moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, index, sizes)
-    pc = None if copies is None else _list(copies, "copies", _BF16, index, sizes)
-    pgs = None if grad_scale is None else _tensor(grad_scale, "grad_scale", _F32, index, (1,))
-    table = _table(pp, pg, pm, pv, pms, pvs, pc, sizes)
-    with _on(index, stream):
-        for held in (params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales, (grad_scale,)):
-            if stream is not None and held is not None:
-                _hold(stream, *held)
-        st = lib.convrot_adamw_step(table.buffer_info()[0], len(sizes), grad_type, 32 if pms is None else 8, lr, beta1, beta2,
-                                    eps, weight_decay, step, pgs, seed & 0xFFFFFFFF, _current_stream_handle(index))
-    _check(st, "convrot_adamw_step")
+    r = _run(_native.adamw_step, params[0], "params", stream,
+             (params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales, grad_scale, step, lr, beta1, beta2,
+              eps, weight_decay, seed & 0xFFFFFFFF),
+             lambda r: (*_listed(params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales), grad_scale))
+    _check(r, "convrot_adamw_step")
 
 
 def convrot_adamw_moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, exp_avg_out=None, exp_avg_sq_out=None,
                           stream=None):
     """8-bit moments of convrot_adamw_step as float32 (for a checkpoint, or to go on
     with float32 moments): (m, v), one tensor after another in two flat tensors."""
-    if not exp_avgs:
+    if not len(exp_avgs):
         raise ValueError("exp_avgs is empty")
-    index = _gpu(exp_avgs[0], "exp_avgs")
-    sizes = [t.numel() for t in exp_avgs]
-    if exp_avg_scales is None or exp_avg_sq_scales is None:
-        raise ValueError("8-bit moments have exp_avg_scales and exp_avg_sq_scales")
-    pm, pv, pms, pvs = _moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, index, sizes)
-    total = sum(sizes)
-    table = _table(None, None, pm, pv, pms, pvs, None, sizes)
-    with _on(index, stream):
-        dev = exp_avgs[0].device
-        exp_avg_out = torch.empty((total,), dtype=_F32, device=dev) if exp_avg_out is None else exp_avg_out
-        exp_avg_sq_out = torch.empty((total,), dtype=_F32, device=dev) if exp_avg_sq_out is None else exp_avg_sq_out
-        po = _tensor(exp_avg_out, "exp_avg_out", _F32, index, (total,))
-        pq = _tensor(exp_avg_sq_out, "exp_avg_sq_out", _F32, index, (total,))
-        for held in (exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, (exp_avg_out, exp_avg_sq_out)):
-            _hold(stream, *held)
-        st = lib.convrot_adamw_moments(table.buffer_info()[0], len(sizes), po, pq, _current_stream_handle(index))
-    _check(st, "convrot_adamw_moments")
-    return exp_avg_out, exp_avg_sq_out
+    r = _run(_native.adamw_moments, exp_avgs[0], "exp_avgs", stream,
+             (exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, exp_avg_out, exp_avg_sq_out),
+             lambda r: (*_listed(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales), *r))
+    if type(r) is int:
+        _check(r, "convrot_adamw_moments")
+    return r

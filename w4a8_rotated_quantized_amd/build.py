@@ -1,15 +1,18 @@
-"""Builds libconvrot.so (all gfx950 HIP kernels and the C-ABI host layer)
-in-tree with hipcc. Every call recompiles."""
+"""Builds libconvrot.so (all gfx950 HIP kernels and the C-ABI host layer) with
+hipcc, and _native.so (the CPython side of some entry points) with g++, both
+in-tree. Every call recompiles."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
+NATIVE = os.path.join(HERE, "_native.so")
 SOURCES = ["rq.hip", "pack.hip", "merge.hip", "gemm_w4a4.hip", "gemm_int.hip", "gemm_w4a8.hip", "gemm_f6.hip", "abi.cpp",
            "lora.hip", "act.hip", "adapter_abi.cpp", "mx.hip", "gemm_mx.hip", "norm.hip", "adamw.hip", "block_abi.cpp"]
 
@@ -40,9 +43,39 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    """binding.cpp against the torch that is installed."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    obj = os.path.join(BUILD, "binding.o")
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-attributes", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-isystem{p}" for p in (*include_paths(), sysconfig.get_paths()["include"], os.path.join(rocm, "include"))],
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    from torch.utils.cpp_extension import library_paths
+    dirs = library_paths()
+    tmp = NATIVE + ".tmp"
+    cmd = ["g++", "-shared", "-fPIC", obj, "-o", tmp, f"-L{HERE}", "-l:libconvrot.so", "-Wl,-rpath,$ORIGIN",
+           *[f"-L{d}" for d in dirs], "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *objs, "-o", tmp]
@@ -50,6 +83,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding.result())
     return LIB
 
 

@@ -127,8 +127,22 @@ CR_DEV v4f root_values(uint32_t c, float s) {
   return v;
 }
 
+// sqrt(x) rounded once, for 2^-100 <= x <= 1: a step on the root and half its
+// reciprocal together, then one with the exact residual.
+CR_DEV float sqrt_rn(float x) {
+  const float y = __builtin_amdgcn_rsqf(x);
+  float s = x * y, h = 0.5f * y;
+  const float e = __builtin_fmaf(-h, s, 0.5f);
+  s = __builtin_fmaf(s, e, s);
+  h = __builtin_fmaf(h, e, h);
+  return __builtin_fmaf(__builtin_fmaf(-s, s, x), h, s);
+}
+
 // Codes of one wave's 256 values and their scale. SIGNED: c = -127..127, else the
 // values are not negative and c = 0..255, at least 1 for a value above 0.
+// |x| / s is rounded once: with s scaled to [0.5, 1) and its reciprocal rounded, one
+// step from x (1 / s) with the exact remainder gives the rounded quotient (a theorem of
+// Markstein's); the library's division takes three times as many instructions.
 template <bool SIGNED>
 CR_DEV uint32_t encode(v4f x, const float (&u)[4], float* scale) {
   constexpr float most = SIGNED ? 127.f : 255.f;
@@ -139,16 +153,21 @@ CR_DEV uint32_t encode(v4f x, const float (&u)[4], float* scale) {
     top = top > b ? top : b;
   }
   top = wave_umax(top);
-  const float s = __uint_as_float(top);
-  *scale = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : s;   // not finite: the block reads as NaN
+  *scale = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top);   // not finite: the block reads as NaN
   if (top == 0 || top >= 0x7F800000u) return 0;
+  const int power = __builtin_amdgcn_frexp_expf(__uint_as_float(top));
+  const float s = ldexpf(__uint_as_float(top), -power);   // in [0.5, 1)
+  const float inv = 1.f / s;
   uint32_t codes = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float t = sqrtf(fabsf(x[e]) / s) * most;
-    float c = floorf(t + u[e]);
-    c = c > most ? most : c;
-    if (!SIGNED && x[e] > 0.f && c < 1.f) c = 1.f;
+    const float a = ldexpf(fabsf(x[e]), -power);
+    float q = a * inv;
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, a), inv, q);
+    // below 2^-100 the root adds less than half a step of u: as good as 2^-100
+    float c = floorf(sqrt_rn(fmaxf(q, 0x1p-100f)) * most + u[e]);
+    c = fminf(c, most);
+    if (!SIGNED) c = fmaxf(c, x[e] > 0.f ? 1.f : 0.f);
     const int k = (int)c;
     codes |= (uint32_t)((SIGNED && x[e] < 0.f ? -k : k) & 0xFF) << (8 * e);
   }
@@ -198,7 +217,8 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(AdamwTable t, AdamwStep
       m[e] = m[e] * p.b1 + g * p.c1;
       v[e] = v[e] * p.b2 + g * g * p.c2;
       root[e] = sqrtf(v[e]);
-      w[e] = w[e] * p.decay - m[e] / (root[e] * p.rsqrt_bias2 + p.eps) * p.rate;
+      // the quotient by the hardware's reciprocal: within two units in the last place of the update
+      w[e] = w[e] * p.decay - m[e] * __builtin_amdgcn_rcpf(root[e] * p.rsqrt_bias2 + p.eps) * p.rate;
     }
     store_f32(a.param, i, n, w);
     if (a.copy) store_bf16(a.copy, i, n, w);
@@ -227,7 +247,7 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(AdamwTable t, AdamwStep
 
 __global__ __launch_bounds__(256) void adamw_moments_kernel(AdamwTable t, int64_t at, float* avg, float* sq) {
   const int which = tensor_of(t, (int)blockIdx.x);
-  for (int i = 0; i < which; ++i) at += t.t[i].n;
+  at += t.before[which];
   const cr_adamw_tensor& a = t.t[which];
   const int64_t base = (int64_t)((int)blockIdx.x - t.first[which]) * ADAMW_CHUNK;
 #pragma unroll

@@ -106,7 +106,8 @@ constexpr int ADAMW_BLOCK = 256;     // elements that share the scale of an 8-bi
 
 struct AdamwTable {
   cr_adamw_tensor t[ADAMW_TENSORS];
-  int first[ADAMW_TENSORS + 1];      // chunks before tensor i
+  int64_t before[ADAMW_TENSORS];     // elements of t[0] .. t[i - 1]
+  int first[ADAMW_TENSORS + 1];      // chunks of t[0] .. t[i - 1]
   int count;
   int ordinal;                       // number of t[0] in the caller's list
 };

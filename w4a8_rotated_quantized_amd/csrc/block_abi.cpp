@@ -76,6 +76,7 @@ hipError_t adamw_tables(const cr_adamw_tensor* t, int count, int* kernels, F lau
       const int64_t c = (t[i].n + cr::ADAMW_CHUNK - 1) / cr::ADAMW_CHUNK;
       if (table.count && chunks + c >= LD_MAX) break;
       table.t[table.count] = t[i];
+      table.before[table.count] = held;
       chunks += c;
       held += t[i].n;
       table.first[++table.count] = (int)chunks;

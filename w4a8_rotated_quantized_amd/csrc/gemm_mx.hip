@@ -48,9 +48,11 @@ CR_DEV void mx_wait_stage(int ahead) {   // at most `ahead` later stages (L load
 // rotate in LDS, S - 1 ahead of the one in use. In LDS a row's four 16-byte
 // pieces are stored at piece ^ (row / 4 % 4): the 16 rows that one phase of a
 // fragment read covers then lie in different banks.
+// KG groups of NW waves share a block where blocks are few: group g takes the
+// stages g, g + KG, ..., each with a ring of its own, and their sums meet in LDS, in order.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int TM, int TN, int S, int MINB, bool F32>
-__global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64, MINB) void mx_gemm_kernel(MxGemm p) {
+template <int BM, int BN, int TM, int TN, int S, int MINB, int KG, bool F32>
+__global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64 * KG, MINB) void mx_gemm_kernel(MxGemm p) {
   constexpr int WN = BN / (32 * TN);
   constexpr int NW = (BM / (32 * TM)) * WN;
   static_assert(BM % (32 * TM) == 0 && BN % (32 * TN) == 0, "whole wave tiles");
@@ -60,15 +62,18 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64, MINB) voi
   constexpr int NC = SC / 1024;                        // 1 KB loads of codes
   constexpr int NS = (BM + BN) / 64;                   // 256-byte loads of scale bytes
   static_assert(NC % NW == 0 && NS <= NW, "even loads");
+  static_assert(KG == 1 || (TM == 1 && TN == 1), "sums that meet in LDS: one tile a wave");
   constexpr int LPW = NC / NW;
   constexpr int RS = TN * 64 + 16;                     // epilogue: LDS row stride of a wave's bf16 tile
   constexpr int TILE = F32 ? 0 : NW * TM * 32 * RS;
-  constexpr int SMEM = S * STAGE > TILE ? S * STAGE : TILE;
+  constexpr int RING = S * STAGE;
+  constexpr int SMEM = KG * RING > TILE + (KG - 1) * BM * BN * 4 ? KG * RING : TILE + (KG - 1) * BM * BN * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
 
   const int tid = threadIdx.x;
   const int l = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % NW;
+  const int group = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 6) / NW;
   const int wm = wave / WN, wn = wave % WN;
 
   // block -> tile: consecutive blocks go round robin over the 8 XCDs, so each
@@ -95,24 +100,25 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64, MINB) voi
     const int r = idx * 16 + (l >> 2);
     const int piece = ((l & 3) ^ ((l >> 4) & 3)) * 16;
     if (idx < A_ST / 1024) {
-      src[j] = p.a + imin64(m0 + r, p.M - 1) * 64 + piece;
-      step[j] = p.M * 64;
+      src[j] = p.a + (group * p.M + imin64(m0 + r, p.M - 1)) * 64 + piece;
+      step[j] = p.M * 64 * KG;
     } else {
-      src[j] = p.w + imin64(n0 + r - BM, p.N - 1) * 64 + piece;
-      step[j] = p.N * 64;
+      src[j] = p.w + (group * p.N + imin64(n0 + r - BM, p.N - 1)) * 64 + piece;
+      step[j] = p.N * 64 * KG;
     }
   }
   const uint8_t* ssrc;
   int64_t sstep;
   if (wave < BM / 64) {
-    ssrc = p.a_scales + imin64(m0 + wave * 64 + l, p.M - 1) * 4;
-    sstep = p.M * 4;
+    ssrc = p.a_scales + (group * p.M + imin64(m0 + wave * 64 + l, p.M - 1)) * 4;
+    sstep = p.M * 4 * KG;
   } else {
-    ssrc = p.w_scales + imin64(n0 + wave * 64 + l - BM, p.N - 1) * 4;
-    sstep = p.N * 4;
+    ssrc = p.w_scales + (group * p.N + imin64(n0 + wave * 64 + l - BM, p.N - 1)) * 4;
+    sstep = p.N * 4 * KG;
   }
-  auto issue = [&](int kb) {
-    uint8_t* st = smem + (kb % S) * STAGE;
+  uint8_t* ring = smem + group * RING;
+  auto issue = [&](int kb) {                          // the group's stage kb; called in order
+    uint8_t* st = ring + (kb % S) * STAGE;
 #pragma unroll
     for (int j = 0; j < LPW; ++j) {
       __builtin_amdgcn_global_load_lds((mx_gptr)src[j], (mx_lptr)(st + (wave + NW * j) * 1024), 16, 0, 0);
@@ -137,15 +143,17 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64, MINB) voi
   const int h = l >> 5;
   const int piece0 = (h ^ ((l >> 2) & 3)) * 16;        // of the stage's first 64 columns; ^ 32: the second
   const int arow = wm * TM * 32 + (l & 31), wrow = wn * TN * 32 + (l & 31);
-  const int nkb = p.tiles;
+  const int nkb = (p.tiles - group + KG - 1) / KG;    // of this group: the first has the most
+  const int rounds = (p.tiles + KG - 1) / KG;
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (s < nkb) issue(s);
-  for (int kb = 0; kb < nkb; ++kb) {
-    wait_stage(min(S - 2, nkb - 1 - kb));             // this wave's loads of stage kb have landed
+  for (int kb = 0; kb < rounds; ++kb) {
+    if (KG == 1 || kb < nkb) wait_stage(min(S - 2, nkb - 1 - kb));   // this wave's loads of stage kb have landed
     __builtin_amdgcn_s_barrier();                     // ... and every wave's; stage kb - 1 is consumed
+    if (KG > 1 && kb >= nkb) break;                   // the last round, and a group without a stage in it
     if (kb + S - 1 < nkb) issue(kb + S - 1);
-    const uint8_t* As = smem + (kb % S) * STAGE;
+    const uint8_t* As = ring + (kb % S) * STAGE;
     const uint8_t* Ws = As + A_ST;
     u32x4 av[2][TM], wv[2][TN];
     int as[TM], ws[TN];
@@ -163,6 +171,9 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64, MINB) voi
     for (int i = 0; i < TM; ++i) as[i] = *reinterpret_cast<const int*>(As + SC + (arow + i * 32) * 4) >> (8 * h);
 #pragma unroll
     for (int j = 0; j < TN; ++j) ws[j] = *reinterpret_cast<const int*>(As + SC + (BM + wrow + j * 32) * 4) >> (8 * h);
+    // all reads of a stage before its products: left to itself the compiler holds the second half back
+    // until the first half's products are under way (8192 x 4096 x 12288: 224 -> 218 us)
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -177,6 +188,25 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64, MINB) voi
                                                                    E2M1, E2M1, 2, ws[j], 2, as[i]);
   }
 
+  if constexpr (KG > 1) {
+    __syncthreads();                                  // every wave is done with the rings
+    v4f* meet = reinterpret_cast<v4f*>(smem + TILE) + wave * 256 + l;
+    if (group > 0) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        meet[(group - 1) * NW * 256 + g * 64] = v4f{acc[0][0][4 * g], acc[0][0][4 * g + 1], acc[0][0][4 * g + 2], acc[0][0][4 * g + 3]};
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int o = 0; o < KG - 1; ++o)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const v4f v = meet[o * NW * 256 + g * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][0][4 * g + e] += v[e];
+      }
+  }
   // lane l of a 32 x 32 result: token l % 32, channels 8 g + 4 (l / 32) + e
   u32x2 bias[TN][4];
 #pragma unroll
@@ -204,7 +234,7 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64, MINB) voi
     }
   } else {
     // the wave's tile passes through LDS, so that stores write whole runs of a row
-    __syncthreads();                                  // every wave is done with the stages
+    if constexpr (KG == 1) __syncthreads();           // every wave is done with the stages
     uint8_t* tile = smem + wave * (TM * 32 * RS);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -234,17 +264,16 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64, MINB) voi
 
 // ---------------------------------------------------------------------------
 // Few tokens (M <= 64): the weights are the traffic. A block owns 16 channels,
-// its 16 waves take the 128-column tiles in turn and read their fragments straight
+// its NW waves take the 128-column tiles in turn and read their fragments straight
 // from memory: v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows x 64 B of a tile,
 // which is 1 KB in one piece (lane l: row l % 16, columns 32 (l / 16) .. +31).
-// Tokens past the end are zeros without a load. Partial sums meet in LDS in a
-// fixed order.
+// U tiles a wave are loaded before the first is used, so the whole of a
+// matrix is on its way at once. Tokens past the end are zeros without a load.
+// Partial sums meet in LDS in a fixed order.
 // ---------------------------------------------------------------------------
-constexpr int MX_FEW_WAVES = 16;
-
-template <int FM, bool F32>
-__global__ __launch_bounds__(MX_FEW_WAVES * 64) void mx_few_kernel(MxGemm p) {
-  constexpr int NW = MX_FEW_WAVES, U = 2;             // tiles in flight per wave
+template <int FM, int NW, int U, bool F32>
+__global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxGemm p) {
+  static_assert(FM <= NW, "a wave for each 16 tokens' sums");
   __shared__ __attribute__((aligned(16))) float red[NW][FM][64][4];
   const int l = threadIdx.x & 63, r = l & 15, q = l >> 4;
   const int wave = threadIdx.x >> 6;
@@ -254,13 +283,14 @@ __global__ __launch_bounds__(MX_FEW_WAVES * 64) void mx_few_kernel(MxGemm p) {
 #pragma unroll
   for (int i = 0; i < FM; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  for (int t0 = wave * U; t0 < p.tiles; t0 += NW * U) {
+  for (int t0 = wave; t0 < p.tiles; t0 += NW * U) {
     u32x4 wr[U], ar[U][FM];
     int ws[U], as[U][FM];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (t0 + u >= p.tiles) break;
-      const int64_t at = (int64_t)(t0 + u) * p.N + n;
+      const int t = t0 + u * NW;
+      if (t >= p.tiles) break;
+      const int64_t at = (int64_t)t * p.N + n;
       wr[u] = *reinterpret_cast<const u32x4*>(p.w + at * 64 + q * 16);
       ws[u] = p.w_scales[at * 4 + q];
 #pragma unroll
@@ -269,7 +299,7 @@ __global__ __launch_bounds__(MX_FEW_WAVES * 64) void mx_few_kernel(MxGemm p) {
         as[u][i] = 0;
         const int64_t m = i * 16 + r;
         if (m < p.M) {
-          const int64_t to = (int64_t)(t0 + u) * p.M + m;
+          const int64_t to = (int64_t)t * p.M + m;
           ar[u][i] = *reinterpret_cast<const u32x4*>(p.a + to * 64 + q * 16);
           as[u][i] = p.a_scales[to * 4 + q];
         }
@@ -277,7 +307,7 @@ __global__ __launch_bounds__(MX_FEW_WAVES * 64) void mx_few_kernel(MxGemm p) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (t0 + u >= p.tiles) break;
+      if (t0 + u * NW >= p.tiles) break;
 #pragma unroll
       for (int i = 0; i < FM; ++i)
         acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(wr[u]), mx_operand(ar[u][i]), acc[i], E2M1, E2M1,
@@ -309,29 +339,52 @@ __global__ __launch_bounds__(MX_FEW_WAVES * 64) void mx_few_kernel(MxGemm p) {
   }
 }
 
-template <int BM, int BN, int TM, int TN, int S, int MINB, bool F32>
+template <int BM, int BN, int TM, int TN, int S, int MINB, int KG, bool F32>
 static void launch_tiles(const MxGemm& p, hipStream_t s) {
   const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, TM, TN, S, MINB, F32>), dim3((unsigned)tiles),
-                     dim3((BM / (32 * TM)) * (BN / (32 * TN)) * 64), 0, s, p);
+  hipLaunchKernelGGL((mx_gemm_kernel<BM, BN, TM, TN, S, MINB, KG, F32>), dim3((unsigned)tiles),
+                     dim3((BM / (32 * TM)) * (BN / (32 * TN)) * 64 * KG), 0, s, p);
+}
+
+// 16 waves a block up to one block a compute unit, 8 beyond: 1 x 4096, N = 4096: 4.0 us either way; 1 x 9728,
+// N = 2560: 4.9 against 6.2 us; 22 x 2560, N = 9728: 7.5 against 6.2 us
+template <int FM, bool F32>
+static void launch_few(const MxGemm& p, hipStream_t s) {
+  const int64_t blocks = (p.N + 15) / 16;
+  if (blocks <= 256) hipLaunchKernelGGL((mx_few_kernel<FM, 16, 2, F32>), dim3((unsigned)blocks), dim3(1024), 0, s, p);
+  else hipLaunchKernelGGL((mx_few_kernel<FM, 8, 2, F32>), dim3((unsigned)blocks), dim3(512), 0, s, p);
 }
 
 template <bool F32>
 static hipError_t launch_out(const MxGemm& p, hipStream_t s) {
   if (p.M <= 64) {
-    const dim3 grid((unsigned)((p.N + 15) / 16));
     switch ((p.M + 15) / 16) {
-      case 1: hipLaunchKernelGGL((mx_few_kernel<1, F32>), grid, dim3(MX_FEW_WAVES * 64), 0, s, p); break;
-      case 2: hipLaunchKernelGGL((mx_few_kernel<2, F32>), grid, dim3(MX_FEW_WAVES * 64), 0, s, p); break;
-      case 3: hipLaunchKernelGGL((mx_few_kernel<3, F32>), grid, dim3(MX_FEW_WAVES * 64), 0, s, p); break;
-      default: hipLaunchKernelGGL((mx_few_kernel<4, F32>), grid, dim3(MX_FEW_WAVES * 64), 0, s, p); break;
+      case 1: launch_few<1, F32>(p, s); break;
+      case 2: launch_few<2, F32>(p, s); break;
+      case 3: launch_few<3, F32>(p, s); break;
+      default: launch_few<4, F32>(p, s); break;
     }
     return hipGetLastError();
   }
+  // The block shape with the least time. A compute unit that has n blocks to do takes at least `alone` a
+  // stage (one block's own chain of waits) and n times `each` once they fill it, in ns. Measured with K = 4096
+  // (256 x 256, 128 x 128, 128 x 64, 64 x 64 blocks, in us): 8192 x 12288: 218, 253, -, -; 4096 x 4096: 39, 50, 53, 62;
+  // 2048 x 4096: 31, 23, 30, 33; 1024 x 4096: 29, 17, 15, 18; 512 x 4096: 29, 16, 13, 11; and 1531 x 2560, N = 9216:
+  // 25, 29, 32, 36.
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 512) launch_tiles<256, 256, 2, 2, 4, 1, F32>(p, s);
-  else if (tiles(128, 128) >= 256) launch_tiles<128, 128, 2, 2, 3, 3, F32>(p, s);
-  else launch_tiles<64, 64, 1, 1, 4, 4, F32>(p, s);
+  auto cost = [&](int64_t bm, int64_t bn, int64_t alone, int64_t each) {
+    const int64_t n = (tiles(bm, bn) + 255) / 256;
+    return n * each > alone ? n * each : alone;
+  };
+  const int64_t c256 = cost(256, 256, 900, 1200), c128 = cost(128, 128, 500, 330), c12864 = cost(128, 64, 390, 230),
+                c64 = cost(64, 64, 310, 140);
+  if (c256 <= c128 && c256 <= c12864 && c256 <= c64) launch_tiles<256, 256, 4, 2, 4, 1, 1, F32>(p, s);
+  else if (c128 <= c12864 && c128 <= c64) launch_tiles<128, 128, 2, 2, 3, 3, 1, F32>(p, s);
+  else if (c12864 <= c64) launch_tiles<128, 64, 2, 1, 4, 3, 1, F32>(p, s);
+  // one block a compute unit leaves it waiting: four groups share the stages, from where each has some
+  // (65 x 4096 x 4096: 9.5 -> 7.5 us, 128 x 9728 x 2560: 18.6 -> 12.5; 300 x 1024 x 328 with 8 stages: 4.4 -> 4.8)
+  else if (tiles(64, 64) <= 256 && p.tiles >= 16) launch_tiles<64, 64, 1, 1, 4, 1, 4, F32>(p, s);
+  else launch_tiles<64, 64, 1, 1, 4, 4, 1, F32>(p, s);
   return hipGetLastError();
 }
 

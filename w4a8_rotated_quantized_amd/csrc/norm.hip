@@ -78,7 +78,7 @@ CR_DEV float wave_sum(float v) {
   return v;
 }
 
-// the sum over the W waves of a row, in a fixed order; `slot` alternates so that one barrier is enough
+// the sums over the W waves of a row, in a fixed order; `slot` changes from call to call, so one barrier is enough
 template <int W>
 CR_DEV float row_sum(float v, float* lds, int wave, int slot) {
   v = wave_sum(v);
@@ -91,6 +91,23 @@ CR_DEV float row_sum(float v, float* lds, int wave, int slot) {
     for (int w = 1; w < W; ++w) v += at[w];
   }
   return v;
+}
+template <int W>
+CR_DEV void row_sums(float& a, float& b, float2* lds, int wave, int slot) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (W > 1) {
+    float2* at = lds + slot * W;
+    if ((threadIdx.x & 63) == 0) at[wave] = float2{a, b};
+    __syncthreads();
+    a = at[0].x;
+    b = at[0].y;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      a += at[w].x;
+      b += at[w].y;
+    }
+  }
 }
 
 // The sequence of a row among S offsets off[0..S], by one wave: the first s whose
@@ -124,6 +141,17 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
     const int c = (v * W * 64 + lane) * 8;
     if (c < p.C) x[v].load(p.x, at + c);
   }
+  // with few values a lane, weight and bias come along: their latency passes with the row's
+  constexpr bool EARLY = V <= 2;
+  float w[EARLY ? V : 1][8], b[EARLY ? V : 1][8];
+  if constexpr (EARLY) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * W * 64 + lane) * 8;
+      if (c < p.C && p.w) load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w[v]);
+      if (c < p.C && p.b) load_affine(p.b, p.w_f32, (int64_t)s * p.C + c, b[v]);
+    }
+  }
   float sum = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -149,105 +177,124 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
   for (int v = 0; v < V; ++v) {
     const int c = (v * W * 64 + lane) * 8;
     if (c >= p.C) continue;
-    float y[8], w[8], b[8];
+    float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (x[v].get(e) - mean) * rstd;
+    constexpr int ONE = EARLY ? 1 : 0;
     if (p.w) {
-      load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w);
+      if constexpr (!EARLY) load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= w[e] + p.plus;
+      for (int e = 0; e < 8; ++e) y[e] *= w[ONE * v][e] + p.plus;
     }
     if (p.b) {
-      load_affine(p.b, p.w_f32, (int64_t)s * p.C + c, b);
+      if constexpr (!EARLY) load_affine(p.b, p.w_f32, (int64_t)s * p.C + c, b[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] += b[e];
+      for (int e = 0; e < 8; ++e) y[e] += b[ONE * v][e];
     }
     store8<YF>(p.y, row * p.ldy + c, y);
   }
 }
 
 // Backward. The rows are cut into p.parts stretches of p.part_rows, a block each. It
-// walks its rows with the sums for dw and db of its columns in registers and
-// writes them out where a sequence ends: part q's share of sequence s goes to
-// slot q + s of the workspace, which no other pair has, as both only grow along the
-// rows. The last launch adds a sequence's slots in order.
+// walks its rows with the sums for dw and db of its columns in registers, the
+// next row's loads under way, and writes the sums out where a sequence ends: part
+// q's share of sequence s goes to slot q + s of the workspace, which no other pair
+// has, as both only grow along the rows. The last launch adds a sequence's slots
+// in order.
 // W == 1: four waves take the block's rows in turn, each with sums of its own,
 // added through LDS before they are written.
 template <int W, int V, bool XF, bool DF>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(NormBackward p) {
   constexpr int RPB = W == 1 ? 4 : 1;
-  __shared__ float lds[4 * W];
+  __shared__ float2 lds[2 * W];
   __shared__ float4 join[W == 1 ? 3 * 64 * 4 : 1];
   const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lane = W == 1 ? l : threadIdx.x;
   int64_t row = (int64_t)blockIdx.x * p.part_rows;
   const int64_t end = imin64(row + p.part_rows, p.rows);
   if (p.off && row < p.off[0]) row = p.off[0];         // rows in no sequence: nothing is read or written
+  Eight<XF> x[V];
+  Eight<DF> dy[V];
+  float mean = 0.f, rstd = 0.f;
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * W * 64 + lane) * 8;
+      if (c < p.C) {
+        x[v].load(p.x, r * p.ldx + c);
+        dy[v].load(p.dy, r * p.lddy + c);
+      }
+    }
+    mean = p.mean[r];
+    rstd = p.rstd[r];
+  };
   int slot = 0;
   while (row < end) {
     const int s = p.off ? sequence_of(p.off, p.S, row, l) : 0;
     if (s >= p.S) return;
     const int64_t stop = p.off ? imin64(end, p.off[s + 1]) : end;
-    float dw[V][8], db[V][8];
+    float w[V][8], dw[V][8], db[V][8];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * W * 64 + lane) * 8;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dw[v][e] = db[v][e] = 0.f;
-
-    for (int64_t r = row + (W == 1 ? wave : 0); r < stop; r += RPB) {
-      Eight<XF> x[V];
-      Eight<DF> dy[V];
+      for (int e = 0; e < 8; ++e) {
+        dw[v][e] = db[v][e] = 0.f;
+        w[v][e] = 1.f;
+      }
+      if (p.w && c < p.C) {
+        load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w[v]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[v][e] += p.plus;
+      }
+    }
+    int64_t r = row + (W == 1 ? wave : 0);
+    if (r < stop) load(r);
+    for (; r < stop; r += RPB) {
+      // this row's values in float32, then the next row's loads
+      const float rs = rstd;
+      float a = 0.f, b = 0.f;
+      float xh[V][8], d[V][8];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = (v * W * 64 + lane) * 8;
-        if (c < p.C) {
-          x[v].load(p.x, r * p.ldx + c);
-          dy[v].load(p.dy, r * p.lddy + c);
+        const bool in = (v * W * 64 + lane) * 8 < p.C;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          d[v][e] = in ? dy[v].get(e) : 0.f;
+          xh[v][e] = in ? (x[v].get(e) - mean) * rs : 0.f;
         }
       }
-      const float mean = p.mean[r], rstd = p.rstd[r];
-      float a = 0.f, b = 0.f;
+      if (r + RPB < stop) load(r + RPB);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float g = d[v][e] * w[v][e];
+          a += g;
+          b = __builtin_fmaf(g, xh[v][e], b);
+          dw[v][e] = __builtin_fmaf(d[v][e], xh[v][e], dw[v][e]);
+          db[v][e] += d[v][e];
+        }
+      if (!p.dx) continue;
+      row_sums<W>(a, b, lds, wave, slot);
+      slot ^= 1;
+      a *= p.inv_c;
+      b *= p.inv_c;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (v * W * 64 + lane) * 8;
         if (c >= p.C) continue;
-        float w[8];
-        if (p.w) load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w);
+        float o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = dy[v].get(e), xh = (x[v].get(e) - mean) * rstd;
-          const float g = p.w ? d * (w[e] + p.plus) : d;
-          a += g;
-          b = __builtin_fmaf(g, xh, b);
-          dw[v][e] = __builtin_fmaf(d, xh, dw[v][e]);
-          db[v][e] += d;
+        for (int e = 0; e < 8; ++e) o[e] = rs * (d[v][e] * w[v][e] - a - xh[v][e] * b);
+        if (p.base) {
+          float t[8];
+          load_affine(p.base, p.dx_f32, r * p.ldb + c, t);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] += t[e];
         }
-      }
-      if (p.dx) {
-        a = row_sum<W>(a, lds, wave, slot) * p.inv_c;
-        b = row_sum<W>(b, lds, wave, slot + 1) * p.inv_c;
-        slot ^= 2;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int c = (v * W * 64 + lane) * 8;
-          if (c >= p.C) continue;
-          float w[8], o[8];
-          if (p.w) load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float d = dy[v].get(e), xh = (x[v].get(e) - mean) * rstd;
-            const float g = p.w ? d * (w[e] + p.plus) : d;
-            o[e] = rstd * (g - a - xh * b);
-          }
-          if (p.base) {
-            float t[8];
-            load_affine(p.base, p.dx_f32, r * p.ldb + c, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] += t[e];
-          }
-          if (p.dx_f32) store8<true>(p.dx, r * p.lddx + c, o);
-          else store8<false>(p.dx, r * p.lddx + c, o);
-        }
+        if (p.dx_f32) store8<true>(p.dx, r * p.lddx + c, o);
+        else store8<false>(p.dx, r * p.lddx + c, o);
       }
     }
     if (p.parts_w) {
@@ -271,11 +318,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const float4 t = join[o * 256 + q * 64 + l];
-                float* d = (q < 2 ? dw[v] : db[v]) + (q & 1) * 4;
-                d[0] += t.x;
-                d[1] += t.y;
-                d[2] += t.z;
-                d[3] += t.w;
+                float* to = (q < 2 ? dw[v] : db[v]) + (q & 1) * 4;
+                to[0] += t.x;
+                to[1] += t.y;
+                to[2] += t.z;
+                to[3] += t.w;
               }
           }
         }
@@ -290,12 +337,13 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
 }
 
 // dw and db of sequence blockIdx.y: the slots of the parts that hold its rows, in order.
-// 256 threads: 32 columns x 8 shares of the slots.
-__global__ __launch_bounds__(256) void norm_join_kernel(NormBackward p) {
-  __shared__ float lds[8][32];
+// A wave reads 128 columns of a slot, 16 waves share the slots, each with several on their way.
+constexpr int JOIN_WAVES = 16;
+__global__ __launch_bounds__(64 * JOIN_WAVES) void norm_join_kernel(NormBackward p) {
+  __shared__ float2 lds[JOIN_WAVES][64];
   const int s = blockIdx.y;
-  const int col = threadIdx.x & 31, share = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + col;
+  const int l = threadIdx.x & 63, share = threadIdx.x >> 6;
+  const int64_t c = ((int64_t)blockIdx.x * 64 + l) * 2;
   int64_t lo = 0, hi = p.rows;
   if (p.off) {
     // the sequence begins at the largest offset up to off[s]
@@ -303,8 +351,8 @@ __global__ __launch_bounds__(256) void norm_join_kernel(NormBackward p) {
     if (threadIdx.x == 0) begin = 0;
     __syncthreads();
     int m = 0;
-    for (int i = threadIdx.x; i <= s; i += 256) m = max(m, p.off[i]);
-    atomicMax(&begin, m);
+    for (int i = threadIdx.x; i <= s; i += 64 * JOIN_WAVES) m = max(m, p.off[i]);
+    if (m) atomicMax(&begin, m);
     __syncthreads();
     lo = begin;
     hi = imin64(p.off[s + 1], p.rows);
@@ -312,20 +360,33 @@ __global__ __launch_bounds__(256) void norm_join_kernel(NormBackward p) {
   const float* from = blockIdx.z ? p.parts_b : p.parts_w;
   float* to = blockIdx.z ? p.db : p.dw;
   if (!to) return;
-  float sum = 0.f;
+  float2 sum = {0.f, 0.f};
   if (lo < hi && c < p.C) {
     const int first = (int)(lo / p.part_rows), last = (int)((hi - 1) / p.part_rows);
-    const int n = last - first + 1, per = (n + 7) / 8;
+    const int n = last - first + 1, per = (n + JOIN_WAVES - 1) / JOIN_WAVES;
     const int q1 = min(first + (share + 1) * per, last + 1);
-    for (int q = first + share * per; q < q1; ++q) sum += from[((int64_t)q + s) * p.C + c];
+    const float* at = from + ((int64_t)(first + share * per) + s) * p.C + c;
+#pragma unroll 8
+    for (int q = first + share * per; q < q1; ++q, at += p.C) {
+      const float2 v = *reinterpret_cast<const float2*>(at);
+      sum.x += v.x;
+      sum.y += v.y;
+    }
   }
-  lds[share][col] = sum;
+  lds[share][l] = sum;
   __syncthreads();
   if (share == 0 && c < p.C) {
 #pragma unroll
-    for (int o = 1; o < 8; ++o) sum += lds[o][col];
-    float* d = to + (int64_t)s * p.C + c;
-    *d = p.accumulate ? *d + sum : sum;
+    for (int o = 1; o < JOIN_WAVES; ++o) {
+      sum.x += lds[o][l].x;
+      sum.y += lds[o][l].y;
+    }
+    float2* d = reinterpret_cast<float2*>(to + (int64_t)s * p.C + c);
+    if (p.accumulate) {
+      sum.x += d->x;
+      sum.y += d->y;
+    }
+    *d = sum;
   }
 }
 
@@ -336,9 +397,11 @@ static hipError_t forward_xy(const NormForward& p, hipStream_t s) {
   const dim3 four((unsigned)((p.rows + 3) / 4)), one((unsigned)p.rows);
 #define CR_NF(W, V) hipLaunchKernelGGL((norm_forward_kernel<W, V, XF, YF>), W == 1 ? four : one, dim3(W == 1 ? 256 : W * 64), 0, s, p)
   if (chunks <= 64) CR_NF(1, 1);
-  else if (chunks <= 128) CR_NF(1, 2);
-  else if (chunks <= 256) CR_NF(1, 4);
-  else if (chunks <= 512) CR_NF(1, 8);
+  else if (p.rows > 1024 && chunks <= 128) CR_NF(1, 2);
+  else if (p.rows > 1024 && chunks <= 256) CR_NF(1, 4);
+  else if (p.rows > 1024 && chunks <= 512) CR_NF(1, 8);
+  else if (chunks <= 256) CR_NF(4, 1);
+  else if (chunks <= 512) CR_NF(4, 2);
   else if (chunks <= 1024) CR_NF(4, 4);
   else CR_NF(4, 8);
 #undef CR_NF
@@ -352,7 +415,7 @@ hipError_t launch_norm_forward(const NormForward& p, hipStream_t s) {
 
 // parts of the backward pass: about two blocks a compute unit, whole rounds of a block's waves
 int norm_parts(int64_t rows, int64_t C, int* part_rows) {
-  const int step = C <= 2048 ? 4 : 1;
+  const int step = C <= 1024 ? 4 : 1;
   int64_t per = (rows + 511) / 512;
   per = (per + step - 1) / step * step;
   *part_rows = (int)per;
@@ -372,10 +435,10 @@ static void backward_xd(const NormBackward& p, hipStream_t s) {
 #define CR_NB(W, V) hipLaunchKernelGGL((norm_backward_kernel<W, V, XF, DF>), grid, dim3(W == 1 ? 256 : W * 64), 0, s, p)
   if (chunks <= 64) CR_NB(1, 1);
   else if (chunks <= 128) CR_NB(1, 2);
-  else if (chunks <= 256) CR_NB(1, 4);
+  else if (chunks <= 256) CR_NB(4, 1);
   else if (chunks <= 512) CR_NB(4, 2);
-  else if (chunks <= 1024) CR_NB(4, 4);
-  else CR_NB(8, 4);
+  else if (chunks <= 1024) CR_NB(8, 2);
+  else CR_NB(16, 2);
 #undef CR_NB
 }
 
@@ -397,7 +460,7 @@ hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int*
   *kernels = 1;
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.parts_w) return e;
-  hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((p.C + 31) / 32), (unsigned)p.S, 2), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((p.C + 127) / 128), (unsigned)p.S, 2), dim3(64 * JOIN_WAVES), 0, s, p);
   *kernels = 2;
   return hipGetLastError();
 }
