@@ -101,7 +101,7 @@ hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int*
 
 // Tensors of one launch of the optimizer step: their table rides in the kernel's arguments.
 constexpr int ADAMW_TENSORS = 48;
-constexpr int ADAMW_CHUNK = 2048;    // elements a block takes
+constexpr int ADAMW_CHUNK = 1024;    // elements a block takes
 constexpr int ADAMW_BLOCK = 256;     // elements that share the scale of an 8-bit moment
 
 struct AdamwTable {

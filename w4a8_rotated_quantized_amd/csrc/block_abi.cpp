@@ -65,6 +65,8 @@ template <typename F>
 hipError_t adamw_tables(const cr_adamw_tensor* t, int count, int* kernels, F launch) {
   *kernels = 0;
   int64_t elements = 0;
+  // tables of the same number of entries, so that the last launch is no stub
+  const int tables = (count + cr::ADAMW_TENSORS - 1) / cr::ADAMW_TENSORS, per = (count + tables - 1) / tables;
   for (int i = 0; i < count;) {
     cr::AdamwTable table;
     table.count = 0;
@@ -72,7 +74,7 @@ hipError_t adamw_tables(const cr_adamw_tensor* t, int count, int* kernels, F lau
     int64_t chunks = 0, held = 0;
     table.first[0] = 0;
     // every entry takes a place, empty ones no chunk, so that ordinals count them
-    while (i < count && table.count < cr::ADAMW_TENSORS) {
+    while (i < count && table.count < per) {
       const int64_t c = (t[i].n + cr::ADAMW_CHUNK - 1) / cr::ADAMW_CHUNK;
       if (table.count && chunks + c >= LD_MAX) break;
       table.t[table.count] = t[i];

@@ -399,7 +399,6 @@ static hipError_t forward_xy(const NormForward& p, hipStream_t s) {
   if (chunks <= 64) CR_NF(1, 1);
   else if (p.rows > 1024 && chunks <= 128) CR_NF(1, 2);
   else if (p.rows > 1024 && chunks <= 256) CR_NF(1, 4);
-  else if (p.rows > 1024 && chunks <= 512) CR_NF(1, 8);
   else if (chunks <= 256) CR_NF(4, 1);
   else if (chunks <= 512) CR_NF(4, 2);
   else if (chunks <= 1024) CR_NF(4, 4);
