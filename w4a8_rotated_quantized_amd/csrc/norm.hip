@@ -337,13 +337,13 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
 }
 
 // dw and db of sequence blockIdx.y: the slots of the parts that hold its rows, in order.
-// A wave reads 128 columns of a slot, 16 waves share the slots, each with several on their way.
+// A wave reads 64 columns of a slot, 16 waves share the slots, each with several on their way.
 constexpr int JOIN_WAVES = 16;
 __global__ __launch_bounds__(64 * JOIN_WAVES) void norm_join_kernel(NormBackward p) {
-  __shared__ float2 lds[JOIN_WAVES][64];
+  __shared__ float lds[JOIN_WAVES][64];
   const int s = blockIdx.y;
   const int l = threadIdx.x & 63, share = threadIdx.x >> 6;
-  const int64_t c = ((int64_t)blockIdx.x * 64 + l) * 2;
+  const int64_t c = (int64_t)blockIdx.x * 64 + l;
   int64_t lo = 0, hi = p.rows;
   if (p.off) {
     // the sequence begins at the largest offset up to off[s]
@@ -360,33 +360,22 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void norm_join_kernel(NormBackward
   const float* from = blockIdx.z ? p.parts_b : p.parts_w;
   float* to = blockIdx.z ? p.db : p.dw;
   if (!to) return;
-  float2 sum = {0.f, 0.f};
+  float sum = 0.f;
   if (lo < hi && c < p.C) {
     const int first = (int)(lo / p.part_rows), last = (int)((hi - 1) / p.part_rows);
     const int n = last - first + 1, per = (n + JOIN_WAVES - 1) / JOIN_WAVES;
     const int q1 = min(first + (share + 1) * per, last + 1);
     const float* at = from + ((int64_t)(first + share * per) + s) * p.C + c;
 #pragma unroll 8
-    for (int q = first + share * per; q < q1; ++q, at += p.C) {
-      const float2 v = *reinterpret_cast<const float2*>(at);
-      sum.x += v.x;
-      sum.y += v.y;
-    }
+    for (int q = first + share * per; q < q1; ++q, at += p.C) sum += *at;
   }
   lds[share][l] = sum;
   __syncthreads();
   if (share == 0 && c < p.C) {
 #pragma unroll
-    for (int o = 1; o < JOIN_WAVES; ++o) {
-      sum.x += lds[o][l].x;
-      sum.y += lds[o][l].y;
-    }
-    float2* d = reinterpret_cast<float2*>(to + (int64_t)s * p.C + c);
-    if (p.accumulate) {
-      sum.x += d->x;
-      sum.y += d->y;
-    }
-    *d = sum;
+    for (int o = 1; o < JOIN_WAVES; ++o) sum += lds[o][l];
+    float* d = to + (int64_t)s * p.C + c;
+    *d = p.accumulate ? *d + sum : sum;
   }
 }
 
@@ -412,10 +401,13 @@ hipError_t launch_norm_forward(const NormForward& p, hipStream_t s) {
   return p.y_f32 ? forward_xy<false, true>(p, s) : forward_xy<false, false>(p, s);
 }
 
-// parts of the backward pass: about two blocks a compute unit, whole rounds of a block's waves
+// Parts of the backward pass: as many blocks as the chip holds at once (two, three, two and one a compute unit by
+// their waves), whole rounds of a block's waves. More parts hide more of a row's latency and make more slots to
+// join. Both launches, 256, 512, 768, 1024 parts, in us: 8192 x 1024: 23, 19, 25, 24; 8192 x 4096: 101, 76, 73, 87;
+// 8192 x 12288: 209, 229, 246, 258.
 int norm_parts(int64_t rows, int64_t C, int* part_rows) {
-  const int step = C <= 1024 ? 4 : 1;
-  int64_t per = (rows + 511) / 512;
+  const int step = C <= 1024 ? 4 : 1, most = C <= 1024 ? 512 : C <= 4096 ? 768 : C <= 8192 ? 512 : 256;
+  int64_t per = (rows + most - 1) / most;
   per = (per + step - 1) / step * step;
   *part_rows = (int)per;
   return (int)((rows + per - 1) / per);
@@ -459,7 +451,7 @@ hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int*
   *kernels = 1;
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.parts_w) return e;
-  hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((p.C + 127) / 128), (unsigned)p.S, 2), dim3(64 * JOIN_WAVES), 0, s, p);
+  hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((p.C + 63) / 64), (unsigned)p.S, 2), dim3(64 * JOIN_WAVES), 0, s, p);
   *kernels = 2;
   return hipGetLastError();
 }
