@@ -679,7 +679,8 @@ cr_status convrot_act_backward(const void* dy, int64_t lddy, const void* codes, 
  *                     1/sqrt(rot_group)) and rounded once
  *   mxfp4_gemm        out[m, n] = sum_k a[m, k] w[n, k] + bias[n]; a and w of the
  *                     same K and rotation. Products and scales are exact, sums
- *                     float32 in an order fixed by the sizes; out is rounded once.
+ *                     float32 in an order fixed by the sizes (those below 2^-126 may
+ *                     come out as 0); out is rounded once.
  *                     out CR_OUT_BF16 or CR_OUT_F32, leading dimension ldc; bias
  *                     optional bf16 [N].
  *   The gradient of the linear: dx = dy W is mxfp4_gemm of dy and of W^T quantized
@@ -721,8 +722,9 @@ cr_status mxfp4_gemm(const void* a_codes, const void* a_scales, const void* w_co
  *   reaches d_weight and d_bias of its sequence only.
  *
  *   x            bf16 or float32 (x_type) [rows, C], leading dimension ldx
- *   weight, bias bf16 or float32 (affine_type, both the same) [S, C]; each may be
- *                NULL (weight: 1 whatever one_plus is, bias: 0)
+ *   weight, bias bf16 or float32 (affine_type, both the same) [S, C], leading dimensions
+ *                ldw and ldbias (not read with S = 1), so that both can be columns of one
+ *                modulation tensor; each may be NULL (weight: 1 whatever one_plus is, bias: 0)
  *   one_plus     0, or 1: the weight is given without its 1 (adaLN's scale)
  *   seg_offsets  int32 [S + 1] on the device, ascending; NULL with S = 1: all rows
  *                are one sequence. Empty sequences are fine. One below an earlier one
@@ -741,18 +743,18 @@ cr_status mxfp4_gemm(const void* a_codes, const void* a_scales, const void* w_co
  *                refuses the sizes), needed for d_weight and d_bias; any contents. Calls
  *                that share one must be ordered on one stream.
  * Shape: 1 <= rows < 2^26, C a multiple of 8 from 8 to 16384, 1 <= S <= 4096, leading
- * dimensions multiples of 8, not below C and below 2^31. Forward one launch,
- * backward one or two.
+ * dimensions multiples of 8, not below C and below 2^31. Outputs must not overlap inputs
+ * in any other way than named. Forward one launch, backward one or two.
  */
-cr_status convrot_layer_norm_forward(const void* x, cr_out x_type, int64_t ldx, const void* weight, const void* bias,
-                                     cr_out affine_type, int one_plus, const int32_t* seg_offsets, int S, double eps,
+cr_status convrot_layer_norm_forward(const void* x, cr_out x_type, int64_t ldx, const void* weight, int64_t ldw,
+                                     const void* bias, int64_t ldbias, cr_out affine_type, int one_plus, const int32_t* seg_offsets, int S, double eps,
                                      void* y, cr_out y_type, int64_t ldy, float* mean, float* rstd,
                                      int64_t rows, int64_t C, hipStream_t stream);
 
 size_t convrot_layer_norm_backward_workspace_size(int64_t rows, int64_t C, int S);
 
 cr_status convrot_layer_norm_backward(const void* dy, cr_out dy_type, int64_t lddy, const void* x, cr_out x_type,
-                                      int64_t ldx, const float* mean, const float* rstd, const void* weight,
+                                      int64_t ldx, const float* mean, const float* rstd, const void* weight, int64_t ldw,
                                       cr_out affine_type, int one_plus, const int32_t* seg_offsets, int S,
                                       const void* dx_base, int64_t ldb, void* dx, cr_out dx_type, int64_t lddx,
                                       float* d_weight, float* d_bias, int accumulate, int64_t rows, int64_t C,

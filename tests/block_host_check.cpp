@@ -59,9 +59,9 @@ int main() {
         mxfp4_quantize(ptr(), lk, M, K, pick(INTS), ptr(), ptr(), nullptr),
         mxfp4_dequantize(ptr(), ptr(), M, K, pick(INTS), ptr(), out(), lk, nullptr),
         mxfp4_gemm(ptr(), ptr(), ptr(), ptr(), ptr(), ptr(), out(), ln, M, N, K, nullptr),
-        convrot_layer_norm_forward(ptr(), out(), lk, ptr(), ptr(), out(), (int)(next_u64() % 3), iptr(), S, real, ptr(), out(), lk,
+        convrot_layer_norm_forward(ptr(), out(), lk, ptr(), lk, ptr(), ln, out(), (int)(next_u64() % 3), iptr(), S, real, ptr(), out(), lk,
                                    fptr(), fptr(), M, K, nullptr),
-        convrot_layer_norm_backward(ptr(), out(), lk, ptr(), out(), lk, fptr(), fptr(), ptr(), out(), (int)(next_u64() % 3), iptr(),
+        convrot_layer_norm_backward(ptr(), out(), lk, ptr(), out(), lk, fptr(), fptr(), ptr(), ln, out(), (int)(next_u64() % 3), iptr(),
                                     S, ptr(), lk, ptr(), out(), lk, fptr(), fptr(), (int)(next_u64() & 1), M, K, ptr(), pick(WSB),
                                     nullptr),
         convrot_adamw_step(have ? list.data() : nullptr, have, out(), bits, real, beta, beta, real, real,

@@ -60,12 +60,12 @@ def test_mx_validation(cr):
 
 
 def test_norm_validation(cr):
-    def f(x=A, xt=0, ldx=64, w=A, b=A, at=0, plus=0, off=None, S=1, eps=1e-6, y=A, yt=0, ldy=64, m=A, r=A, rows=5, C=64):
-        return cr.lib.convrot_layer_norm_forward(x, xt, ldx, w, b, at, plus, off, S, eps, y, yt, ldy, m, r, rows, C, None)
+    def f(x=A, xt=0, ldx=64, w=A, ldw=16392, b=A, ldbias=16392, at=0, plus=0, off=None, S=1, eps=1e-6, y=A, yt=0, ldy=64, m=A, r=A, rows=5, C=64):
+        return cr.lib.convrot_layer_norm_forward(x, xt, ldx, w, ldw, b, ldbias, at, plus, off, S, eps, y, yt, ldy, m, r, rows, C, None)
 
-    def b(dy=A, dyt=0, lddy=64, x=A, xt=0, ldx=64, m=A, r=A, w=A, at=0, plus=0, off=None, S=1, base=None, ldb=64, dx=A, dxt=0,
+    def b(dy=A, dyt=0, lddy=64, x=A, xt=0, ldx=64, m=A, r=A, w=A, ldw=16392, at=0, plus=0, off=None, S=1, base=None, ldb=64, dx=A, dxt=0,
           lddx=64, dw=A, db=A, acc=0, rows=5, C=64, ws=A, wsb=1 << 30):
-        return cr.lib.convrot_layer_norm_backward(dy, dyt, lddy, x, xt, ldx, m, r, w, at, plus, off, S, base, ldb, dx, dxt, lddx, dw,
+        return cr.lib.convrot_layer_norm_backward(dy, dyt, lddy, x, xt, ldx, m, r, w, ldw, at, plus, off, S, base, ldb, dx, dxt, lddx, dw,
                                                   db, acc, rows, C, ws, wsb, None)
 
     assert f() == 4 and f(w=None, b=None) == 4 and f(off=A, S=7, plus=1) == 4
@@ -91,6 +91,10 @@ def test_norm_validation(cr):
         assert f(**wide, **k) == 2, k
         assert b(lddy=16392, ldx=16392, lddx=16392, **k) == 2, k
     assert f(ldx=56) == 2 and f(ldy=68) == 2 and b(lddy=56) == 2 and b(lddx=1 << 31) == 2 and b(base=A + 64, ldb=56) == 2
+    for ld in (0, 56, 68, 1 << 31):
+        assert f(off=A, S=2, ldw=ld) == 2 and f(off=A, S=2, ldbias=ld) == 2 and b(off=A, S=2, ldw=ld) == 2
+        assert f(ldw=ld, ldbias=ld) == 4 and b(ldw=ld) == 4                # one row: not read
+        assert f(off=A, S=2, w=None, ldw=ld) == 4 and f(off=A, S=2, b=None, ldbias=ld) == 4
     need = cr.convrot_layer_norm_backward_workspace_size(5, 64, 1)
     assert need > 0 and b(wsb=need) == 4 and b(wsb=need - 1) == 6
     for k in ((0, 64, 1), (5, 12, 1), (5, 64, 0), (5, 64, 4097)):

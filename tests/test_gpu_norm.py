@@ -244,6 +244,27 @@ def test_offsets_that_descend(cr):
         assert np.allclose(_f64(dw), dww, atol=1e-4, rtol=1e-4) and np.allclose(_f64(db), dbw, atol=1e-4, rtol=1e-4), off
 
 
+def test_modulation_columns(cr):
+    """Weight and bias as column blocks of one modulation tensor, as the adaLN layer gives it."""
+    g = np.random.default_rng(13)
+    M, C, S = 90, 328, 3
+    x, dy = _input(g, (M, C), torch.bfloat16), _input(g, (M, C), torch.bfloat16)
+    off = torch.tensor([0, 30, 31, 90], dtype=torch.int32, device=DEV)
+    for dtype in (torch.bfloat16, torch.float32):
+        mod = dev(g.standard_normal((S, 6 * C)).astype(np.float32)).to(dtype)
+        shift, scale = mod.chunk(6, 1)[3], mod.chunk(6, 1)[1]
+        y, mean, rstd = cr.convrot_layer_norm_forward(x, scale, shift, seg_offsets=off, one_plus=True)
+        y2, _, _ = cr.convrot_layer_norm_forward(x, scale.contiguous(), shift.contiguous(), seg_offsets=off, one_plus=True)
+        assert torch.equal(y, y2)
+        a = cr.convrot_layer_norm_backward(dy, x, mean, rstd, scale, seg_offsets=off, one_plus=True)
+        b = cr.convrot_layer_norm_backward(dy, x, mean, rstd, scale.contiguous(), seg_offsets=off, one_plus=True)
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    # one sequence takes its only row wherever the next would lie
+    y, _, _ = cr.convrot_layer_norm_forward(x, scale[:1], shift[:1], seg_offsets=off[[0, 3]].contiguous())
+    want, _, _ = cr.convrot_layer_norm_forward(x, scale[0].contiguous(), shift[0].contiguous())
+    assert torch.equal(y, want)
+
+
 def test_side_stream_and_graph(cr):
     """On a given stream, and captured: replays equal the eager results, other work between them."""
     g = np.random.default_rng(12)

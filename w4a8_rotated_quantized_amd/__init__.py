@@ -116,10 +116,10 @@ _SIGS = {
     "mxfp4_quantize": (_i, [_vp, _i64, _i64, _i64, _i, _vp, _vp, _vp]),
     "mxfp4_dequantize": (_i, [_vp, _vp, _i64, _i64, _i, _vp, _i, _i64, _vp]),
     "mxfp4_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i64, _i64, _i64, _i64, _vp]),
-    "convrot_layer_norm_forward": (_i, [_vp, _i, _i64, _vp, _vp, _i, _i, _vp, _i, ctypes.c_double, _vp, _i, _i64, _vp, _vp,
+    "convrot_layer_norm_forward": (_i, [_vp, _i, _i64, _vp, _i64, _vp, _i64, _i, _i, _vp, _i, ctypes.c_double, _vp, _i, _i64, _vp, _vp,
                                         _i64, _i64, _vp]),
     "convrot_layer_norm_backward_workspace_size": (_sz, [_i64, _i64, _i]),
-    "convrot_layer_norm_backward": (_i, [_vp, _i, _i64, _vp, _i, _i64, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _i64, _vp, _i,
+    "convrot_layer_norm_backward": (_i, [_vp, _i, _i64, _vp, _i, _i64, _vp, _vp, _vp, _i64, _i, _i, _vp, _i, _vp, _i64, _vp, _i,
                                          _i64, _vp, _vp, _i, _i64, _i64, _vp, _sz, _vp]),
     "convrot_adamw_step": (_i, [_vp, _i, _i, _i, *[ctypes.c_double] * 5, _i64, _vp, ctypes.c_uint32, _vp]),
     "convrot_adamw_moments": (_i, [_vp, _i, _vp, _vp, _vp]),
@@ -747,9 +747,9 @@ def convrot_layer_norm_forward(x, weight=None, bias=None, seg_offsets=None, eps=
                                out=None, mean=None, rstd=None, stream=None):
     """y = (x - mean) rstd (weight + one_plus) + bias over the last dimension of x
     [M, C] (bf16 or float32; C a multiple of 8). weight, bias: [C], or [S, C]
-    with seg_offsets int32 [S + 1], a pair for the rows seg_offsets[s] ..
-    seg_offsets[s+1] of each sequence (adaLN: one_plus=True with the scales as
-    weight). Rows in no sequence are left as they are in the given outputs. Returns
+    (rows may lie further apart: columns of one modulation tensor) with seg_offsets
+    int32 [S + 1], a pair for the rows seg_offsets[s] .. seg_offsets[s+1] of each
+    sequence (adaLN: one_plus=True with the scales as weight). Rows in no sequence are left as they are in the given outputs. Returns
     (y in out_type, mean, rstd): mean and rstd float32 [M] are what
     convrot_layer_norm_backward reads. Not recorded by autograd."""
     r = _run(_native.layer_norm_forward, x, "x", stream,

@@ -245,15 +245,15 @@ PyObject* mx_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // layer norm
 // ---------------------------------------------------------------------------
 struct Affine {
-  int64_t S;
+  int64_t S, ldw, ldb;
   cr_out type;
   const void *w, *b;
   const int32_t* off;
-  std::vector<int64_t> shape;
+  std::vector<int64_t> shape;      // of their gradients
 };
-// weight, bias [C], or [S, C] with seg_offsets [S + 1]
+// weight, bias [C], or [S, C] (rows may lie further apart) with seg_offsets [S + 1]
 Affine affine(const Tensor* w, const Tensor* b, const Tensor* off, int index, int64_t C) {
-  Affine r{1, CR_OUT_F32, nullptr, nullptr, nullptr, {C}};
+  Affine r{1, C, C, CR_OUT_F32, nullptr, nullptr, nullptr, {C}};
   if (off) {
     if (off->dim() != 1 || off->size(0) < 1) wrong("seg_offsets is int32 [S + 1]");
     r.S = off->size(0) - 1;
@@ -263,8 +263,13 @@ Affine affine(const Tensor* w, const Tensor* b, const Tensor* off, int index, in
   if (const Tensor* first = w ? w : b) {
     r.type = float_type(*first, "weight and bias");
     const ScalarType dt = first->scalar_type();
-    r.w = dense_or_null(w, "weight", dt, index, r.shape);
-    r.b = dense_or_null(b, "bias", dt, index, r.shape);
+    if (off) {
+      r.w = w ? spaced(*w, "weight", dt, index, r.S, C, &r.ldw) : nullptr;
+      r.b = b ? spaced(*b, "bias", dt, index, r.S, C, &r.ldb) : nullptr;
+    } else {
+      r.w = dense_or_null(w, "weight", dt, index, r.shape);
+      r.b = dense_or_null(b, "bias", dt, index, r.shape);
+    }
   }
   return r;
 }
@@ -291,7 +296,7 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool plus = truth(a[5]);
     const Tensor out = go ? *go : empty({M, C}, dt, x);
     const Tensor mean = gm ? *gm : empty({M}, ScalarType::Float, x), rstd = gr ? *gr : empty({M}, ScalarType::Float, x);
-    const cr_status st = convrot_layer_norm_forward(px, x_type, ldx, f.w, f.b, f.type, plus, f.off, count_of(f.S), eps,
+    const cr_status st = convrot_layer_norm_forward(px, x_type, ldx, f.w, f.ldw, f.b, f.ldb, f.type, plus, f.off, count_of(f.S), eps,
                                                     out.data_ptr(), (cr_out)type, ldy, static_cast<float*>(mean.data_ptr()),
                                                     static_cast<float*>(rstd.data_ptr()), M, C, stream_of(a[10]));
     return st ? refused(st) : pack({&out, &mean, &rstd});
@@ -340,7 +345,7 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = gs ? *gs : empty({(int64_t)(need < 16 ? 16 : need)}, ScalarType::Byte, dy);
     }
     const cr_status st = convrot_layer_norm_backward(
-        pdy, dy_type, lddy, px, x_type, ldx, pm, pr, f.w, f.type, truth(a[6]), f.off, count_of(f.S), pb, ldb,
+        pdy, dy_type, lddy, px, x_type, ldx, pm, pr, f.w, f.ldw, f.type, truth(a[6]), f.off, count_of(f.S), pb, ldb,
         want_dx ? dx.data_ptr() : nullptr, (cr_out)type, lddx, want_w ? static_cast<float*>(dw.data_ptr()) : nullptr,
         want_w ? static_cast<float*>(db.data_ptr()) : nullptr, accumulate, M, C, want_w ? ws.data_ptr() : nullptr,
         want_w ? ws.nbytes() : 0, stream_of(a[16]));

@@ -51,8 +51,9 @@ hipError_t launch_mx_gemm(const MxGemm& p, hipStream_t s);
 struct NormForward {
   const void* x;
   int64_t ldx;
-  const void* w;            // [S][C] or null
-  const void* b;
+  const void* w;            // [S][ldw] or null
+  const void* b;            // [S][ldbias] or null
+  int64_t ldw, ldbias;
   int w_f32;                // of w and b
   float plus;               // added to w
   const int32_t* off;       // [S + 1], or null: one sequence of all rows
@@ -75,7 +76,8 @@ struct NormBackward {
   int64_t ldx;
   const float* mean;
   const float* rstd;
-  const void* w;            // [S][C] or null
+  const void* w;            // [S][ldw] or null
+  int64_t ldw;
   int w_f32;
   float plus;
   const int32_t* off;

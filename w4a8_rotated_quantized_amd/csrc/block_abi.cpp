@@ -145,8 +145,8 @@ cr_status mxfp4_gemm(const void* a_codes, const void* a_scales, const void* w_co
   return cr::host_finish(cr::launch_mx_gemm(p, stream), cr::HE_MX, 1);
 }
 
-cr_status convrot_layer_norm_forward(const void* x, cr_out x_type, int64_t ldx, const void* weight, const void* bias,
-                                     cr_out affine_type, int one_plus, const int32_t* seg_offsets, int S, double eps,
+cr_status convrot_layer_norm_forward(const void* x, cr_out x_type, int64_t ldx, const void* weight, int64_t ldw,
+                                     const void* bias, int64_t ldbias, cr_out affine_type, int one_plus, const int32_t* seg_offsets, int S, double eps,
                                      void* y, cr_out y_type, int64_t ldy, float* mean, float* rstd,
                                      int64_t rows, int64_t C, hipStream_t stream) {
   cr::host_tag("convrot_layer_norm_forward", rows, C, S, x_type, affine_type, y_type);
@@ -159,13 +159,16 @@ cr_status convrot_layer_norm_forward(const void* x, cr_out x_type, int64_t ldx, 
     if ((st = float_output(type)) != CR_OK) return st;
   if ((st = norm_sizes(rows, C, S)) != CR_OK) return st;
   if (!seg_offsets && S != 1) return CR_ERR_INVALID_ARGUMENT;
-  if (bad_ld(ldx, C) || bad_ld(ldy, C)) return CR_ERR_UNSUPPORTED_SHAPE;
+  if (bad_ld(ldx, C) || bad_ld(ldy, C) || (S > 1 && ((weight && bad_ld(ldw, C)) || (bias && bad_ld(ldbias, C)))))
+    return CR_ERR_UNSUPPORTED_SHAPE;
   if ((st = cr::host_device_check()) != CR_OK) return st;
   cr::NormForward p{};
   p.x = x;
   p.ldx = ldx;
   p.w = weight;
+  p.ldw = ldw;
   p.b = bias;
+  p.ldbias = ldbias;
   p.w_f32 = affine_type == CR_OUT_F32;
   p.plus = one_plus ? 1.f : 0.f;
   p.off = seg_offsets;
@@ -188,7 +191,7 @@ size_t convrot_layer_norm_backward_workspace_size(int64_t rows, int64_t C, int S
 }
 
 cr_status convrot_layer_norm_backward(const void* dy, cr_out dy_type, int64_t lddy, const void* x, cr_out x_type,
-                                      int64_t ldx, const float* mean, const float* rstd, const void* weight,
+                                      int64_t ldx, const float* mean, const float* rstd, const void* weight, int64_t ldw,
                                       cr_out affine_type, int one_plus, const int32_t* seg_offsets, int S,
                                       const void* dx_base, int64_t ldb, void* dx, cr_out dx_type, int64_t lddx,
                                       float* d_weight, float* d_bias, int accumulate, int64_t rows, int64_t C,
@@ -205,7 +208,8 @@ cr_status convrot_layer_norm_backward(const void* dy, cr_out dy_type, int64_t ld
     if ((st = float_output(type)) != CR_OK) return st;
   if ((st = norm_sizes(rows, C, S)) != CR_OK) return st;
   if (!seg_offsets && S != 1) return CR_ERR_INVALID_ARGUMENT;
-  if (bad_ld(lddy, C) || bad_ld(ldx, C) || (dx && bad_ld(lddx, C)) || (dx && dx_base && bad_ld(ldb, C)))
+  if (bad_ld(lddy, C) || bad_ld(ldx, C) || (dx && bad_ld(lddx, C)) || (dx && dx_base && bad_ld(ldb, C)) ||
+      (S > 1 && weight && bad_ld(ldw, C)))
     return CR_ERR_UNSUPPORTED_SHAPE;
   if (dx && dx_base == dx && ldb != lddx) return CR_ERR_INVALID_ARGUMENT;
   if (d_weight || d_bias) {
@@ -221,6 +225,7 @@ cr_status convrot_layer_norm_backward(const void* dy, cr_out dy_type, int64_t ld
   p.mean = mean;
   p.rstd = rstd;
   p.w = weight;
+  p.ldw = ldw;
   p.w_f32 = affine_type == CR_OUT_F32;
   p.plus = one_plus ? 1.f : 0.f;
   p.off = seg_offsets;

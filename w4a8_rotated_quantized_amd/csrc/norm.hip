@@ -148,8 +148,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * W * 64 + lane) * 8;
-      if (c < p.C && p.w) load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w[v]);
-      if (c < p.C && p.b) load_affine(p.b, p.w_f32, (int64_t)s * p.C + c, b[v]);
+      if (c < p.C && p.w) load_affine(p.w, p.w_f32, s * p.ldw + c, w[v]);
+      if (c < p.C && p.b) load_affine(p.b, p.w_f32, s * p.ldbias + c, b[v]);
     }
   }
   float sum = 0.f;
@@ -182,12 +182,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
     for (int e = 0; e < 8; ++e) y[e] = (x[v].get(e) - mean) * rstd;
     constexpr int ONE = EARLY ? 1 : 0;
     if (p.w) {
-      if constexpr (!EARLY) load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w[0]);
+      if constexpr (!EARLY) load_affine(p.w, p.w_f32, s * p.ldw + c, w[0]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] *= w[ONE * v][e] + p.plus;
     }
     if (p.b) {
-      if constexpr (!EARLY) load_affine(p.b, p.w_f32, (int64_t)s * p.C + c, b[0]);
+      if constexpr (!EARLY) load_affine(p.b, p.w_f32, s * p.ldbias + c, b[0]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] += b[ONE * v][e];
     }
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
         w[v][e] = 1.f;
       }
       if (p.w && c < p.C) {
-        load_affine(p.w, p.w_f32, (int64_t)s * p.C + c, w[v]);
+        load_affine(p.w, p.w_f32, s * p.ldw + c, w[v]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[v][e] += p.plus;
       }
