@@ -794,6 +794,12 @@ def _listed(*lists):
     return [t for held in lists if held is not None for t in held]
 
 
+def _refused_lists(status, where, **lists):
+    """Raises for lists that were not accepted, naming those that hold addresses that the library does not take."""
+    off = [k for k, held in lists.items() if held is not None and any(t.data_ptr() % 16 for t in held)]
+    _check(status, f"{where} ({', '.join(off)}: not at a multiple of 16 bytes)" if off else where)
+
+
 def convrot_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
                        copies=None, grad_scale=None, exp_avg_scales=None, exp_avg_sq_scales=None, seed=0, stream=None):
     """One AdamW step over lists of tensors, in place: params float32, grads bf16
@@ -809,7 +815,8 @@ def convrot_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1=0.9
              (params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales, grad_scale, step, lr, beta1, beta2,
               eps, weight_decay, seed & 0xFFFFFFFF),
              lambda r: (*_listed(params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales), grad_scale))
-    _check(r, "convrot_adamw_step")
+    if r:
+        _refused_lists(r, "convrot_adamw_step", params=params, grads=grads, exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs, copies=copies)
 
 
 def convrot_adamw_moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, exp_avg_out=None, exp_avg_sq_out=None,
@@ -822,5 +829,5 @@ def convrot_adamw_moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scal
              (exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, exp_avg_out, exp_avg_sq_out),
              lambda r: (*_listed(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales), *r))
     if type(r) is int:
-        _check(r, "convrot_adamw_moments")
+        _refused_lists(r, "convrot_adamw_moments", exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs)
     return r
