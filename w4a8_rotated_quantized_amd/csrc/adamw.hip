@@ -178,12 +178,13 @@ CR_DEV uint32_t encode(v4f x, const uint32_t (&h16)[4], float* scale) {
   return codes;
 }
 
-// the tensor of a chunk
-CR_DEV int tensor_of(const AdamwTable& t, int chunk) {
+// the entry of a chunk: the last that begins at or before it and holds something
+template <typename T>
+CR_DEV int entry_of(const T& t, int chunk) {
   int lo = 0, hi = t.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (t.first[mid] <= chunk) lo = mid;
+    if (t.t[mid].first <= chunk) lo = mid;
     else hi = mid;
   }
   return lo;
@@ -191,7 +192,7 @@ CR_DEV int tensor_of(const AdamwTable& t, int chunk) {
 
 // Four consecutive elements a lane, FULL: all inside the tensor.
 template <bool G16, int BITS, bool FULL>
-CR_DEV void step_chunk(const cr_adamw_tensor& a, const AdamwStep& p, int64_t base, uint32_t key, float gs) {
+CR_DEV void step_chunk(const AdamwEntry& a, const AdamwStep& p, int64_t base, uint32_t key, float gs) {
   const int64_t i = base + threadIdx.x * 4;
   const int64_t left = a.n - i;
   const int n = FULL || left >= 4 ? 4 : left > 0 ? (int)left : 0;
@@ -201,12 +202,12 @@ CR_DEV void step_chunk(const cr_adamw_tensor& a, const AdamwStep& p, int64_t bas
   const v4f grad = G16 ? load_bf16(a.grad, i, n) : load_f32(a.grad, i, n);
   v4f m, v;
   if constexpr (BITS == 8) {
-    m = avg_values(load_codes(a.exp_avg, i, n), some ? a.avg_scales[block] : 0.f);
-    v = root_values(load_codes(a.exp_avg_sq, i, n), some ? a.sq_scales[block] : 0.f);
+    m = avg_values(load_codes(a.avg, i, n), some ? a.avg_scales[block] : 0.f);
+    v = root_values(load_codes(a.sq, i, n), some ? a.sq_scales[block] : 0.f);
     v = v * v;
   } else {
-    m = load_f32(a.exp_avg, i, n);
-    v = load_f32(a.exp_avg_sq, i, n);
+    m = load_f32(a.avg, i, n);
+    v = load_f32(a.sq, i, n);
   }
   v4f root;
 #pragma unroll
@@ -230,39 +231,38 @@ CR_DEV void step_chunk(const cr_adamw_tensor& a, const AdamwStep& p, int64_t bas
       if (!FULL && e >= n) m[e] = root[e] = 0.f;         // past the end: no part of the largest
     }
     float sm, sv;
-    store_codes(a.exp_avg, i, n, encode<true>(m, um, &sm));
-    store_codes(a.exp_avg_sq, i, n, encode<false>(root, uv, &sv));
+    store_codes(a.avg, i, n, encode<true>(m, um, &sm));
+    store_codes(a.sq, i, n, encode<false>(root, uv, &sv));
     if (some && (threadIdx.x & 63) == 0) {
       a.avg_scales[block] = sm;
       a.sq_scales[block] = sv;
     }
   } else {
-    store_f32(a.exp_avg, i, n, m);
-    store_f32(a.exp_avg_sq, i, n, v);
+    store_f32(a.avg, i, n, m);
+    store_f32(a.sq, i, n, v);
   }
 }
 
 template <bool G16, int BITS>
 __global__ __launch_bounds__(256) void adamw_step_kernel(AdamwTable t, AdamwStep p) {
-  const int which = tensor_of(t, (int)blockIdx.x);
-  const cr_adamw_tensor& a = t.t[which];
-  const int64_t base = (int64_t)((int)blockIdx.x - t.first[which]) * ADAMW_CHUNK;
+  const int which = entry_of(t, (int)blockIdx.x);
+  const AdamwEntry& a = t.t[which];
+  const int64_t base = (int64_t)((int)blockIdx.x - a.first) * ADAMW_CHUNK;
   const float gs = p.grad_scale ? *p.grad_scale : 1.f;
   const uint32_t key = BITS == 8 ? mix32(p.seed + 0x9E3779B9u * (uint32_t)(t.ordinal + which + 1)) : 0u;
   if (base + ADAMW_CHUNK <= a.n) step_chunk<G16, BITS, true>(a, p, base, key, gs);
   else step_chunk<G16, BITS, false>(a, p, base, key, gs);
 }
 
-__global__ __launch_bounds__(256) void adamw_moments_kernel(AdamwTable t, int64_t at, float* avg, float* sq) {
-  const int which = tensor_of(t, (int)blockIdx.x);
-  at += t.before[which];
-  const cr_adamw_tensor& a = t.t[which];
-  const int64_t i = (int64_t)((int)blockIdx.x - t.first[which]) * ADAMW_CHUNK + threadIdx.x * 4;
+__global__ __launch_bounds__(256) void adamw_moments_kernel(MomentsTable t, float* avg, float* sq) {
+  const MomentsEntry& a = t.t[entry_of(t, (int)blockIdx.x)];
+  const int64_t i = (int64_t)((int)blockIdx.x - a.first) * ADAMW_CHUNK + threadIdx.x * 4;
+  const int64_t at = a.at;
   const int64_t left = a.n - i;
   const int n = left >= 4 ? 4 : left > 0 ? (int)left : 0;
   if (n == 0) return;
-  const v4f m = avg_values(load_codes(a.exp_avg, i, n), a.avg_scales[i / ADAMW_BLOCK]);
-  v4f v = root_values(load_codes(a.exp_avg_sq, i, n), a.sq_scales[i / ADAMW_BLOCK]);
+  const v4f m = avg_values(load_codes(a.avg, i, n), a.avg_scales[i / ADAMW_BLOCK]);
+  v4f v = root_values(load_codes(a.sq, i, n), a.sq_scales[i / ADAMW_BLOCK]);
   v = v * v;
   if (n == 4 && (at & 3) == 0) {
     *reinterpret_cast<v4f*>(avg + at + i) = m;
@@ -277,20 +277,20 @@ __global__ __launch_bounds__(256) void adamw_moments_kernel(AdamwTable t, int64_
   }
 }
 
-hipError_t launch_adamw_step(const AdamwTable& t, const AdamwStep& p, hipStream_t s) {
-  const dim3 grid((unsigned)t.first[t.count]);
-  if (p.bits == 8) {
-    if (p.grad_bf16) hipLaunchKernelGGL((adamw_step_kernel<true, 8>), grid, dim3(256), 0, s, t, p);
+hipError_t launch_adamw_step(const AdamwTable& t, const AdamwStep& p, bool grad_bf16, int bits, int chunks, hipStream_t s) {
+  const dim3 grid((unsigned)chunks);
+  if (bits == 8) {
+    if (grad_bf16) hipLaunchKernelGGL((adamw_step_kernel<true, 8>), grid, dim3(256), 0, s, t, p);
     else hipLaunchKernelGGL((adamw_step_kernel<false, 8>), grid, dim3(256), 0, s, t, p);
   } else {
-    if (p.grad_bf16) hipLaunchKernelGGL((adamw_step_kernel<true, 32>), grid, dim3(256), 0, s, t, p);
+    if (grad_bf16) hipLaunchKernelGGL((adamw_step_kernel<true, 32>), grid, dim3(256), 0, s, t, p);
     else hipLaunchKernelGGL((adamw_step_kernel<false, 32>), grid, dim3(256), 0, s, t, p);
   }
   return hipGetLastError();
 }
 
-hipError_t launch_adamw_moments(const AdamwTable& t, int64_t at, float* avg, float* sq, hipStream_t s) {
-  hipLaunchKernelGGL(adamw_moments_kernel, dim3((unsigned)t.first[t.count]), dim3(256), 0, s, t, at, avg, sq);
+hipError_t launch_adamw_moments(const MomentsTable& t, float* avg, float* sq, int chunks, hipStream_t s) {
+  hipLaunchKernelGGL(adamw_moments_kernel, dim3((unsigned)chunks), dim3(256), 0, s, t, avg, sq);
   return hipGetLastError();
 }
 

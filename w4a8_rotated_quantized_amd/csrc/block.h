@@ -101,26 +101,50 @@ struct NormBackward {
 size_t norm_backward_ws_bytes(int64_t rows, int64_t C, int S);
 hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int* kernels);
 
-// Tensors of one launch of the optimizer step: their table rides in the kernel's arguments.
-constexpr int ADAMW_TENSORS = 48;
+// Tensors of one launch of the optimizer step: their table rides in the kernel's arguments,
+// which take 4096 bytes.
+constexpr int ADAMW_TENSORS = 63, ADAMW_MOMENTS = 84;
 constexpr int ADAMW_CHUNK = 1024;    // elements a block takes
 constexpr int ADAMW_BLOCK = 256;     // elements that share the scale of an 8-bit moment
 
+struct AdamwEntry {
+  void* param;
+  const void* grad;
+  void* avg;
+  void* sq;
+  float* avg_scales;
+  float* sq_scales;
+  void* copy;
+  int n;
+  int first;                         // chunks of the entries before
+};
 struct AdamwTable {
-  cr_adamw_tensor t[ADAMW_TENSORS];
-  int64_t before[ADAMW_TENSORS];     // elements of t[0] .. t[i - 1]
-  int first[ADAMW_TENSORS + 1];      // chunks of t[0] .. t[i - 1]
+  AdamwEntry t[ADAMW_TENSORS];
   int count;
   int ordinal;                       // number of t[0] in the caller's list
+};
+struct MomentsEntry {
+  const void* avg;
+  const void* sq;
+  const float* avg_scales;
+  const float* sq_scales;
+  int64_t at;                        // where it begins in the outputs
+  int n;
+  int first;
+};
+struct MomentsTable {
+  MomentsEntry t[ADAMW_MOMENTS];
+  int count;
 };
 struct AdamwStep {
   float decay, b1, c1, b2, c2, rsqrt_bias2, eps, rate;   // c = 1 - b; rate = lr / (1 - b1^t)
   const float* grad_scale;           // or null
   uint32_t seed;
-  int grad_bf16, bits;
 };
-hipError_t launch_adamw_step(const AdamwTable& t, const AdamwStep& p, hipStream_t s);
-// moments in 8 bits -> float32, tensor after tensor; `at`: where t[0] begins
-hipError_t launch_adamw_moments(const AdamwTable& t, int64_t at, float* avg, float* sq, hipStream_t s);
+static_assert(sizeof(AdamwTable) + sizeof(AdamwStep) <= 4096 && sizeof(MomentsTable) + 2 * sizeof(float*) <= 4096, "arguments of a launch");
+// `chunks` of all entries together
+hipError_t launch_adamw_step(const AdamwTable& t, const AdamwStep& p, bool grad_bf16, int bits, int chunks, hipStream_t s);
+// moments in 8 bits -> float32
+hipError_t launch_adamw_moments(const MomentsTable& t, float* avg, float* sq, int chunks, hipStream_t s);
 
 }  // namespace cr

@@ -59,37 +59,35 @@ cr_status adamw_entries(const cr_adamw_tensor* t, int count, bool step, bool cod
   return CR_OK;
 }
 
-// Calls launch(table) for the entries that hold something, a table at a time; `elements`
-// is what lies before the table's first entry.
-template <typename F>
-hipError_t adamw_tables(const cr_adamw_tensor* t, int count, int* kernels, F launch) {
+// Calls launch(table, chunks) for the entries of a list, a table at a time: tables of the same
+// number of entries, so that the last launch is no stub. fill(entry, tensor, elements before it).
+template <typename Table, int MOST, typename F, typename L>
+hipError_t adamw_tables(const cr_adamw_tensor* t, int count, int* kernels, F fill, L launch) {
   *kernels = 0;
   int64_t elements = 0;
-  // tables of the same number of entries, so that the last launch is no stub
-  const int tables = (count + cr::ADAMW_TENSORS - 1) / cr::ADAMW_TENSORS, per = (count + tables - 1) / tables;
+  const int tables = (count + MOST - 1) / MOST, per = (count + tables - 1) / tables;
   for (int i = 0; i < count;) {
-    cr::AdamwTable table;
+    Table table;
     table.count = 0;
-    table.ordinal = i;
-    int64_t chunks = 0, held = 0;
-    table.first[0] = 0;
-    // every entry takes a place, empty ones no chunk, so that ordinals count them
+    const int begin = i;
+    int64_t chunks = 0;
+    // every entry takes a place, empty ones no chunk, so that their numbers count them
     while (i < count && table.count < per) {
       const int64_t c = (t[i].n + cr::ADAMW_CHUNK - 1) / cr::ADAMW_CHUNK;
       if (table.count && chunks + c >= LD_MAX) break;
-      table.t[table.count] = t[i];
-      table.before[table.count] = held;
+      auto& e = table.t[table.count++];
+      fill(e, t[i], elements);
+      e.n = (int)t[i].n;
+      e.first = (int)chunks;
       chunks += c;
-      held += t[i].n;
-      table.first[++table.count] = (int)chunks;
+      elements += t[i].n;
       ++i;
     }
     if (chunks) {
-      const hipError_t e = launch(table, elements);
+      const hipError_t e = launch(table, begin, (int)chunks);
       if (e != hipSuccess) return e;
       ++*kernels;
     }
-    elements += held;
   }
   return hipSuccess;
 }
@@ -271,12 +269,23 @@ cr_status convrot_adamw_step(const cr_adamw_tensor* tensors, int count, cr_out g
   p.rate = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
   p.grad_scale = grad_scale;
   p.seed = seed;
-  p.grad_bf16 = grad_type == CR_OUT_BF16;
-  p.bits = state_bits;
+  const bool grad_bf16 = grad_type == CR_OUT_BF16;
   int kernels = 0;
-  const hipError_t e = adamw_tables(tensors, count, &kernels, [&](const cr::AdamwTable& t, int64_t) {
-    return cr::launch_adamw_step(t, p, stream);
-  });
+  const hipError_t e = adamw_tables<cr::AdamwTable, cr::ADAMW_TENSORS>(
+      tensors, count, &kernels,
+      [](cr::AdamwEntry& d, const cr_adamw_tensor& t, int64_t) {
+        d.param = t.param;
+        d.grad = t.grad;
+        d.avg = t.exp_avg;
+        d.sq = t.exp_avg_sq;
+        d.avg_scales = t.avg_scales;
+        d.sq_scales = t.sq_scales;
+        d.copy = t.copy;
+      },
+      [&](cr::AdamwTable& t, int begin, int chunks) {
+        t.ordinal = begin;
+        return cr::launch_adamw_step(t, p, grad_bf16, state_bits, chunks, stream);
+      });
   return cr::host_finish(e, cr::HE_LORA, (uint64_t)kernels);
 }
 
@@ -288,9 +297,18 @@ cr_status convrot_adamw_moments(const cr_adamw_tensor* tensors, int count, float
   if (st != CR_OK) return st;
   if ((st = cr::host_device_check()) != CR_OK) return st;
   int kernels = 0;
-  const hipError_t e = adamw_tables(tensors, count, &kernels, [&](const cr::AdamwTable& t, int64_t at) {
-    return cr::launch_adamw_moments(t, at, exp_avg_out, exp_avg_sq_out, stream);
-  });
+  const hipError_t e = adamw_tables<cr::MomentsTable, cr::ADAMW_MOMENTS>(
+      tensors, count, &kernels,
+      [](cr::MomentsEntry& d, const cr_adamw_tensor& t, int64_t before) {
+        d.avg = t.exp_avg;
+        d.sq = t.exp_avg_sq;
+        d.avg_scales = t.avg_scales;
+        d.sq_scales = t.sq_scales;
+        d.at = before;
+      },
+      [&](const cr::MomentsTable& t, int, int chunks) {
+        return cr::launch_adamw_moments(t, exp_avg_out, exp_avg_sq_out, chunks, stream);
+      });
   return cr::host_finish(e, cr::HE_LORA, (uint64_t)kernels);
 }
 
