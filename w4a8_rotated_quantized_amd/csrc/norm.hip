@@ -451,11 +451,13 @@ hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int*
   *kernels = 1;
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.parts_w) return e;
-  // 16 waves where a sequence has many slots, 4 where there are few and many sequences instead (800 rows of 3032 in 38
-  // sequences, about 12 slots each: 34 -> 22 us for both launches)
+  // Waves that share a sequence's slots: 4 where it has few (800 rows of 3032 in 38 sequences, about 12 slots each: 34 us
+  // with 16 waves, 22 with 4, for both launches), else 8 once the blocks are more than one a compute unit (8192 x 4096
+  // in 5 sequences: the join alone 9.4 us with 16, 6.5 with 8), else 16 (1531 x 2560: 5.9 us)
   const dim3 join((unsigned)((p.C + 63) / 64), (unsigned)p.S, 2);
-  if (p.parts / p.S >= 32) hipLaunchKernelGGL((norm_join_kernel<16>), join, dim3(1024), 0, s, p);
-  else hipLaunchKernelGGL((norm_join_kernel<4>), join, dim3(256), 0, s, p);
+  if (p.parts / p.S < 32) hipLaunchKernelGGL((norm_join_kernel<4>), join, dim3(256), 0, s, p);
+  else if (join.x * join.y * 2 > 256) hipLaunchKernelGGL((norm_join_kernel<8>), join, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((norm_join_kernel<16>), join, dim3(1024), 0, s, p);
   *kernels = 2;
   return hipGetLastError();
 }
