@@ -35,9 +35,7 @@ CR_DEV void mx_wait_vmcnt() {
 }
 template <int L>
 CR_DEV void mx_wait_stage(int ahead) {   // at most `ahead` later stages (L loads each) left in flight
-  if (ahead >= 4) mx_wait_vmcnt<4 * L>();
-  else if (ahead == 3) mx_wait_vmcnt<3 * L>();
-  else if (ahead == 2) mx_wait_vmcnt<2 * L>();
+  if (ahead == 2) mx_wait_vmcnt<2 * L>();
   else if (ahead == 1) mx_wait_vmcnt<L>();
   else mx_wait_vmcnt<0>();
 }
@@ -57,7 +55,7 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64 * KG, MINB
   constexpr int NW = (BM / (32 * TM)) * WN;
   static_assert(BM % (32 * TM) == 0 && BN % (32 * TN) == 0, "whole wave tiles");
   static_assert(BM % 64 == 0 && BN % 64 == 0, "scale loads take 64 rows");
-  static_assert(S >= 2 && S <= 6, "stages in flight ahead of the current one: 0 to 4");
+  static_assert(S >= 2 && S <= 4, "stages in flight ahead of the current one: 0 to 2");
   constexpr int A_ST = BM * 64, W_ST = BN * 64, SC = A_ST + W_ST, STAGE = SC + (BM + BN) * 4;
   constexpr int NC = SC / 1024;                        // 1 KB loads of codes
   constexpr int NS = (BM + BN) / 64;                   // 256-byte loads of scale bytes

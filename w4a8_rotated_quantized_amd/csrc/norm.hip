@@ -8,7 +8,7 @@
 // Both sums of a row run over the values held in registers: x is read once,
 // and the variance is that of the differences, which x^2 - mean^2 would lose.
 //
-// A row is shared by W waves (1, 4 or 8), each lane holding eight consecutive
+// A row is shared by W waves (1, 4, 8 or 16), each lane holding eight consecutive
 // columns at a time, V times. The memory rate bounds both directions, so a wave
 // keeps a whole row's loads in flight at once.
 #include "block.h"
@@ -141,17 +141,6 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
     const int c = (v * W * 64 + lane) * 8;
     if (c < p.C) x[v].load(p.x, at + c);
   }
-  // with few values a lane, weight and bias come along: their latency passes with the row's
-  constexpr bool EARLY = V <= 2;
-  float w[EARLY ? V : 1][8], b[EARLY ? V : 1][8];
-  if constexpr (EARLY) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * W * 64 + lane) * 8;
-      if (c < p.C && p.w) load_affine(p.w, p.w_f32, s * p.ldw + c, w[v]);
-      if (c < p.C && p.b) load_affine(p.b, p.w_f32, s * p.ldbias + c, b[v]);
-    }
-  }
   float sum = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -177,19 +166,18 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
   for (int v = 0; v < V; ++v) {
     const int c = (v * W * 64 + lane) * 8;
     if (c >= p.C) continue;
-    float y[8];
+    float y[8], a[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (x[v].get(e) - mean) * rstd;
-    constexpr int ONE = EARLY ? 1 : 0;
     if (p.w) {
-      if constexpr (!EARLY) load_affine(p.w, p.w_f32, s * p.ldw + c, w[0]);
+      load_affine(p.w, p.w_f32, s * p.ldw + c, a);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= w[ONE * v][e] + p.plus;
+      for (int e = 0; e < 8; ++e) y[e] *= a[e] + p.plus;
     }
     if (p.b) {
-      if constexpr (!EARLY) load_affine(p.b, p.w_f32, s * p.ldbias + c, b[0]);
+      load_affine(p.b, p.w_f32, s * p.ldbias + c, a);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] += b[ONE * v][e];
+      for (int e = 0; e < 8; ++e) y[e] += a[e];
     }
     store8<YF>(p.y, row * p.ldy + c, y);
   }
@@ -379,19 +367,22 @@ __global__ __launch_bounds__(64 * NW) void norm_join_kernel(NormBackward p) {
   }
 }
 
-// waves of a row and column groups of a lane: up to 32 values a lane (64 forward), the fewest waves for that
+// Waves of a row and column groups of a lane: the fewest waves with at most 32 values a lane, four from few rows on,
+// where a wave to a row leaves the chip empty. In us: 8192 x 1024 with 1 / 2 / 4 waves: 9.1, 9.2, 11; 8192 x 2048: 14.6,
+// 14.7, 15.1; 1024 x 2048: 5.7, 4.8, 4.3; 8192 x 4096 with 1 / 2 / 4 / 8: 36, 32, 29, 31; 8192 x 12288 with 4 / 8 / 16: 84,
+// 77, 90. Loading weight and bias along with the row instead of behind its sums cost registers: 8192 x 2560 22.7 us for 21.0.
 template <bool XF, bool YF>
 static hipError_t forward_xy(const NormForward& p, hipStream_t s) {
   const int chunks = (p.C + 7) / 8;
   const dim3 four((unsigned)((p.rows + 3) / 4)), one((unsigned)p.rows);
 #define CR_NF(W, V) hipLaunchKernelGGL((norm_forward_kernel<W, V, XF, YF>), W == 1 ? four : one, dim3(W == 1 ? 256 : W * 64), 0, s, p)
   if (chunks <= 64) CR_NF(1, 1);
-  else if (p.rows > 1024 && chunks <= 128) CR_NF(1, 2);
+  else if (chunks <= 128) CR_NF(1, 2);
   else if (p.rows > 1024 && chunks <= 256) CR_NF(1, 4);
   else if (chunks <= 256) CR_NF(4, 1);
   else if (chunks <= 512) CR_NF(4, 2);
   else if (chunks <= 1024) CR_NF(4, 4);
-  else CR_NF(4, 8);
+  else CR_NF(8, 4);
 #undef CR_NF
   return hipGetLastError();
 }
