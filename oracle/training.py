@@ -68,8 +68,9 @@ def norm_backward(dy, x, mean, rstd, w=None, rows=None, plus=0.0, S=1, base=None
     if base is not None:
         dx = dx + np.asarray(base, np.float64)
     dw, db = np.zeros((S, C)), np.zeros((S, C))
-    for s in range(S):
-        dw[s], db[s] = (dy * xh)[rows == s].sum(0), dy[rows == s].sum(0)
+    at = rows >= 0
+    np.add.at(dw, rows[at], (dy * xh)[at])
+    np.add.at(db, rows[at], dy[at])
     return dx, dw, db
 
 

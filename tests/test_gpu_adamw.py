@@ -85,7 +85,7 @@ def _codes(n):
 
 
 @pytest.mark.parametrize("grad", ["f32", "bf16"])
-@pytest.mark.parametrize("repeat", [1, 5])
+@pytest.mark.parametrize("repeat", [1, 5, 7])
 def test_moments_in_8_bits(cr, grad, repeat):
     sizes = SIZES * repeat
     say(f"adamw 8 {grad} {len(sizes)} tensors")

@@ -265,6 +265,56 @@ def test_modulation_columns(cr):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("C", [72, 640, 1200, 4104])
+@pytest.mark.parametrize("S,kind", [(300, "ragged"), (1500, "even"), (4096, "ragged"), (700, "descending")])
+def test_many_sequences(cr, C, S, kind):
+    """Hundreds and thousands of sequences: whole in a part, across parts, empty; offsets that descend here and there."""
+    M = 2100
+    say(f"norm {S} {kind} sequences of {C}")
+    g = np.random.default_rng([S, C])
+    off = np.arange(S + 1) * M // S if kind == "even" else np.sort(np.concatenate([[3, M - 5], g.integers(0, M + 1, S - 1)]))
+    if kind == "descending":
+        at = g.integers(1, S, 60)
+        off[at] = g.integers(-50, M, 60)
+    off = off.astype(np.int32)
+    rows = tr.sequences(off, M)
+    x, dy = _input(g, (M, C), torch.bfloat16, 1.5, 0.7), _input(g, (M, C), torch.bfloat16, 0.1)
+    w, b = (dev((g.standard_normal((S, C)) * 0.3).astype(np.float32)) for _ in range(2))
+    to = dev(off)
+    y = torch.full((M, C), -9.0, device=DEV)
+    mean, rstd = torch.zeros(M, device=DEV), torch.zeros(M, device=DEV)
+    cr.convrot_layer_norm_forward(x, w, b, seg_offsets=to, one_plus=True, out_type=cr.OUT.F32, out=y, mean=mean, rstd=rstd)
+    want, m64, r64 = tr.norm_forward(_f64(x), _f64(w), _f64(b), rows, 1.0)
+    wr = _f64(w)[rows] + 1
+    bound, _, _ = _forward_bound(_f64(x), wr, want, m64, r64, torch.float32, 1e-6)
+    at = rows >= 0
+    assert np.all((np.abs(_f64(y) - want) <= bound)[at]) and np.all(_f64(y)[~at] == -9)
+    start = torch.ones((S, C), device=DEV), torch.full((S, C), 2.0, device=DEV)
+    dx, dw, db = cr.convrot_layer_norm_backward(dy, x, mean, rstd, w, seg_offsets=to, one_plus=True, dx_type=cr.OUT.F32)
+    dxw, dww, dbw = tr.norm_backward(_f64(dy), _f64(x), _f64(mean), _f64(rstd), _f64(w), rows, 1.0, S)
+    assert np.all((np.abs(_f64(dx) - dxw) <= _backward_bound(_f64(dy), _f64(x), _f64(mean), _f64(rstd), wr, dxw, torch.float32))[at])
+    xh = np.abs((_f64(x) - _f64(mean)[:, None]) * _f64(rstd)[:, None])
+    mag_w, mag_b, most = np.zeros((S, C)), np.zeros((S, C)), np.zeros((S, 1))
+    np.add.at(mag_w, rows[at], (np.abs(_f64(dy)) * xh)[at])
+    np.add.at(mag_b, rows[at], np.abs(_f64(dy))[at])
+    np.add.at(most, rows[at], 1.0)
+    assert np.all(np.abs(_f64(dw) - dww) <= (most + 34) * U * mag_w) and np.all(np.abs(_f64(db) - dbw) <= (most + 34) * U * mag_b)
+    cr.convrot_layer_norm_backward(dy, x, mean, rstd, w, seg_offsets=to, one_plus=True, want_dx=False, d_weight=start[0], d_bias=start[1],
+                                   accumulate=True)
+    assert torch.equal(start[0], dw + 1) and torch.equal(start[1], db + 2)
+
+
+def test_one_row(cr):
+    """One part: the backward pass in one launch gives the sums itself."""
+    g = np.random.default_rng(14)
+    x, dy = _input(g, (1, 520), torch.float32), _input(g, (1, 520), torch.float32)
+    _, mean, rstd = cr.convrot_layer_norm_forward(x)
+    cr.reset_counters()
+    _, dw, db = cr.convrot_layer_norm_backward(dy, x, mean, rstd, dx_type=cr.OUT.F32)
+    assert cr.get_counters()["act"] == 1 and cr.get_counters()["fallbacks"] == 0
+    assert torch.equal(db, dy[0]) and torch.equal(dw, dy[0] * ((x[0] - mean) * rstd))
+
+
 def test_side_stream_and_graph(cr):
     """On a given stream, and captured: replays equal the eager results, other work between them."""
     g = np.random.default_rng(12)

@@ -97,6 +97,7 @@ struct NormBackward {
   int parts, part_rows;
   float* parts_w;           // [parts + S][C] each
   float* parts_b;
+  int* begins;              // [S] first row of each sequence, or null
 };
 size_t norm_backward_ws_bytes(int64_t rows, int64_t C, int S);
 hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int* kernels);

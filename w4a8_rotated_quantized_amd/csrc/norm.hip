@@ -11,6 +11,8 @@
 // A row is shared by W waves (1, 4, 8 or 16), each lane holding eight consecutive
 // columns at a time, V times. The memory rate bounds both directions, so a wave
 // keeps a whole row's loads in flight at once.
+#include <algorithm>
+
 #include "block.h"
 #include "common.h"
 
@@ -110,13 +112,46 @@ CR_DEV void row_sums(float& a, float& b, float2* lds, int wave, int slot) {
   }
 }
 
+CR_DEV int wave_max_int(int v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_xor(v, d);
+    v = v > o ? v : o;
+  }
+  return v;
+}
+
 // The sequence of a row among S offsets off[0..S], by one wave: the first s whose
-// end off[s + 1] lies behind the row, 64 at a time; S: none. An offset below an
-// earlier one so counts as that earlier one, and off[s + 1] > row for the s found.
-CR_DEV int sequence_of(const int32_t* off, int S, int64_t row, int l) {
-  for (int at = 0; at < S; at += 64) {
-    const uint64_t behind = __ballot(at + l < S && off[1 + min(at + l, S - 1)] > row);
-    if (behind) return at + __builtin_ctzll(behind);
+// end off[s + 1] lies behind the row, 256 offsets at a time; S: none. An offset
+// below an earlier one so counts as that earlier one, and off[s + 1] > row for the s
+// found. BEGIN: *begin is the sequence's first row, the largest of off[0..s] and 0.
+template <bool BEGIN>
+CR_DEV int sequence_of(const int32_t* off, int S, int64_t row, int l, int* begin = nullptr) {
+  int most = 0;                                        // of the ends before, this lane's
+  for (int at = 0; at < S; at += 256) {
+    int end[4], s = S;
+    uint64_t behind[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = at + k * 64 + l;
+      end[k] = i < S ? off[1 + i] : 0;
+      behind[k] = __ballot(i < S && end[k] > row);
+    }
+#pragma unroll
+    for (int k = 3; k >= 0; --k)
+      if (behind[k]) s = at + k * 64 + __builtin_ctzll(behind[k]);
+    if constexpr (BEGIN) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (at + k * 64 + l < s && end[k] > most) most = end[k];
+    }
+    if (s < S) {
+      if constexpr (BEGIN) {
+        most = wave_max_int(most);
+        *begin = most > off[0] ? most : off[0];
+      }
+      return s;
+    }
   }
   return S;
 }
@@ -130,7 +165,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
   if (row >= p.rows) return;
   int s = 0;
   if (p.off) {
-    s = sequence_of(p.off, p.S, row, l);
+    s = sequence_of<false>(p.off, p.S, row, l);
     if (s >= p.S || row < p.off[0]) return;           // in no sequence: left as it is
   }
   const int lane = W == 1 ? l : threadIdx.x;
@@ -183,12 +218,23 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
   }
 }
 
+CR_DEV void give(float* to, int64_t at, float (&v)[8], int accumulate) {
+  if (accumulate) {
+    float old[8];
+    load_affine(to, 1, at, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += old[e];
+  }
+  store8<true>(to, at, v);
+}
+
 // Backward. The rows are cut into p.parts stretches of p.part_rows, a block each. It
 // walks its rows with the sums for dw and db of its columns in registers, the
-// next row's loads under way, and writes the sums out where a sequence ends: part
-// q's share of sequence s goes to slot q + s of the workspace, which no other pair
-// has, as both only grow along the rows. The last launch adds a sequence's slots
-// in order.
+// next row's loads under way, and writes the sums out where a sequence ends. Those of a
+// sequence that lies in one part are the result. Else part q's share of sequence s goes
+// to slot q + s of the workspace, which no other pair has, as both only grow along the
+// rows, and the last launch adds the sequence's slots in order. For that launch, block 0
+// writes down where the sequences begin.
 // W == 1: four waves take the block's rows in turn, each with sums of its own,
 // added through LDS before they are written.
 template <int W, int V, bool XF, bool DF>
@@ -200,6 +246,30 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
   const int lane = W == 1 ? l : threadIdx.x;
   int64_t row = (int64_t)blockIdx.x * p.part_rows;
   const int64_t end = imin64(row + p.part_rows, p.rows);
+  if (p.begins && blockIdx.x == 0 && wave == 0) {
+    // the largest offset up to each, 256 at a time
+    int before = 0;
+    for (int at = 0; at < p.S; at += 256) {
+      int v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = at + l * 4 + k < p.S ? p.off[at + l * 4 + k] : 0;
+#pragma unroll
+      for (int k = 1; k < 4; ++k) v[k] = max(v[k], v[k - 1]);
+      int upto = v[3];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(upto, d);
+        if (l >= d) upto = max(upto, o);
+      }
+      const int ahead = __shfl_up(upto, 1);
+      before = l ? max(before, ahead) : before;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (at + l * 4 + k < p.S) p.begins[at + l * 4 + k] = max(v[k], before);
+      before = max(__shfl(before, 0), __shfl(upto, 63));
+    }
+  }
+  const int64_t part = row;
   if (p.off && row < p.off[0]) row = p.off[0];         // rows in no sequence: nothing is read or written
   Eight<XF> x[V];
   Eight<DF> dy[V];
@@ -218,9 +288,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
   };
   int slot = 0;
   while (row < end) {
-    const int s = p.off ? sequence_of(p.off, p.S, row, l) : 0;
+    int s = 0, begin = 0;
+    if (p.off) s = sequence_of<true>(p.off, p.S, row, l, &begin);
     if (s >= p.S) return;
-    const int64_t stop = p.off ? imin64(end, p.off[s + 1]) : end;
+    const int64_t last = p.off ? imin64(p.rows, p.off[s + 1]) : p.rows, stop = imin64(end, last);
+    const bool whole = begin >= part && last <= end;
     float w[V][8], dw[V][8], db[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -314,56 +386,61 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
               }
           }
         }
-        if (c < p.C && (W > 1 || wave == 0)) {
+        if (c >= p.C || (W == 1 && wave != 0)) continue;
+        if (!whole) {
           store8<true>(p.parts_w, at + c, dw[v]);
           store8<true>(p.parts_b, at + c, db[v]);
+          continue;
         }
+        const int64_t to = (int64_t)s * p.C + c;
+        if (p.dw) give(p.dw, to, dw[v], p.accumulate);
+        if (p.db) give(p.db, to, db[v], p.accumulate);
       }
     }
     row = stop;
   }
 }
 
-// dw and db of sequence blockIdx.y: the slots of the parts that hold its rows, in order.
-// A wave reads 64 columns of a slot, NW waves share the slots, each with several on their way.
-template <int NW>
+// dw and db of the sequences that have no single part: the slots of the parts that hold a sequence's rows, in
+// order, and zeros for those without rows. A wave reads 64 columns of a slot; SHARES waves share the slots, each
+// with several on their way, the block's other waves take other columns.
+template <int NW, int SHARES>
 __global__ __launch_bounds__(64 * NW) void norm_join_kernel(NormBackward p) {
   __shared__ float lds[NW][64];
-  const int s = blockIdx.y;
-  const int l = threadIdx.x & 63, share = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + l;
-  int64_t lo = 0, hi = p.rows;
-  if (p.off) {
-    // the sequence begins at the largest offset up to off[s]
-    __shared__ int begin;
-    if (threadIdx.x == 0) begin = 0;
-    __syncthreads();
-    int m = 0;
-    for (int i = threadIdx.x; i <= s; i += 64 * NW) m = max(m, p.off[i]);
-    if (m) atomicMax(&begin, m);
-    __syncthreads();
-    lo = begin;
-    hi = imin64(p.off[s + 1], p.rows);
-  }
+  const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, share = wave % SHARES;
+  const int64_t c = ((int64_t)blockIdx.x * (NW / SHARES) + wave / SHARES) * 64 + l;
   const float* from = blockIdx.z ? p.parts_b : p.parts_w;
   float* to = blockIdx.z ? p.db : p.dw;
   if (!to) return;
-  float sum = 0.f;
-  if (lo < hi && c < p.C) {
-    const int first = (int)(lo / p.part_rows), last = (int)((hi - 1) / p.part_rows);
-    const int n = last - first + 1, per = (n + NW - 1) / NW;
-    const int q1 = min(first + (share + 1) * per, last + 1);
-    const float* at = from + ((int64_t)(first + share * per) + s) * p.C + c;
+  for (int s = blockIdx.y; s < p.S; s += gridDim.y) {
+    const int64_t lo = p.off ? p.begins[s] : 0, hi = p.off ? imin64(p.off[s + 1], p.rows) : p.rows;
+    int first = 0, last = -1;
+    if (lo < hi) {
+      first = (int)(lo / p.part_rows);
+      last = (int)((hi - 1) / p.part_rows);
+      if (first == last) continue;                     // whole in one part, which gave the result
+    }
+    float sum = 0.f;
+    if (c < p.C) {
+      const int per = (last - first + SHARES) / SHARES;
+      const int q1 = min(first + (share + 1) * per, last + 1);
+      const float* at = from + ((int64_t)(first + share * per) + s) * p.C + c;
 #pragma unroll 8
-    for (int q = first + share * per; q < q1; ++q, at += p.C) sum += *at;
-  }
-  lds[share][l] = sum;
-  __syncthreads();
-  if (share == 0 && c < p.C) {
+      for (int q = first + share * per; q < q1; ++q, at += p.C) sum += *at;
+    }
+    if constexpr (SHARES > 1) {
+      lds[wave][l] = sum;
+      __syncthreads();
+      if (share == 0) {
 #pragma unroll
-    for (int o = 1; o < NW; ++o) sum += lds[o][l];
-    float* d = to + (int64_t)s * p.C + c;
-    *d = p.accumulate ? *d + sum : sum;
+        for (int o = 1; o < SHARES; ++o) sum += lds[wave + o][l];
+      }
+      __syncthreads();
+    }
+    if (share == 0 && c < p.C) {
+      float* d = to + (int64_t)s * p.C + c;
+      *d = p.accumulate ? *d + sum : sum;
+    }
   }
 }
 
@@ -407,7 +484,8 @@ int norm_parts(int64_t rows, int64_t C, int* part_rows) {
 size_t norm_backward_ws_bytes(int64_t rows, int64_t C, int S) {
   int per;
   const int parts = norm_parts(rows, C, &per);
-  return (size_t)2 * (size_t)(parts + S) * (size_t)C * sizeof(float);
+  // the slots of dw and of db, then where the sequences begin
+  return (size_t)2 * (size_t)(parts + S) * (size_t)C * sizeof(float) + ((size_t)S * sizeof(int) + 15) / 16 * 16;
 }
 
 template <bool XF, bool DF>
@@ -431,6 +509,7 @@ hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int*
   if (p.dw || p.db) {
     p.parts_w = reinterpret_cast<float*>(ws);
     p.parts_b = p.parts_w + (size_t)(p.parts + p.S) * p.C;
+    if (p.off) p.begins = reinterpret_cast<int*>(p.parts_b + (size_t)(p.parts + p.S) * p.C);
   }
   if (p.x_f32) {
     if (p.dy_f32) backward_xd<true, true>(p, s);
@@ -441,14 +520,18 @@ hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int*
   }
   *kernels = 1;
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !p.parts_w) return e;
-  // Waves that share a sequence's slots: 4 where it has few (800 rows of 3032 in 38 sequences, about 12 slots each: 34 us
-  // with 16 waves, 22 with 4, for both launches), else 8 once the blocks are more than one a compute unit (8192 x 4096
-  // in 5 sequences: the join alone 9.4 us with 16, 6.5 with 8), else 16 (1531 x 2560: 5.9 us)
-  const dim3 join((unsigned)((p.C + 63) / 64), (unsigned)p.S, 2);
-  if (p.parts / p.S < 32) hipLaunchKernelGGL((norm_join_kernel<4>), join, dim3(256), 0, s, p);
-  else if (join.x * join.y * 2 > 256) hipLaunchKernelGGL((norm_join_kernel<8>), join, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((norm_join_kernel<16>), join, dim3(1024), 0, s, p);
+  if (e != hipSuccess || !p.parts_w || (p.parts == 1 && !p.off)) return e;
+  // Waves that share a sequence's slots: 1 or 4 where it has few (800 rows of 3032 in 38 sequences, about 12 slots
+  // each: 34 us with 16 waves, 22 with 4, for both launches), else 8 once the blocks are more than one a compute unit
+  // (8192 x 4096 in 5 sequences: the join alone 9.4 us with 16, 6.5 with 8), else 16 (1531 x 2560: 5.9 us). Blocks walk
+  // the sequences beyond 2048 blocks' worth: most of many lie whole in a part and want nothing here.
+  const int slots = p.parts / p.S;
+  const unsigned cols = (unsigned)((p.C + 63) / 64), wide = (unsigned)((p.C + 255) / 256);
+  auto down = [&](unsigned across) { return (unsigned)std::max(1, std::min(p.S, (int)(1024 / across))); };
+  if (slots < 4) hipLaunchKernelGGL((norm_join_kernel<4, 1>), dim3(wide, down(wide), 2), dim3(256), 0, s, p);
+  else if (slots < 32) hipLaunchKernelGGL((norm_join_kernel<4, 4>), dim3(cols, (unsigned)p.S, 2), dim3(256), 0, s, p);
+  else if (cols * p.S * 2 > 256) hipLaunchKernelGGL((norm_join_kernel<8, 8>), dim3(cols, (unsigned)p.S, 2), dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((norm_join_kernel<16, 16>), dim3(cols, (unsigned)p.S, 2), dim3(1024), 0, s, p);
   *kernels = 2;
   return hipGetLastError();
 }
