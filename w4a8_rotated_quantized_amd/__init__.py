@@ -684,19 +684,16 @@ def convrot_act_backward(dy, codes, scales, act, dz=None, stream=None):
 # native module (csrc/binding.cpp): their small sizes are bound by the host. A call
 # that the library refuses comes back as its status.
 # ---------------------------------------------------------------------------
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _run(call, first, what, stream, args, held):
-    """call(*args, stream handle) on the GPU of `first` and the given stream
-    (default: that GPU's current one). held(result): the tensors of the call."""
+def _elsewhere(call, first, what, stream, args, *held):
+    """A call on a given stream, or on tensors of another GPU than the current one
+    (what a native call answers NotImplemented to). held: its tensors besides
+    those that come back."""
     index = _gpu(first, what)
-    if stream is None and index == _current_device():
-        return call(*args, _current_stream_handle(index))
     with _on(index, stream):
         result = call(*args, _current_stream_handle(index))
     if type(result) is not int or result == 0:
-        _hold(stream, *held(result))
+        back = result if type(result) is tuple else (result,) if type(result) is torch.Tensor else ()
+        _hold(stream, *held, *back)
     return result
 
 
@@ -712,7 +709,9 @@ def mxfp4_quantize(x, rot_group=0, codes=None, scales=None, stream=None):
     [ceil(K/128), rows, 64], scales uint8 [ceil(K/128), rows, 4]. rot_group: 0
     (none), 16, 64, 256 or 1024 columns rotated first. Weights and activations of
     one product take the same rot_group."""
-    r = _run(_native.mxfp4_quantize, x, "x", stream, (x, rot_group, codes, scales), lambda r: (x, *r))
+    r = _native.mxfp4_quantize(x, rot_group, codes, scales, None) if stream is None else NotImplemented
+    if r is NotImplemented:
+        r = _elsewhere(_native.mxfp4_quantize, x, "x", stream, (x, rot_group, codes, scales), x)
     if type(r) is int:
         _refused(r, "mxfp4_quantize", x=x, codes=codes, scales=scales)
     return r
@@ -721,8 +720,9 @@ def mxfp4_quantize(x, rot_group=0, codes=None, scales=None, stream=None):
 def mxfp4_dequantize(codes, scales, K, rot_group=0, out_type=OUT.BF16, out=None, stream=None):
     """The values that the codes of mxfp4_quantize stand for, [rows, K] in
     out_type, rotated back by rot_group (0: left in the basis of the codes)."""
-    r = _run(_native.mxfp4_dequantize, codes, "codes", stream, (codes, scales, K, rot_group, out_type, out),
-             lambda r: (codes, scales, r))
+    r = _native.mxfp4_dequantize(codes, scales, K, rot_group, out_type, out, None) if stream is None else NotImplemented
+    if r is NotImplemented:
+        r = _elsewhere(_native.mxfp4_dequantize, codes, "codes", stream, (codes, scales, K, rot_group, out_type, out), codes, scales)
     if type(r) is int:
         _refused(r, "mxfp4_dequantize", codes=codes, scales=scales, out=out)
     return r
@@ -733,8 +733,12 @@ def mxfp4_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, out_type=OUT.BF1
     w [N, K] (weights, N a multiple of 8), quantized with the same rot_group.
     bias: bf16 [N]. Returns [M, N] in out_type; rows of a given out may lie
     further apart. Not recorded by autograd."""
-    r = _run(_native.mxfp4_gemm, a_codes, "a_codes", stream, (a_codes, a_scales, w_codes, w_scales, bias, out_type, out),
-             lambda r: (a_codes, a_scales, w_codes, w_scales, bias, r))
+    r = NotImplemented
+    if stream is None:
+        r = _native.mxfp4_gemm(a_codes, a_scales, w_codes, w_scales, bias, out_type, out, None)
+    if r is NotImplemented:
+        r = _elsewhere(_native.mxfp4_gemm, a_codes, "a_codes", stream, (a_codes, a_scales, w_codes, w_scales, bias, out_type, out),
+                       a_codes, a_scales, w_codes, w_scales, bias)
     if type(r) is int:
         _refused(r, "mxfp4_gemm", a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out)
     return r
@@ -752,9 +756,12 @@ def convrot_layer_norm_forward(x, weight=None, bias=None, seg_offsets=None, eps=
     sequence (adaLN: one_plus=True with the scales as weight). Rows in no sequence are left as they are in the given outputs. Returns
     (y in out_type, mean, rstd): mean and rstd float32 [M] are what
     convrot_layer_norm_backward reads. Not recorded by autograd."""
-    r = _run(_native.layer_norm_forward, x, "x", stream,
-             (x, weight, bias, seg_offsets, eps, one_plus, out_type, out, mean, rstd),
-             lambda r: (x, weight, bias, seg_offsets, *r))
+    r = NotImplemented
+    if stream is None:
+        r = _native.layer_norm_forward(x, weight, bias, seg_offsets, eps, one_plus, out_type, out, mean, rstd, None)
+    if r is NotImplemented:
+        r = _elsewhere(_native.layer_norm_forward, x, "x", stream,
+                       (x, weight, bias, seg_offsets, eps, one_plus, out_type, out, mean, rstd), x, weight, bias, seg_offsets)
     if type(r) is int:
         _refused(r, "convrot_layer_norm_forward", x=x, weight=weight, bias=bias, seg_offsets=seg_offsets, out=out, mean=mean,
                  rstd=rstd)
@@ -773,10 +780,11 @@ def convrot_layer_norm_backward(dy, x, mean, rstd, weight=None, seg_offsets=None
     dx_type (None with want_dx=False), d_weight and d_bias float32 shaped like the
     weight, [C] or [S, C] (None with want_weights=False; accumulate=True adds to
     the given ones)."""
-    r = _run(_native.layer_norm_backward, dy, "dy", stream,
-             (dy, x, mean, rstd, weight, seg_offsets, one_plus, dx_base, dx_type, dx, d_weight, d_bias, want_dx, want_weights,
-              accumulate, workspace),
-             lambda r: (dy, x, mean, rstd, weight, seg_offsets, dx_base, *r))
+    args = (dy, x, mean, rstd, weight, seg_offsets, one_plus, dx_base, dx_type, dx, d_weight, d_bias, want_dx, want_weights,
+            accumulate, workspace)
+    r = _native.layer_norm_backward(*args, None) if stream is None else NotImplemented
+    if r is NotImplemented:
+        r = _elsewhere(_native.layer_norm_backward, dy, "dy", stream, args, dy, x, mean, rstd, weight, seg_offsets, dx_base)
     if type(r) is int:
         read = dict(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, seg_offsets=seg_offsets)
         if want_weights:
@@ -811,10 +819,12 @@ def convrot_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1=0.9
     once."""
     if not len(params):
         raise ValueError("params is empty")
-    r = _run(_native.adamw_step, params[0], "params", stream,
-             (params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales, grad_scale, step, lr, beta1, beta2,
-              eps, weight_decay, seed & 0xFFFFFFFF),
-             lambda r: (*_listed(params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales), grad_scale))
+    args = (params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales, grad_scale, step, lr, beta1, beta2,
+            eps, weight_decay, seed & 0xFFFFFFFF)
+    r = _native.adamw_step(*args, None) if stream is None else NotImplemented
+    if r is NotImplemented:
+        r = _elsewhere(_native.adamw_step, params[0], "params", stream, args, grad_scale,
+                       *_listed(params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales))
     if r:
         _refused_lists(r, "convrot_adamw_step", params=params, grads=grads, exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs, copies=copies)
 
@@ -825,9 +835,11 @@ def convrot_adamw_moments(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scal
     with float32 moments): (m, v), one tensor after another in two flat tensors."""
     if not len(exp_avgs):
         raise ValueError("exp_avgs is empty")
-    r = _run(_native.adamw_moments, exp_avgs[0], "exp_avgs", stream,
-             (exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, exp_avg_out, exp_avg_sq_out),
-             lambda r: (*_listed(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales), *r))
+    args = (exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, exp_avg_out, exp_avg_sq_out)
+    r = _native.adamw_moments(*args, None) if stream is None else NotImplemented
+    if r is NotImplemented:
+        r = _elsewhere(_native.adamw_moments, exp_avgs[0], "exp_avgs", stream, args,
+                       *_listed(exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales))
     if type(r) is int:
         _refused_lists(r, "convrot_adamw_moments", exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs)
     return r

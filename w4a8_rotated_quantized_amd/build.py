@@ -65,7 +65,7 @@ def _link_binding(obj: str) -> None:
     dirs = library_paths()
     tmp = NATIVE + ".tmp"
     cmd = ["g++", "-shared", "-fPIC", obj, "-o", tmp, f"-L{HERE}", "-l:libconvrot.so", "-Wl,-rpath,$ORIGIN",
-           *[f"-L{d}" for d in dirs], "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           *[f"-L{d}" for d in dirs], "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

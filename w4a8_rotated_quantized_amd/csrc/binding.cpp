@@ -2,7 +2,9 @@
 // optimizer step: checks of tensor arguments, allocation of outputs, and the call
 // into the C ABI. The Python functions in __init__.py wrap these with their
 // signatures; here arguments are positional. A call that the library refuses returns its
-// status as an int; wrong tensors raise ValueError.
+// status as an int; wrong tensors raise ValueError. The last argument is the stream's
+// handle, or None for the current stream of the tensors' GPU; NotImplemented comes back
+// where that GPU is not the current one.
 //
 // Why native: the small sizes of these operators are bound by the host. Checking and
 // allocating in Python through ctypes took 12.4 us for a layer norm of 77 rows,
@@ -13,6 +15,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
 
 #include <cstdio>
 #include <vector>
@@ -111,10 +115,21 @@ int small(PyObject* o) {
   const int64_t v = whole(o);
   return v < -1 || v > (1 << 20) ? -1 : (int)v;
 }
-hipStream_t stream_of(PyObject* o) {
+// the stream that a call runs on; false: the current GPU is another one
+bool stream_for(PyObject* o, int index, hipStream_t* s) {
+  if (o == Py_None) {
+    if (c10::hip::current_device() != index) return false;
+    *s = c10::hip::getCurrentHIPStream((c10::DeviceIndex)index).stream();
+    return true;
+  }
   void* p = PyLong_AsVoidPtr(o);
   if (!p && PyErr_Occurred()) throw python_error();
-  return static_cast<hipStream_t>(p);
+  *s = static_cast<hipStream_t>(p);
+  return true;
+}
+PyObject* elsewhere() {
+  Py_INCREF(Py_NotImplemented);
+  return Py_NotImplemented;
 }
 
 ScalarType out_dtype(int out_type) {
@@ -170,6 +185,8 @@ PyObject* mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
     const Tensor& x = tensor(a[0], "x");
     const int index = gpu_of(x, "x");
+    hipStream_t stream;
+    if (!stream_for(a[4], index, &stream)) return elsewhere();
     if (x.dim() != 2) wrong("x is [rows, K]");
     const int64_t rows = x.size(0), K = x.size(1), tiles = (K + 127) / 128;
     int64_t ldx;
@@ -179,7 +196,7 @@ PyObject* mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     dense_or_null(gs, "scales", ScalarType::Byte, index, {tiles, rows, 4});
     const Tensor codes = gc ? *gc : empty({tiles, rows, 64}, ScalarType::Byte, x);
     const Tensor scales = gs ? *gs : empty({tiles, rows, 4}, ScalarType::Byte, x);
-    const cr_status st = mxfp4_quantize(px, ldx, rows, K, small(a[1]), codes.data_ptr(), scales.data_ptr(), stream_of(a[4]));
+    const cr_status st = mxfp4_quantize(px, ldx, rows, K, small(a[1]), codes.data_ptr(), scales.data_ptr(), stream);
     return st ? refused(st) : pack({&codes, &scales});
   });
 }
@@ -206,6 +223,8 @@ PyObject* mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 7, [&]() -> PyObject* {
     const Tensor& codes = tensor(a[0], "codes");
     const int index = gpu_of(codes, "codes");
+    hipStream_t stream;
+    if (!stream_for(a[6], index, &stream)) return elsewhere();
     const MxPair p = mx_pair(codes, tensor(a[1], "scales"), "the", index);
     const int64_t K = whole(a[2]);
     if (K < 0 || K > p.tiles * 128 || p.tiles != (K + 127) / 128) wrong("K does not fit the codes' tiles");
@@ -215,7 +234,7 @@ PyObject* mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int64_t ldo = K;
     if (go) spaced(*go, "out", dt, index, p.rows, K, &ldo);
     const Tensor out = go ? *go : empty({p.rows, K}, dt, codes);
-    const cr_status st = mxfp4_dequantize(p.codes, p.scales, p.rows, K, small(a[3]), out.data_ptr(), (cr_out)type, ldo, stream_of(a[6]));
+    const cr_status st = mxfp4_dequantize(p.codes, p.scales, p.rows, K, small(a[3]), out.data_ptr(), (cr_out)type, ldo, stream);
     return st ? refused(st) : THPVariable_Wrap(out);
   });
 }
@@ -225,6 +244,8 @@ PyObject* mx_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> PyObject* {
     const Tensor& ac = tensor(a[0], "a_codes");
     const int index = gpu_of(ac, "a_codes");
+    hipStream_t stream;
+    if (!stream_for(a[7], index, &stream)) return elsewhere();
     const MxPair p = mx_pair(ac, tensor(a[1], "a_scales"), "a", index);
     const MxPair w = mx_pair(tensor(a[2], "w_codes"), tensor(a[3], "w_scales"), "w", index);
     if (p.tiles != w.tiles) wrong("a and w have different K");
@@ -236,7 +257,7 @@ PyObject* mx_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (go) spaced(*go, "out", dt, index, p.rows, w.rows, &ldc);
     const Tensor out = go ? *go : empty({p.rows, w.rows}, dt, ac);
     const cr_status st = mxfp4_gemm(p.codes, p.scales, w.codes, w.scales, pb, out.data_ptr(), (cr_out)type, ldc, p.rows, w.rows,
-                                    p.tiles * 128, stream_of(a[7]));
+                                    p.tiles * 128, stream);
     return st ? refused(st) : THPVariable_Wrap(out);
   });
 }
@@ -280,6 +301,8 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject* {
     const Tensor& x = tensor(a[0], "x");
     const int index = gpu_of(x, "x");
+    hipStream_t stream;
+    if (!stream_for(a[10], index, &stream)) return elsewhere();
     if (x.dim() != 2) wrong("x is [M, C]");
     const int64_t M = x.size(0), C = x.size(1);
     const cr_out x_type = float_type(x, "x");
@@ -298,7 +321,7 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor mean = gm ? *gm : empty({M}, ScalarType::Float, x), rstd = gr ? *gr : empty({M}, ScalarType::Float, x);
     const cr_status st = convrot_layer_norm_forward(px, x_type, ldx, f.w, f.ldw, f.b, f.ldb, f.type, plus, f.off, count_of(f.S), eps,
                                                     out.data_ptr(), (cr_out)type, ldy, static_cast<float*>(mean.data_ptr()),
-                                                    static_cast<float*>(rstd.data_ptr()), M, C, stream_of(a[10]));
+                                                    static_cast<float*>(rstd.data_ptr()), M, C, stream);
     return st ? refused(st) : pack({&out, &mean, &rstd});
   });
 }
@@ -309,6 +332,8 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 17, [&]() -> PyObject* {
     const Tensor& dy = tensor(a[0], "dy");
     const int index = gpu_of(dy, "dy");
+    hipStream_t stream;
+    if (!stream_for(a[16], index, &stream)) return elsewhere();
     if (dy.dim() != 2) wrong("dy is [M, C]");
     const int64_t M = dy.size(0), C = dy.size(1);
     const bool want_dx = truth(a[12]), want_w = truth(a[13]), accumulate = truth(a[14]);
@@ -348,7 +373,7 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         pdy, dy_type, lddy, px, x_type, ldx, pm, pr, f.w, f.ldw, f.type, truth(a[6]), f.off, count_of(f.S), pb, ldb,
         want_dx ? dx.data_ptr() : nullptr, (cr_out)type, lddx, want_w ? static_cast<float*>(dw.data_ptr()) : nullptr,
         want_w ? static_cast<float*>(db.data_ptr()) : nullptr, accumulate, M, C, want_w ? ws.data_ptr() : nullptr,
-        want_w ? ws.nbytes() : 0, stream_of(a[16]));
+        want_w ? ws.nbytes() : 0, stream);
     return st ? refused(st) : pack({want_dx ? &dx : nullptr, want_w ? &dw : nullptr, want_w ? &db : nullptr, want_w ? &ws : nullptr});
   });
 }
@@ -409,6 +434,8 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         ms(a[5], "exp_avg_scales"), vs(a[6], "exp_avg_sq_scales");
     if (p.n < 1) wrong("params is empty");
     const int index = gpu_of(p[0], "params");
+    hipStream_t stream;
+    if (!stream_for(a[15], index, &stream)) return elsewhere();
     for (const Tensors* l : {&g, &c})
       if ((l == &g || *l) && l->n != p.n) wrong("%s must hold one tensor for each of params, of its size", l->what);
     const cr_out grad_type = float_type(g[0], "grads");
@@ -426,7 +453,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float* scale =
         static_cast<const float*>(dense_or_null(tensor_or_none(a[7], "grad_scale"), "grad_scale", ScalarType::Float, index, {1}));
     return refused(convrot_adamw_step(e.data(), entries(e), grad_type, ms ? 8 : 32, real(a[9]), real(a[10]), real(a[11]), real(a[12]),
-                                      real(a[13]), whole(a[8]), scale, (uint32_t)whole(a[14]), stream_of(a[15])));
+                                      real(a[13]), whole(a[8]), scale, (uint32_t)whole(a[14]), stream));
   });
 }
 
@@ -437,6 +464,8 @@ PyObject* adamw_moments(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (m.n < 1) wrong("exp_avgs is empty");
     if (!ms || !vs) wrong("8-bit moments have exp_avg_scales and exp_avg_sq_scales");
     const int index = gpu_of(m[0], "exp_avgs");
+    hipStream_t stream;
+    if (!stream_for(a[6], index, &stream)) return elsewhere();
     std::vector<cr_adamw_tensor> e((size_t)m.n);
     int64_t total = 0;
     for (Py_ssize_t i = 0; i < m.n; ++i) {
@@ -449,7 +478,7 @@ PyObject* adamw_moments(PyObject*, PyObject* const* a, Py_ssize_t n) {
     dense_or_null(gv, "exp_avg_sq_out", ScalarType::Float, index, {total});
     const Tensor om = gm ? *gm : empty({total}, ScalarType::Float, m[0]), ov = gv ? *gv : empty({total}, ScalarType::Float, m[0]);
     const cr_status st = convrot_adamw_moments(e.data(), entries(e), static_cast<float*>(om.data_ptr()),
-                                               static_cast<float*>(ov.data_ptr()), stream_of(a[6]));
+                                               static_cast<float*>(ov.data_ptr()), stream);
     return st ? refused(st) : pack({&om, &ov});
   });
 }
