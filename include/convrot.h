@@ -797,7 +797,7 @@ cr_status convrot_layer_norm_backward(const void* dy, cr_out dy_type, int64_t ld
  *                in exp_avg_out and exp_avg_sq_out [sum of n] (param, grad and copy of the
  *                entries are not read).
  * 1 <= count <= 65536, step >= 1, lr, eps and weight_decay >= 0, 0 <= beta < 1. One launch for
- * up to 63 entries (84 of convrot_adamw_moments), in the list's order; entries of a list
+ * up to 63 entries (84 of convrot_adamw_moments) of 2^31 elements together, in the list's order; entries of a list
  * may hold the same tensor only once.
  */
 typedef struct cr_adamw_tensor {

@@ -227,3 +227,62 @@ def test_memory_freed_under_a_call(cr):
         side.synchronize()
         assert torch.equal(out, want)
         del junk
+
+
+def _spread(rows):
+    return torch.cat([torch.arange(0, 70), torch.arange(rows // 2 - 35, rows // 2 + 35), torch.arange(rows - 70, rows)]).to(DEV)
+
+
+def test_more_blocks_than_a_grid_row(cr):
+    """Beyond 2^20 blocks the grid goes on along its second axis: rows at its ends and in
+    the middle are those of a call on them alone, and nothing behind the last is written."""
+    rows = (1 << 26) - 1
+    g = torch.Generator(device=DEV).manual_seed(11)
+    x = torch.randn(rows, 8, generator=g, device=DEV, dtype=torch.bfloat16)
+    at = _spread(rows)
+    out = torch.full((rows + 3, 8), 7.0, device=DEV, dtype=torch.bfloat16)
+    mean, rstd = torch.full((rows + 3,), 7.0, device=DEV), torch.full((rows + 3,), 7.0, device=DEV)
+    cr.convrot_layer_norm_forward(x, out=out[:rows], mean=mean[:rows], rstd=rstd[:rows])
+    y, m, r = cr.convrot_layer_norm_forward(x[at])
+    assert torch.equal(out[at], y) and torch.equal(mean[at], m) and torch.equal(rstd[at], r)
+    assert bool((out[rows:] == 7).all()) and bool((mean[rows:] == 7).all()) and bool((rstd[rows:] == 7).all())
+    del x, out, mean, rstd
+    rows = (1 << 21) + 3                                # a row a block
+    x = torch.randn(rows, 1032, generator=g, device=DEV, dtype=torch.bfloat16)
+    at = _spread(rows)
+    y, m, r = cr.convrot_layer_norm_forward(x)
+    small = cr.convrot_layer_norm_forward(x[torch.cat([at] * 6)])   # more than 1024 rows: the same shape of block
+    assert torch.equal(y[at], small[0][:at.numel()]) and torch.equal(r[at], small[2][:at.numel()])
+    del x, y
+    rows = (1 << 24) + 5
+    x = torch.randn(rows, 64, generator=g, device=DEV, dtype=torch.bfloat16)
+    at = _spread(rows)
+    for rot in (0, 64):
+        codes, scales = cr.mxfp4_quantize(x, rot)
+        some = cr.mxfp4_quantize(x[at], rot)
+        assert torch.equal(codes[:, at], some[0]) and torch.equal(scales[:, at], some[1])
+        back = cr.mxfp4_dequantize(codes, scales, 64, rot)
+        assert torch.equal(back[at], cr.mxfp4_dequantize(*some, 64, rot))
+
+
+def test_adamw_longest_tensor(cr):
+    """A tensor of nearly 2^31 elements fills a launch: the next one takes another."""
+    sizes = [(1 << 31) - 8, 5001, 1 << 20]
+    some = [torch.cat([torch.arange(0, 9), torch.arange(n // 2 - 4, n // 2 + 5), torch.arange(n - 9, n)]).to(DEV) for n in sizes]
+    g = torch.Generator(device=DEV).manual_seed(12)
+    lists = []
+    for kind in range(4):                               # parameters, gradients, both moments: zeros but for some
+        lists.append([])
+        for n, at in zip(sizes, some):
+            t = torch.zeros(n, device=DEV, dtype=torch.bfloat16 if kind == 1 else torch.float32)
+            t[at] = torch.rand(at.numel(), generator=g, device=DEV).to(t.dtype)
+            lists[-1].append(t)
+    few = [[t[at].clone() for t, at in zip(l, some)] for l in lists]
+    kw = dict(step=3, lr=0.01, weight_decay=0.1)
+    cr.convrot_adamw_step(*lists, **kw)
+    cr.convrot_adamw_step(*few, **kw)
+    for l, f in zip(lists, few):
+        for t, at, want in zip(l, some, f):
+            assert torch.equal(t[at], want)
+            t[at] = 0
+            assert t.count_nonzero() == 0

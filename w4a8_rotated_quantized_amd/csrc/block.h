@@ -102,10 +102,18 @@ struct NormBackward {
 size_t norm_backward_ws_bytes(int64_t rows, int64_t C, int S);
 hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int* kernels);
 
+// A launch takes fewer than 2^32 threads along x: blocks beyond 2^20 go on along y.
+constexpr int GRID_LG = 20;
+inline dim3 long_grid(int64_t blocks) {
+  const int64_t most = (int64_t)1 << GRID_LG;
+  return blocks <= most ? dim3((unsigned)blocks) : dim3((unsigned)most, (unsigned)((blocks + most - 1) / most));
+}
+
 // Tensors of one launch of the optimizer step: their table rides in the kernel's arguments,
 // which take 4096 bytes.
 constexpr int ADAMW_TENSORS = 63, ADAMW_MOMENTS = 84;
 constexpr int ADAMW_CHUNK = 1024;    // elements a block takes
+constexpr int ADAMW_CHUNKS = 1 << 21;   // blocks of one launch: those of the longest tensor
 constexpr int ADAMW_BLOCK = 256;     // elements that share the scale of an 8-bit moment
 
 struct AdamwEntry {

@@ -74,7 +74,7 @@ hipError_t adamw_tables(const cr_adamw_tensor* t, int count, int* kernels, F fil
     // every entry takes a place, empty ones no chunk, so that their numbers count them
     while (i < count && table.count < per) {
       const int64_t c = (t[i].n + cr::ADAMW_CHUNK - 1) / cr::ADAMW_CHUNK;
-      if (table.count && chunks + c >= LD_MAX) break;
+      if (table.count && chunks + c > cr::ADAMW_CHUNKS) break;
       auto& e = table.t[table.count++];
       fill(e, t[i], elements);
       e.n = (int)t[i].n;

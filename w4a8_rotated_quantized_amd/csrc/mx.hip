@@ -67,9 +67,9 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxQuantize p, int lg_r
   constexpr int NC = MxRot<NR>::chunks;
   const int seg = threadIdx.x >> 4;
   const LaneRot lr = lane_rot<MxRot<NR>::lanes>(threadIdx.x & 15);
-  const uint32_t down = blockIdx.x / (uint32_t)across;
+  const uint32_t block = (blockIdx.y << GRID_LG) + blockIdx.x, down = block / (uint32_t)across;
   const int64_t row = ((int64_t)down << lg_rpb) + (seg & ((1 << lg_rpb) - 1));
-  const int group = (int)(blockIdx.x - down * across) * (16 >> lg_rpb) + (seg >> lg_rpb);
+  const int group = (int)(block - down * across) * (16 >> lg_rpb) + (seg >> lg_rpb);
   if (row >= p.rows || group >= groups) return;        // whole segments: DPP stays inside them
   const int tiles = (int)((p.K + MX_TILE - 1) / MX_TILE);
 
@@ -155,9 +155,9 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantize p, int 
   __shared__ __attribute__((aligned(16))) float lds[F32 ? 16 : 1][F32 ? 256 : 1];
   const int seg = threadIdx.x >> 4;
   const LaneRot lr = lane_rot<MxRot<NR>::lanes>(threadIdx.x & 15);
-  const uint32_t down = blockIdx.x / (uint32_t)across;
+  const uint32_t block = (blockIdx.y << GRID_LG) + blockIdx.x, down = block / (uint32_t)across;
   const int64_t row = ((int64_t)down << lg_rpb) + (seg & ((1 << lg_rpb) - 1));
-  const int group = (int)(blockIdx.x - down * across) * (16 >> lg_rpb) + (seg >> lg_rpb);
+  const int group = (int)(block - down * across) * (16 >> lg_rpb) + (seg >> lg_rpb);
   if (row >= p.rows || group >= groups) return;
   float v[NC][16];
 #pragma unroll
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantize p, int 
 
 struct MxGrid {
   int lg_rpb, groups, across;
-  unsigned blocks;
+  dim3 blocks;
 };
 // 16 rows a block, fewer where there are fewer; blocks along the columns first
 static MxGrid mx_grid(int64_t rows, int64_t K, int chunks) {
@@ -237,22 +237,22 @@ static MxGrid mx_grid(int64_t rows, int64_t K, int chunks) {
   const int per = 16 >> g.lg_rpb;
   g.across = (g.groups + per - 1) / per;
   const int64_t rpb = (int64_t)1 << g.lg_rpb;
-  g.blocks = (unsigned)(g.across * ((rows + rpb - 1) / rpb));
+  g.blocks = long_grid(g.across * ((rows + rpb - 1) / rpb));
   return g;
 }
 
 template <int NR>
 static hipError_t quantize_nr(const MxQuantize& p, hipStream_t s) {
   const MxGrid g = mx_grid(p.rows, p.K, MxRot<NR>::chunks);
-  hipLaunchKernelGGL((mx_quantize_kernel<NR>), dim3(g.blocks), dim3(256), 0, s, p, g.lg_rpb, g.groups, g.across);
+  hipLaunchKernelGGL((mx_quantize_kernel<NR>), g.blocks, dim3(256), 0, s, p, g.lg_rpb, g.groups, g.across);
   return hipGetLastError();
 }
 
 template <int NR>
 static hipError_t dequantize_nr(const MxDequantize& p, hipStream_t s) {
   const MxGrid g = mx_grid(p.rows, p.K, MxRot<NR>::chunks);
-  if (p.out_f32) hipLaunchKernelGGL((mx_dequantize_kernel<NR, true>), dim3(g.blocks), dim3(256), 0, s, p, g.lg_rpb, g.groups, g.across);
-  else hipLaunchKernelGGL((mx_dequantize_kernel<NR, false>), dim3(g.blocks), dim3(256), 0, s, p, g.lg_rpb, g.groups, g.across);
+  if (p.out_f32) hipLaunchKernelGGL((mx_dequantize_kernel<NR, true>), g.blocks, dim3(256), 0, s, p, g.lg_rpb, g.groups, g.across);
+  else hipLaunchKernelGGL((mx_dequantize_kernel<NR, false>), g.blocks, dim3(256), 0, s, p, g.lg_rpb, g.groups, g.across);
   return hipGetLastError();
 }
 

@@ -161,7 +161,7 @@ template <int W, int V, bool XF, bool YF>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(NormForward p) {
   __shared__ float lds[2 * W];
   const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  const int64_t block = ((int64_t)blockIdx.y << GRID_LG) + blockIdx.x, row = W == 1 ? block * 4 + wave : block;
   if (row >= p.rows) return;
   int s = 0;
   if (p.off) {
@@ -451,7 +451,7 @@ __global__ __launch_bounds__(64 * NW) void norm_join_kernel(NormBackward p) {
 template <bool XF, bool YF>
 static hipError_t forward_xy(const NormForward& p, hipStream_t s) {
   const int chunks = (p.C + 7) / 8;
-  const dim3 four((unsigned)((p.rows + 3) / 4)), one((unsigned)p.rows);
+  const dim3 four = long_grid((p.rows + 3) / 4), one = long_grid(p.rows);
 #define CR_NF(W, V) hipLaunchKernelGGL((norm_forward_kernel<W, V, XF, YF>), W == 1 ? four : one, dim3(W == 1 ? 256 : W * 64), 0, s, p)
   if (chunks <= 64) CR_NF(1, 1);
   else if (chunks <= 128) CR_NF(1, 2);
