@@ -8,7 +8,7 @@
 // Both sums of a row run over the values held in registers: x is read once,
 // and the variance is that of the differences, which x^2 - mean^2 would lose.
 //
-// A row is shared by W waves (1, 4, 8 or 16), each lane holding eight consecutive
+// A row is shared by W waves (1 to 16), each lane holding eight consecutive
 // columns at a time, V times. The memory rate bounds both directions, so a wave
 // keeps a whole row's loads in flight at once.
 #include <algorithm>
@@ -121,14 +121,14 @@ CR_DEV int wave_max_int(int v) {
   return v;
 }
 
-// The sequence of a row among S offsets off[0..S], by one wave: the first s whose
-// end off[s + 1] lies behind the row, 256 offsets at a time; S: none. An offset
+// The sequence of a row among S offsets off[0..S], by one wave: the first s, `from`
+// on, whose end off[s + 1] lies behind the row, 256 offsets at a time; S: none. An offset
 // below an earlier one so counts as that earlier one, and off[s + 1] > row for the s
-// found. BEGIN: *begin is the sequence's first row, the largest of off[0..s] and 0.
+// found. BEGIN, from the first sequence on: *begin is the sequence's first row, the largest of off[0..s] and 0.
 template <bool BEGIN>
-CR_DEV int sequence_of(const int32_t* off, int S, int64_t row, int l, int* begin = nullptr) {
+CR_DEV int sequence_of(const int32_t* off, int S, int64_t row, int l, int from = 0, int64_t* begin = nullptr) {
   int most = 0;                                        // of the ends before, this lane's
-  for (int at = 0; at < S; at += 256) {
+  for (int at = from; at < S; at += 256) {
     int end[4], s = S;
     uint64_t behind[4];
 #pragma unroll
@@ -235,15 +235,14 @@ CR_DEV void give(float* to, int64_t at, float (&v)[8], int accumulate) {
 // to slot q + s of the workspace, which no other pair has, as both only grow along the
 // rows, and the last launch adds the sequence's slots in order. For that launch, block 0
 // writes down where the sequences begin.
-// W == 1: four waves take the block's rows in turn, each with sums of its own,
-// added through LDS before they are written.
-template <int W, int V, bool XF, bool DF>
-__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(NormBackward p) {
-  constexpr int RPB = W == 1 ? 4 : 1;
-  __shared__ float2 lds[2 * W];
-  __shared__ float4 join[W == 1 ? 3 * 64 * 4 : 1];
-  const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int lane = W == 1 ? l : threadIdx.x;
+// G groups of W waves take the block's rows in turn, each with sums of its own, added
+// through LDS before they are written: rows on their way at once, without a slot for each.
+template <int W, int V, int G, bool XF, bool DF>
+__global__ __launch_bounds__(G * W * 64) void norm_backward_kernel(NormBackward p) {
+  __shared__ float2 lds[G][2 * W];
+  __shared__ float4 join[G > 1 ? (G - 1) * W * 64 * 4 : 1];
+  const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, group = wave / W;
+  const int lane = threadIdx.x - group * W * 64;
   int64_t row = (int64_t)blockIdx.x * p.part_rows;
   const int64_t end = imin64(row + p.part_rows, p.rows);
   if (p.begins && blockIdx.x == 0 && wave == 0) {
@@ -286,11 +285,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
     mean = p.mean[r];
     rstd = p.rstd[r];
   };
-  int slot = 0;
-  while (row < end) {
-    int s = 0, begin = 0;
-    if (p.off) s = sequence_of<true>(p.off, p.S, row, l, &begin);
-    if (s >= p.S) return;
+  int slot = 0, s = 0;
+  int64_t begin = 0;
+  if (p.off && row < end) s = sequence_of<true>(p.off, p.S, row, l, 0, &begin);
+  while (row < end && s < p.S) {
     const int64_t last = p.off ? imin64(p.rows, p.off[s + 1]) : p.rows, stop = imin64(end, last);
     const bool whole = begin >= part && last <= end;
     float w[V][8], dw[V][8], db[V][8];
@@ -308,23 +306,25 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
         for (int e = 0; e < 8; ++e) w[v][e] += p.plus;
       }
     }
-    int64_t r = row + (W == 1 ? wave : 0);
+    int64_t r = row + group;
     if (r < stop) load(r);
-    for (; r < stop; r += RPB) {
+    // the groups meet at the block's barriers: each takes the same number of rounds
+    for (int64_t round = row; round < stop; round += G, r += G) {
+      const bool some = G == 1 || r < stop;
       // this row's values in float32, then the next row's loads
       const float rs = rstd;
       float a = 0.f, b = 0.f;
       float xh[V][8], d[V][8];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const bool in = (v * W * 64 + lane) * 8 < p.C;
+        const bool in = some && (v * W * 64 + lane) * 8 < p.C;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           d[v][e] = in ? dy[v].get(e) : 0.f;
           xh[v][e] = in ? (x[v].get(e) - mean) * rs : 0.f;
         }
       }
-      if (r + RPB < stop) load(r + RPB);
+      if (r + G < stop) load(r + G);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -336,14 +336,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
           db[v][e] += d[v][e];
         }
       if (!p.dx) continue;
-      row_sums<W>(a, b, lds, wave, slot);
+      row_sums<W>(a, b, lds[group], wave - group * W, slot);
       slot ^= 1;
       a *= p.inv_c;
       b *= p.inv_c;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (v * W * 64 + lane) * 8;
-        if (c >= p.C) continue;
+        if (c >= p.C || !some) continue;
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = rs * (d[v][e] * w[v][e] - a - xh[v][e] * b);
@@ -362,22 +362,22 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (v * W * 64 + lane) * 8;
-        if constexpr (W == 1) {
+        if constexpr (G > 1) {
           __syncthreads();
-          if (wave) {
-            float4* to = join + (wave - 1) * 64 * 4;
-            to[l] = float4{dw[v][0], dw[v][1], dw[v][2], dw[v][3]};
-            to[64 + l] = float4{dw[v][4], dw[v][5], dw[v][6], dw[v][7]};
-            to[128 + l] = float4{db[v][0], db[v][1], db[v][2], db[v][3]};
-            to[192 + l] = float4{db[v][4], db[v][5], db[v][6], db[v][7]};
+          if (group) {
+            float4* to = join + (group - 1) * (W * 64 * 4) + lane;
+            to[0] = float4{dw[v][0], dw[v][1], dw[v][2], dw[v][3]};
+            to[W * 64] = float4{dw[v][4], dw[v][5], dw[v][6], dw[v][7]};
+            to[2 * W * 64] = float4{db[v][0], db[v][1], db[v][2], db[v][3]};
+            to[3 * W * 64] = float4{db[v][4], db[v][5], db[v][6], db[v][7]};
           }
           __syncthreads();
-          if (wave == 0) {
+          if (group == 0) {
 #pragma unroll
-            for (int o = 0; o < 3; ++o)
+            for (int o = 0; o < G - 1; ++o)
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const float4 t = join[o * 256 + q * 64 + l];
+                const float4 t = join[(o * 4 + q) * (W * 64) + lane];
                 float* to = (q < 2 ? dw[v] : db[v]) + (q & 1) * 4;
                 to[0] += t.x;
                 to[1] += t.y;
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
               }
           }
         }
-        if (c >= p.C || (W == 1 && wave != 0)) continue;
+        if (c >= p.C || group) continue;
         if (!whole) {
           store8<true>(p.parts_w, at + c, dw[v]);
           store8<true>(p.parts_b, at + c, db[v]);
@@ -397,7 +397,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_backward_kernel(No
         if (p.db) give(p.db, to, db[v], p.accumulate);
       }
     }
-    row = stop;
+    // one that begins in this part begins at the row behind the last: no offset between is behind that row
+    row = begin = stop;
+    if (row < end) s = sequence_of<false>(p.off, p.S, row, l, s + 1);
   }
 }
 
@@ -469,12 +471,11 @@ hipError_t launch_norm_forward(const NormForward& p, hipStream_t s) {
   return p.y_f32 ? forward_xy<false, true>(p, s) : forward_xy<false, false>(p, s);
 }
 
-// Parts of the backward pass: as many blocks as the chip holds at once (two, three, two and one a compute unit by
-// their waves), whole rounds of a block's waves. More parts hide more of a row's latency and make more slots to
-// join. Both launches, 256, 512, 768, 1024 parts, in us: 8192 x 1024: 23, 19, 25, 24; 8192 x 4096: 101, 76, 73, 87;
-// 8192 x 12288: 209, 229, 246, 258.
+// Parts of the backward pass: a block a compute unit, two of narrow rows; whole rounds of a block's groups.
+// More parts hide more of a row's latency and make more slots to join.
+static int norm_groups(int64_t C) { return C <= 512 ? 8 : C <= 1536 ? 4 : C <= 2048 ? 3 : C <= 4096 ? 2 : 1; }
 int norm_parts(int64_t rows, int64_t C, int* part_rows) {
-  const int step = C <= 1024 ? 4 : 1, most = C <= 1024 ? 512 : C <= 4096 ? 768 : C <= 8192 ? 512 : 256;
+  const int step = norm_groups(C), most = C <= 512 ? 512 : 256;
   int64_t per = (rows + most - 1) / most;
   per = (per + step - 1) / step * step;
   *part_rows = (int)per;
@@ -488,17 +489,24 @@ size_t norm_backward_ws_bytes(int64_t rows, int64_t C, int S) {
   return (size_t)2 * (size_t)(parts + S) * (size_t)C * sizeof(float) + ((size_t)S * sizeof(int) + 15) / 16 * 16;
 }
 
+// Waves of a row, eight columns a lane (two times eight from 8192 columns on, where waves end), and the groups that
+// make up a block. Sixteen columns a lane, or more blocks instead of groups, leave a block's few waves waiting for their
+// row: both launches in us, with 16 columns a lane and one group / 8 and one / 8 and these groups: 1531 x 2560: 19, 16, 13;
+// 8192 x 2048: 34, 26, 23; 8192 x 4096: 46, 45, 44; 8192 x 1024: 19, 18, 15.
 template <bool XF, bool DF>
 static void backward_xd(const NormBackward& p, hipStream_t s) {
-  const int chunks = (p.C + 7) / 8;
   const dim3 grid((unsigned)p.parts);
-#define CR_NB(W, V) hipLaunchKernelGGL((norm_backward_kernel<W, V, XF, DF>), grid, dim3(W == 1 ? 256 : W * 64), 0, s, p)
-  if (chunks <= 64) CR_NB(1, 1);
-  else if (chunks <= 128) CR_NB(1, 2);
-  else if (chunks <= 256) CR_NB(4, 1);
-  else if (chunks <= 512) CR_NB(4, 2);
-  else if (chunks <= 1024) CR_NB(8, 2);
-  else CR_NB(16, 2);
+#define CR_NB(W, V, G) hipLaunchKernelGGL((norm_backward_kernel<W, V, G, XF, DF>), grid, dim3(G * W * 64), 0, s, p)
+  if (p.C <= 512) CR_NB(1, 1, 8);
+  else if (p.C <= 1024) CR_NB(2, 1, 4);
+  else if (p.C <= 1536) CR_NB(3, 1, 4);
+  else if (p.C <= 2048) CR_NB(4, 1, 3);
+  else if (p.C <= 3072) CR_NB(6, 1, 2);
+  else if (p.C <= 4096) CR_NB(8, 1, 2);
+  else if (p.C <= 6144) CR_NB(12, 1, 1);
+  else if (p.C <= 8192) CR_NB(16, 1, 1);
+  else if (p.C <= 12288) CR_NB(12, 2, 1);
+  else CR_NB(16, 2, 1);
 #undef CR_NB
 }
 
@@ -521,15 +529,15 @@ hipError_t launch_norm_backward(NormBackward p, uint8_t* ws, hipStream_t s, int*
   *kernels = 1;
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.parts_w || (p.parts == 1 && !p.off)) return e;
-  // Waves that share a sequence's slots: 1 or 4 where it has few (800 rows of 3032 in 38 sequences, about 12 slots
-  // each: 34 us with 16 waves, 22 with 4, for both launches), else 8 once the blocks are more than one a compute unit
-  // (8192 x 4096 in 5 sequences: the join alone 9.4 us with 16, 6.5 with 8), else 16 (1531 x 2560: 5.9 us). Blocks walk
+  // Waves that share a sequence's slots: 1 or 4 where it has few (8192 x 4096 in 48 sequences: 45 us with 1, 49 with 4,
+  // 64 with 16, for both launches; 1000 x 8192 in 7: 22.5, 22.8, 27.5), else 8 once the blocks are more than one a compute
+  // unit (1531 x 2560 in 4 sequences: 15.4 with 8, 16.9 with 16), else 16 (40000 x 128: 22.5, 20.1). Blocks walk
   // the sequences beyond 2048 blocks' worth: most of many lie whole in a part and want nothing here.
   const int slots = p.parts / p.S;
   const unsigned cols = (unsigned)((p.C + 63) / 64), wide = (unsigned)((p.C + 255) / 256);
   auto down = [&](unsigned across) { return (unsigned)std::max(1, std::min(p.S, (int)(1024 / across))); };
-  if (slots < 4) hipLaunchKernelGGL((norm_join_kernel<4, 1>), dim3(wide, down(wide), 2), dim3(256), 0, s, p);
-  else if (slots < 32) hipLaunchKernelGGL((norm_join_kernel<4, 4>), dim3(cols, (unsigned)p.S, 2), dim3(256), 0, s, p);
+  if (slots < 24) hipLaunchKernelGGL((norm_join_kernel<4, 1>), dim3(wide, down(wide), 2), dim3(256), 0, s, p);
+  else if (slots < 64) hipLaunchKernelGGL((norm_join_kernel<4, 4>), dim3(cols, (unsigned)p.S, 2), dim3(256), 0, s, p);
   else if (cols * p.S * 2 > 256) hipLaunchKernelGGL((norm_join_kernel<8, 8>), dim3(cols, (unsigned)p.S, 2), dim3(512), 0, s, p);
   else hipLaunchKernelGGL((norm_join_kernel<16, 16>), dim3(cols, (unsigned)p.S, 2), dim3(1024), 0, s, p);
   *kernels = 2;
