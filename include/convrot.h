@@ -730,7 +730,7 @@ cr_status mxfp4_gemm(const void* a_codes, const void* a_scales, const void* w_co
  *                are one sequence. Empty sequences are fine. One below an earlier one
  *                counts as that earlier one. Rows before the first or behind the last
  *                offset are in no sequence: their places in y, mean, rstd and dx are left
- *                as they are, and nothing of them is read.
+ *                as they are, and what x and dy hold there does not matter.
  *   y, dx        CR_OUT_BF16 or CR_OUT_F32, leading dimensions ldy, lddx
  *   mean, rstd   float32 [rows], written by the forward and read by the backward
  *   dy           bf16 or float32 (dy_type), leading dimension lddy

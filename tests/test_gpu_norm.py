@@ -340,3 +340,34 @@ def test_side_stream_and_graph(cr):
         for t, e in zip((cy, *cg), want):
             assert torch.equal(t, e)
         (x.float() @ x.float().t()).sum().item()
+
+
+@pytest.mark.parametrize("M,C,S,xt,yt", [(4100, 2056, 3, "bf16", "f32"), (4203, 2560, 0, "f32", "bf16"), (4200, 1200, 6, "bf16", "bf16"),
+                                         (2101, 2048, 4, "f32", "f32"), (1531, 1536, 2, "bf16", "bf16"), (900, 3000, 5, "bf16", "f32"),
+                                         (2050, 2568, 0, "bf16", "bf16"), (701, 6000, 3, "f32", "f32"), (517, 10008, 4, "bf16", "bf16"),
+                                         (5000, 400, 30, "bf16", "bf16")])
+def test_shapes_of_many_rows(cr, M, C, S, xt, yt):
+    """Variants that only many rows take, and parts of several rounds of every group."""
+    test_forward_and_backward(cr, M, C, S, xt, yt)
+
+
+def test_what_stands_in_no_sequence_does_not_matter(cr):
+    g = np.random.default_rng(21)
+    M, C = 700, 2560
+    off = torch.tensor([90, 300, 300, 610], dtype=torch.int32, device=DEV)
+    x, dy = _input(g, (M, C), torch.bfloat16, 1.5, 0.7), _input(g, (M, C), torch.bfloat16)
+    w, b = dev(g.standard_normal((3, C)).astype(np.float32)), dev(g.standard_normal((3, C)).astype(np.float32))
+
+    def run():
+        y, dx = torch.full((M, C), -9.0, device=DEV), torch.full((M, C), -9.0, device=DEV)
+        mean, rstd = torch.zeros(M, device=DEV), torch.zeros(M, device=DEV)
+        cr.convrot_layer_norm_forward(x, w, b, seg_offsets=off, out_type=cr.OUT.F32, out=y, mean=mean, rstd=rstd)
+        return (y, mean, rstd, *cr.convrot_layer_norm_backward(dy, x, mean, rstd, w, seg_offsets=off, dx_type=cr.OUT.F32, dx=dx))
+
+    want = run()
+    for v in (float("nan"), float("inf"), -3e38):
+        for t in (x, dy):
+            t[:90] = v
+            t[610:] = v
+        for a, e in zip(run(), want):
+            assert torch.equal(a, e)

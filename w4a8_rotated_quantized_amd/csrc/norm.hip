@@ -163,18 +163,19 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_forward_kernel(Nor
   const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t block = ((int64_t)blockIdx.y << GRID_LG) + blockIdx.x, row = W == 1 ? block * 4 + wave : block;
   if (row >= p.rows) return;
-  int s = 0;
-  if (p.off) {
-    s = sequence_of<false>(p.off, p.S, row, l);
-    if (s >= p.S || row < p.off[0]) return;           // in no sequence: left as it is
-  }
   const int lane = W == 1 ? l : threadIdx.x;
+  // the row's loads before its sequence is known (8192 x 4096 in 6 sequences: 30.3 -> 28.7 us)
   Eight<XF> x[V];
   const int64_t at = row * p.ldx;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * W * 64 + lane) * 8;
     if (c < p.C) x[v].load(p.x, at + c);
+  }
+  int s = 0;
+  if (p.off) {
+    s = sequence_of<false>(p.off, p.S, row, l);
+    if (s >= p.S || row < p.off[0]) return;           // in no sequence: left as it is
   }
   float sum = 0.f;
 #pragma unroll
@@ -446,10 +447,11 @@ __global__ __launch_bounds__(64 * NW) void norm_join_kernel(NormBackward p) {
   }
 }
 
-// Waves of a row and column groups of a lane: the fewest waves with at most 32 values a lane, four from few rows on,
-// where a wave to a row leaves the chip empty. In us: 8192 x 1024 with 1 / 2 / 4 waves: 9.1, 9.2, 11; 8192 x 2048: 14.6,
-// 14.7, 15.1; 1024 x 2048: 5.7, 4.8, 4.3; 8192 x 4096 with 1 / 2 / 4 / 8: 36, 32, 29, 31; 8192 x 12288 with 4 / 8 / 16: 84,
-// 77, 90. Loading weight and bias along with the row instead of behind its sums cost registers: 8192 x 2560 22.7 us for 21.0.
+// Waves of a row and column groups of a lane: the fewest waves that hold it, as long as the rows fill the chip. In us, by
+// waves of a row: 8192 x 2560 in 6 sequences with 1 / 3 / 4 / 5: 21.1, 21.7, 22.7, 25.9, 3000 x 2560: 11.7, 10.8, 11.2, 11.8;
+// 8192 x 2048 with 1 / 4: 15.4, 18.8, 1000 x 2048: 6.4, 5.2; 8192 x 3000 with
+// 3 / 4: 25.0, 25.8; 8192 x 4096 with 4 / 8: 28.7, 33.5; 8192 x 12288 with 8 / 16: 77, 86. Loading weight and bias along
+// with the row instead of behind its sums cost registers: 8192 x 2560 22.7 us for 21.0.
 template <bool XF, bool YF>
 static hipError_t forward_xy(const NormForward& p, hipStream_t s) {
   const int chunks = (p.C + 7) / 8;
@@ -457,8 +459,10 @@ static hipError_t forward_xy(const NormForward& p, hipStream_t s) {
 #define CR_NF(W, V) hipLaunchKernelGGL((norm_forward_kernel<W, V, XF, YF>), W == 1 ? four : one, dim3(W == 1 ? 256 : W * 64), 0, s, p)
   if (chunks <= 64) CR_NF(1, 1);
   else if (chunks <= 128) CR_NF(1, 2);
-  else if (p.rows > 1024 && chunks <= 256) CR_NF(1, 4);
+  else if (chunks <= 256 && p.rows > 1024) CR_NF(1, 4);
   else if (chunks <= 256) CR_NF(4, 1);
+  else if (chunks <= 320 && p.rows > 4096) CR_NF(1, 5);
+  else if (chunks <= 384) CR_NF(3, 2);
   else if (chunks <= 512) CR_NF(4, 2);
   else if (chunks <= 1024) CR_NF(4, 4);
   else CR_NF(8, 4);
