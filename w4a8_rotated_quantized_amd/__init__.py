@@ -5,12 +5,14 @@ behind the C ABI declared in include/convrot.h. PyTorch provides device
 memory and the current stream. There is no fallback: if the library is
 missing this module raises at import, and every non-OK status raises
 ConvRotError with the library's status text. The calls go through ctypes, or
-through the native module where the host's time counts.
+through the native module where the host's time counts: that one is built for one
+Python and one torch, and where it is missing the calls that need it raise ImportError.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
 
 import torch
@@ -32,14 +34,30 @@ __all__ = [
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libconvrot.so")
 
-if not all(os.path.exists(os.path.join(_HERE, f)) for f in ("libconvrot.so", "_native.so")):
+if not os.path.exists(LIB_PATH):
     raise ImportError(
-        f"{LIB_PATH} and _native.so are not built; run __graft_entry__.build() "
+        f"{LIB_PATH} is not built; run __graft_entry__.build() "
         "(hipcc --offload-arch=gfx950). There is no non-HIP fallback.")
 
 lib = ctypes.CDLL(LIB_PATH)
 
-from . import _native  # noqa: E402  (links against the library loaded above)
+
+class _Absent:
+    """In the place of the native module where it cannot be loaded."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        if name.startswith("__"):
+            raise AttributeError(name)
+        raise ImportError(f"this call needs {__name__}._native ({self._why}); run __graft_entry__.build()")
+
+
+try:
+    _native = importlib.import_module("._native", __name__)     # links against the library loaded above
+except ImportError as _why:
+    _native = _Absent(str(_why))
 
 
 class Q:

@@ -1,6 +1,6 @@
 """Builds libconvrot.so (all gfx950 HIP kernels and the C-ABI host layer) with
-hipcc, and _native.so (the CPython side of some entry points) with g++, both
-in-tree. Every call recompiles."""
+hipcc, and _native (the CPython side of some entry points, for this Python and
+this torch) with g++, both in-tree. Every call recompiles."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
-NATIVE = os.path.join(HERE, "_native.so")
+# named for the interpreter, so that no other one loads it: it uses more than the stable interface
+NATIVE = os.path.join(HERE, "_native" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["rq.hip", "pack.hip", "merge.hip", "gemm_w4a4.hip", "gemm_int.hip", "gemm_w4a8.hip", "gemm_f6.hip", "abi.cpp",
            "lora.hip", "act.hip", "adapter_abi.cpp", "mx.hip", "gemm_mx.hip", "norm.hip", "adamw.hip", "block_abi.cpp"]
 
@@ -50,7 +51,7 @@ def _compile_binding() -> str:
     obj = os.path.join(BUILD, "binding.o")
     rocm = os.path.dirname(os.path.dirname(HIPCC))
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-attributes", "-D__HIP_PLATFORM_AMD__",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DBUILT_FOR_TORCH="{torch.__version__}"',
            *[f"-isystem{p}" for p in (*include_paths(), sysconfig.get_paths()["include"], os.path.join(rocm, "include"))],
            "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -70,6 +71,9 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, NATIVE)
+    unnamed = os.path.join(HERE, "_native.so")           # its earlier name, which any interpreter loads
+    if os.path.exists(unnamed):
+        os.remove(unnamed)
 
 
 def build(verbose: bool = False) -> str:

@@ -19,6 +19,7 @@
 #include <c10/hip/HIPStream.h>
 
 #include <cstdio>
+#include <cstring>
 #include <vector>
 
 #include "../../include/convrot.h"
@@ -501,4 +502,14 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nu
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__native() { return PyModule_Create(&module); }
+// Tensors are read through inlined code of the headers, which fits one torch.
+PyMODINIT_FUNC PyInit__native() {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  Py_XDECREF(torch);
+  const char* text = version ? PyUnicode_AsUTF8(version) : nullptr;
+  const bool same = text && !std::strcmp(text, BUILT_FOR_TORCH);
+  if (text && !same) PyErr_Format(PyExc_ImportError, "built for torch %s, this is %s", BUILT_FOR_TORCH, text);
+  Py_XDECREF(version);
+  return same ? PyModule_Create(&module) : nullptr;
+}
