@@ -65,3 +65,94 @@ def test_native_module_is_named_for_its_python():
     """No other Python takes the file for its own: the interface that it uses is not the stable one."""
     import w4a8_rotated_quantized_amd as cr
     assert cr._native.__file__ == NATIVE and not os.path.exists(os.path.join(PKG, "_native.so"))
+
+
+# ---------------------------------------------------------------------------
+# Around a call: the native module linked to a stand-in for the library
+# (binding_stub.cpp), on tensors that are said to be on a GPU and have no memory.
+# ---------------------------------------------------------------------------
+def _stub_missing():
+    if not shutil.which("g++"):
+        return "g++ not available"
+    if not os.path.isdir("/opt/rocm/include/hip"):
+        return "HIP headers not available"
+    if not os.path.exists(NATIVE):
+        return "the native module is not built"
+    return None
+
+
+@pytest.fixture(scope="module")
+def stub(tmp_path_factory):
+    if _stub_missing():
+        pytest.skip(_stub_missing())
+    to = tmp_path_factory.mktemp("stub") / "libconvrot.so"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-pthread", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                    f"-I{os.path.join(ROOT, 'include')}", "-Wl,-soname,libconvrot.so", os.path.join(ROOT, "tests", "binding_stub.cpp"),
+                    "-o", str(to)], check=True)
+    return to
+
+
+HARNESS = """
+import ctypes, importlib.util, sys, threading, time, weakref
+import torch
+stub = ctypes.CDLL(sys.argv[1], ctypes.RTLD_GLOBAL)
+spec = importlib.util.spec_from_file_location("_native", sys.argv[2])
+n = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(n)
+
+class OnGpu(torch.Tensor):
+    @staticmethod
+    def __new__(cls, dtype, *shape):
+        return torch.Tensor._make_wrapper_subclass(cls, shape, dtype=dtype, device="cuda:0")
+    @classmethod
+    def __torch_dispatch__(cls, f, types, args=(), kwargs=None):
+        raise AssertionError(str(f))
+
+T = OnGpu
+bf, f32, u8, i8 = torch.bfloat16, torch.float32, torch.uint8, torch.int8
+M, C, N = 4, 64, 8
+moments = lambda: ([T(i8, 300), T(i8, 5)], [T(u8, 300), T(u8, 5)], [T(f32, 2), T(f32, 1)], [T(f32, 2), T(f32, 1)])
+two = lambda dtype: [T(dtype, 300), T(dtype, 5)]
+
+def calls():
+    # name, function, arguments, places of the tensors that it writes (in lists: all of a list)
+    m, v, ms, vs = moments()
+    yield "mxfp4_quantize", [T(bf, M, C), 0, T(u8, 1, M, 64), T(u8, 1, M, 4), 0], [2, 3]
+    yield "mxfp4_dequantize", [T(u8, 1, M, 64), T(u8, 1, M, 4), C, 0, 0, T(bf, M, C), 0], [5]
+    yield "mxfp4_gemm", [T(u8, 1, M, 64), T(u8, 1, M, 4), T(u8, 1, N, 64), T(u8, 1, N, 4), None, 1, T(f32, M, N), 0], [6]
+    yield "layer_norm_forward", [T(bf, M, C), T(bf, C), T(bf, C), None, 1e-6, False, 0, T(bf, M, C), T(f32, M), T(f32, M), 0], [7, 8, 9]
+    yield "layer_norm_backward", [T(bf, M, C), T(bf, M, C), T(f32, M), T(f32, M), T(bf, C), None, False, None, 0, T(bf, M, C), T(f32, C),
+                                  T(f32, C), True, True, True, T(u8, 64), 0], [9, 10, 11, 15]
+    yield "adamw_step", [two(f32), two(f32), two(f32), two(f32), None, None, None, None, 1, .1, .9, .99, 1e-8, 0., 0, 0], [0, 2, 3]
+    yield "adamw_step", [two(f32), two(bf), m, v, two(bf), ms, vs, T(f32, 1), 1, .1, .9, .99, 1e-8, 0., 0, 0], [0, 2, 3, 4, 5, 6]
+    m, v, ms, vs = moments()
+    yield "adamw_moments", [m, v, ms, vs, T(f32, 305), T(f32, 305), 0], [4, 5]
+
+def flat(args):
+    return [t for a in args for t in (a if type(a) is list else [a]) if isinstance(t, torch.Tensor)]
+"""
+
+OTHERS = HARNESS + """
+for i, (name, args, _) in enumerate(calls()):
+    held, alive = [weakref.ref(t) for t in flat(args)], []
+    lists = [a for a in args if type(a) is list]
+    def other():
+        while stub.stub_calls() <= i:
+            time.sleep(0.001)
+        for l in lists:                        # the caller's lists change under the call
+            l.clear()
+        alive.append(all(r() is not None for r in held))
+        stub.stub_word()
+    t = threading.Thread(target=other)
+    t.start()
+    result = getattr(n, name)(*args)
+    t.join()
+    assert type(result) is not int or result == 0, f"{name}: no other thread ran during the call"
+    assert alive == [True], name
+print("ok")
+"""
+
+
+def test_other_threads_run_during_a_call(stub):
+    """A call may wait, for memory or for a place in the queue, for what another Python thread has yet to do."""
+    assert "ok" in _python(OTHERS, ROOT, stub, NATIVE)

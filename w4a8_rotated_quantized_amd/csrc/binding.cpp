@@ -161,6 +161,17 @@ PyObject* pack(std::initializer_list<const Tensor*> ts) {
 }
 PyObject* refused(cr_status st) { return PyLong_FromLong((long)st); }
 
+// Without the interpreter's lock: outputs are allocated and the call is launched, either of
+// which may wait for the GPU, and so for what another thread of the interpreter does. Between
+// this and its end nothing of Python's is touched.
+struct Unlocked {
+  PyThreadState* thread = PyEval_SaveThread();
+  Unlocked() = default;
+  ~Unlocked() { PyEval_RestoreThread(thread); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+};
+
 // Every entry runs inside this: Wrong -> ValueError, torch's errors as torch turns them.
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -195,9 +206,15 @@ PyObject* mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor *gc = tensor_or_none(a[2], "codes"), *gs = tensor_or_none(a[3], "scales");
     dense_or_null(gc, "codes", ScalarType::Byte, index, {tiles, rows, 64});
     dense_or_null(gs, "scales", ScalarType::Byte, index, {tiles, rows, 4});
-    const Tensor codes = gc ? *gc : empty({tiles, rows, 64}, ScalarType::Byte, x);
-    const Tensor scales = gs ? *gs : empty({tiles, rows, 4}, ScalarType::Byte, x);
-    const cr_status st = mxfp4_quantize(px, ldx, rows, K, small(a[1]), codes.data_ptr(), scales.data_ptr(), stream);
+    const int rot_group = small(a[1]);
+    Tensor codes, scales;
+    cr_status st;
+    {
+      const Unlocked free;
+      codes = gc ? *gc : empty({tiles, rows, 64}, ScalarType::Byte, x);
+      scales = gs ? *gs : empty({tiles, rows, 4}, ScalarType::Byte, x);
+      st = mxfp4_quantize(px, ldx, rows, K, rot_group, codes.data_ptr(), scales.data_ptr(), stream);
+    }
     return st ? refused(st) : pack({&codes, &scales});
   });
 }
@@ -229,13 +246,18 @@ PyObject* mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const MxPair p = mx_pair(codes, tensor(a[1], "scales"), "the", index);
     const int64_t K = whole(a[2]);
     if (K < 0 || K > p.tiles * 128 || p.tiles != (K + 127) / 128) wrong("K does not fit the codes' tiles");
-    const int type = small(a[4]);
+    const int rot_group = small(a[3]), type = small(a[4]);
     const ScalarType dt = out_dtype(type);
     const Tensor* go = tensor_or_none(a[5], "out");
     int64_t ldo = K;
     if (go) spaced(*go, "out", dt, index, p.rows, K, &ldo);
-    const Tensor out = go ? *go : empty({p.rows, K}, dt, codes);
-    const cr_status st = mxfp4_dequantize(p.codes, p.scales, p.rows, K, small(a[3]), out.data_ptr(), (cr_out)type, ldo, stream);
+    Tensor out;
+    cr_status st;
+    {
+      const Unlocked free;
+      out = go ? *go : empty({p.rows, K}, dt, codes);
+      st = mxfp4_dequantize(p.codes, p.scales, p.rows, K, rot_group, out.data_ptr(), (cr_out)type, ldo, stream);
+    }
     return st ? refused(st) : THPVariable_Wrap(out);
   });
 }
@@ -256,9 +278,14 @@ PyObject* mx_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* go = tensor_or_none(a[6], "out");
     int64_t ldc = w.rows;
     if (go) spaced(*go, "out", dt, index, p.rows, w.rows, &ldc);
-    const Tensor out = go ? *go : empty({p.rows, w.rows}, dt, ac);
-    const cr_status st = mxfp4_gemm(p.codes, p.scales, w.codes, w.scales, pb, out.data_ptr(), (cr_out)type, ldc, p.rows, w.rows,
-                                    p.tiles * 128, stream);
+    Tensor out;
+    cr_status st;
+    {
+      const Unlocked free;
+      out = go ? *go : empty({p.rows, w.rows}, dt, ac);
+      st = mxfp4_gemm(p.codes, p.scales, w.codes, w.scales, pb, out.data_ptr(), (cr_out)type, ldc, p.rows, w.rows, p.tiles * 128,
+                      stream);
+    }
     return st ? refused(st) : THPVariable_Wrap(out);
   });
 }
@@ -318,11 +345,17 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     dense_or_null(gr, "rstd", ScalarType::Float, index, {M});
     const double eps = real(a[4]);
     const bool plus = truth(a[5]);
-    const Tensor out = go ? *go : empty({M, C}, dt, x);
-    const Tensor mean = gm ? *gm : empty({M}, ScalarType::Float, x), rstd = gr ? *gr : empty({M}, ScalarType::Float, x);
-    const cr_status st = convrot_layer_norm_forward(px, x_type, ldx, f.w, f.ldw, f.b, f.ldb, f.type, plus, f.off, count_of(f.S), eps,
-                                                    out.data_ptr(), (cr_out)type, ldy, static_cast<float*>(mean.data_ptr()),
-                                                    static_cast<float*>(rstd.data_ptr()), M, C, stream);
+    Tensor out, mean, rstd;
+    cr_status st;
+    {
+      const Unlocked free;
+      out = go ? *go : empty({M, C}, dt, x);
+      mean = gm ? *gm : empty({M}, ScalarType::Float, x);
+      rstd = gr ? *gr : empty({M}, ScalarType::Float, x);
+      st = convrot_layer_norm_forward(px, x_type, ldx, f.w, f.ldw, f.b, f.ldb, f.type, plus, f.off, count_of(f.S), eps, out.data_ptr(),
+                                      (cr_out)type, ldy, static_cast<float*>(mean.data_ptr()), static_cast<float*>(rstd.data_ptr()), M,
+                                      C, stream);
+    }
     return st ? refused(st) : pack({&out, &mean, &rstd});
   });
 }
@@ -363,18 +396,23 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dense_or_null(gd, "d_bias", ScalarType::Float, index, f.shape);
       if (gs && (!on(*gs, index) || !gs->is_contiguous())) wrong("workspace must be contiguous on GPU %d", index);
     }
-    if (want_dx) dx = gx ? *gx : empty({M, C}, dt, dy);
-    if (want_w) {
-      dw = gw ? *gw : empty(f.shape, ScalarType::Float, dy);
-      db = gd ? *gd : empty(f.shape, ScalarType::Float, dy);
-      const size_t need = convrot_layer_norm_backward_workspace_size(M, C, count_of(f.S));
-      ws = gs ? *gs : empty({(int64_t)(need < 16 ? 16 : need)}, ScalarType::Byte, dy);
+    const bool plus = truth(a[6]);
+    cr_status st;
+    {
+      const Unlocked free;
+      if (want_dx) dx = gx ? *gx : empty({M, C}, dt, dy);
+      if (want_w) {
+        dw = gw ? *gw : empty(f.shape, ScalarType::Float, dy);
+        db = gd ? *gd : empty(f.shape, ScalarType::Float, dy);
+        const size_t need = convrot_layer_norm_backward_workspace_size(M, C, count_of(f.S));
+        ws = gs ? *gs : empty({(int64_t)(need < 16 ? 16 : need)}, ScalarType::Byte, dy);
+      }
+      st = convrot_layer_norm_backward(pdy, dy_type, lddy, px, x_type, ldx, pm, pr, f.w, f.ldw, f.type, plus, f.off, count_of(f.S), pb,
+                                       ldb, want_dx ? dx.data_ptr() : nullptr, (cr_out)type, lddx,
+                                       want_w ? static_cast<float*>(dw.data_ptr()) : nullptr,
+                                       want_w ? static_cast<float*>(db.data_ptr()) : nullptr, accumulate, M, C,
+                                       want_w ? ws.data_ptr() : nullptr, want_w ? ws.nbytes() : 0, stream);
     }
-    const cr_status st = convrot_layer_norm_backward(
-        pdy, dy_type, lddy, px, x_type, ldx, pm, pr, f.w, f.ldw, f.type, truth(a[6]), f.off, count_of(f.S), pb, ldb,
-        want_dx ? dx.data_ptr() : nullptr, (cr_out)type, lddx, want_w ? static_cast<float*>(dw.data_ptr()) : nullptr,
-        want_w ? static_cast<float*>(db.data_ptr()) : nullptr, accumulate, M, C, want_w ? ws.data_ptr() : nullptr,
-        want_w ? ws.nbytes() : 0, stream);
     return st ? refused(st) : pack({want_dx ? &dx : nullptr, want_w ? &dw : nullptr, want_w ? &db : nullptr, want_w ? &ws : nullptr});
   });
 }
@@ -382,22 +420,23 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // ---------------------------------------------------------------------------
 // optimizer step
 // ---------------------------------------------------------------------------
-// a list or tuple of tensors
+// a list or tuple of tensors, held with its tensors until the call has returned: the caller's list may change
+// while the interpreter's lock is given up
 struct Tensors {
-  PyObject* fast = nullptr;
+  PyObject* held = nullptr;
   const char* what;
   Py_ssize_t n = 0;
   Tensors(PyObject* o, const char* what) : what(what) {
     if (o == Py_None) return;
-    fast = PySequence_Fast(o, "lists of tensors are wanted");
-    if (!fast) throw python_error();
-    n = PySequence_Fast_GET_SIZE(fast);
+    held = PySequence_Tuple(o);
+    if (!held) throw python_error();
+    n = PyTuple_GET_SIZE(held);
   }
-  ~Tensors() { Py_XDECREF(fast); }
+  ~Tensors() { Py_XDECREF(held); }
   Tensors(const Tensors&) = delete;
   Tensors& operator=(const Tensors&) = delete;
-  explicit operator bool() const { return fast != nullptr; }
-  const Tensor& operator[](Py_ssize_t i) const { return tensor(PySequence_Fast_GET_ITEM(fast, i), what); }
+  explicit operator bool() const { return held != nullptr; }
+  const Tensor& operator[](Py_ssize_t i) const { return tensor(PyTuple_GET_ITEM(held, i), what); }
 };
 
 void* element(const Tensors& l, Py_ssize_t i, ScalarType type, int index, int64_t numel) {
@@ -453,8 +492,15 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     moments(e, m, v, ms, vs, index);
     const float* scale =
         static_cast<const float*>(dense_or_null(tensor_or_none(a[7], "grad_scale"), "grad_scale", ScalarType::Float, index, {1}));
-    return refused(convrot_adamw_step(e.data(), entries(e), grad_type, ms ? 8 : 32, real(a[9]), real(a[10]), real(a[11]), real(a[12]),
-                                      real(a[13]), whole(a[8]), scale, (uint32_t)whole(a[14]), stream));
+    const double lr = real(a[9]), beta1 = real(a[10]), beta2 = real(a[11]), eps = real(a[12]), decay = real(a[13]);
+    const int64_t step = whole(a[8]);
+    const uint32_t seed = (uint32_t)whole(a[14]);
+    cr_status st;
+    {
+      const Unlocked free;
+      st = convrot_adamw_step(e.data(), entries(e), grad_type, ms ? 8 : 32, lr, beta1, beta2, eps, decay, step, scale, seed, stream);
+    }
+    return refused(st);
   });
 }
 
@@ -477,9 +523,15 @@ PyObject* adamw_moments(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor *gm = tensor_or_none(a[4], "exp_avg_out"), *gv = tensor_or_none(a[5], "exp_avg_sq_out");
     dense_or_null(gm, "exp_avg_out", ScalarType::Float, index, {total});
     dense_or_null(gv, "exp_avg_sq_out", ScalarType::Float, index, {total});
-    const Tensor om = gm ? *gm : empty({total}, ScalarType::Float, m[0]), ov = gv ? *gv : empty({total}, ScalarType::Float, m[0]);
-    const cr_status st = convrot_adamw_moments(e.data(), entries(e), static_cast<float*>(om.data_ptr()),
-                                               static_cast<float*>(ov.data_ptr()), stream);
+    const Tensor& like = m[0];
+    Tensor om, ov;
+    cr_status st;
+    {
+      const Unlocked free;
+      om = gm ? *gm : empty({total}, ScalarType::Float, like);
+      ov = gv ? *gv : empty({total}, ScalarType::Float, like);
+      st = convrot_adamw_moments(e.data(), entries(e), static_cast<float*>(om.data_ptr()), static_cast<float*>(ov.data_ptr()), stream);
+    }
     return st ? refused(st) : pack({&om, &ov});
   });
 }
