@@ -156,3 +156,27 @@ print("ok")
 def test_other_threads_run_during_a_call(stub):
     """A call may wait, for memory or for a place in the queue, for what another Python thread has yet to do."""
     assert "ok" in _python(OTHERS, ROOT, stub, NATIVE)
+
+
+VERSIONS = HARNESS + """
+stub.stub_wait(0)
+for name, args, written in calls():
+    places = [flat([args[k]]) for k in written]
+    ours = [t for p in places for t in p]
+    result = getattr(n, name)(*args)
+    assert type(result) is not int or result == 0, name
+    for t in flat(args):
+        assert t._version == any(t is o for o in ours), (name, tuple(t.shape), t.dtype, t._version)
+with torch.inference_mode():
+    inner = T(f32, M, C)
+assert inner.is_inference()
+for mode in (torch.inference_mode, torch.no_grad):     # tensors without a version are left alone
+    with mode():
+        assert type(n.mxfp4_gemm(T(u8, 1, M, 64), T(u8, 1, M, 4), T(u8, 1, 64, 64), T(u8, 1, 64, 4), None, 1, inner, 0)) is not int
+print("ok")
+"""
+
+
+def test_written_tensors_change_their_version(stub):
+    """Autograd then refuses a backward pass that needs what was there before."""
+    assert "ok" in _python(VERSIONS, ROOT, stub, NATIVE)

@@ -200,3 +200,24 @@ def test_trains_without_sticking(cr):
     m8, v8 = cr.convrot_adamw_moments([m], [v], [ms], [vs])
     # rounding up and down by turns: the moments are those of the float32 run on average
     assert abs(float(v8.mean() / V[0].mean()) - 1) < 0.05
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_backward_pass_behind_the_step_is_refused(cr, given):
+    """What a graph of before the step needs of the parameters and their copies is gone: autograd says so."""
+    stream = torch.cuda.Stream() if given else None
+    p = torch.ones(64, device=DEV, requires_grad=True)
+    copy = torch.ones(64, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    late, late_copy = (p * p).sum(), (copy * copy).sum()
+    early, = torch.autograd.grad((p * 3.0).sum(), p)
+    torch.cuda.synchronize()
+    cr.convrot_adamw_step([p], [early], [torch.zeros(64, device=DEV)], [torch.zeros(64, device=DEV)], step=1, lr=0.5, weight_decay=0.0,
+                          copies=[copy], stream=stream)
+    torch.cuda.synchronize()
+    for loss in (late, late_copy):
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    again, = torch.autograd.grad((p * p).sum(), p)
+    assert torch.equal(again, 2 * p.detach()) and torch.equal(copy.detach(), p.detach().to(torch.bfloat16))
+    # 1 - 0.5 * 3 / (3 + 1e-8), a few roundings off
+    assert float((p.detach() - 0.5).abs().max()) < 1e-6

@@ -161,6 +161,14 @@ PyObject* pack(std::initializer_list<const Tensor*> ts) {
 }
 PyObject* refused(cr_status st) { return PyLong_FromLong((long)st); }
 
+// A given tensor that a call has written: its version changes, so that autograd refuses a backward
+// pass that needs what it held before. Tensors of inference mode have none.
+void written(const Tensor* t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+// a call that enqueued something, all of it or (with a launch that failed) a part
+bool ran(cr_status st) { return st == CR_OK || st == CR_ERR_HIP; }
+
 // Without the interpreter's lock: outputs are allocated and the call is launched, either of
 // which may wait for the GPU, and so for what another thread of the interpreter does. Between
 // this and its end nothing of Python's is touched.
@@ -215,6 +223,8 @@ PyObject* mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       scales = gs ? *gs : empty({tiles, rows, 4}, ScalarType::Byte, x);
       st = mxfp4_quantize(px, ldx, rows, K, rot_group, codes.data_ptr(), scales.data_ptr(), stream);
     }
+    if (ran(st))
+      for (const Tensor* t : {gc, gs}) written(t);
     return st ? refused(st) : pack({&codes, &scales});
   });
 }
@@ -258,6 +268,7 @@ PyObject* mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       out = go ? *go : empty({p.rows, K}, dt, codes);
       st = mxfp4_dequantize(p.codes, p.scales, p.rows, K, rot_group, out.data_ptr(), (cr_out)type, ldo, stream);
     }
+    if (ran(st)) written(go);
     return st ? refused(st) : THPVariable_Wrap(out);
   });
 }
@@ -286,6 +297,7 @@ PyObject* mx_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       st = mxfp4_gemm(p.codes, p.scales, w.codes, w.scales, pb, out.data_ptr(), (cr_out)type, ldc, p.rows, w.rows, p.tiles * 128,
                       stream);
     }
+    if (ran(st)) written(go);
     return st ? refused(st) : THPVariable_Wrap(out);
   });
 }
@@ -356,6 +368,8 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                       (cr_out)type, ldy, static_cast<float*>(mean.data_ptr()), static_cast<float*>(rstd.data_ptr()), M,
                                       C, stream);
     }
+    if (ran(st))
+      for (const Tensor* t : {go, gm, gr}) written(t);
     return st ? refused(st) : pack({&out, &mean, &rstd});
   });
 }
@@ -412,6 +426,11 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                        want_w ? static_cast<float*>(dw.data_ptr()) : nullptr,
                                        want_w ? static_cast<float*>(db.data_ptr()) : nullptr, accumulate, M, C,
                                        want_w ? ws.data_ptr() : nullptr, want_w ? ws.nbytes() : 0, stream);
+    }
+    if (ran(st)) {
+      if (want_dx) written(gx);
+      if (want_w)
+        for (const Tensor* t : {gw, gd, gs}) written(t);
     }
     return st ? refused(st) : pack({want_dx ? &dx : nullptr, want_w ? &dw : nullptr, want_w ? &db : nullptr, want_w ? &ws : nullptr});
   });
@@ -500,6 +519,9 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const Unlocked free;
       st = convrot_adamw_step(e.data(), entries(e), grad_type, ms ? 8 : 32, lr, beta1, beta2, eps, decay, step, scale, seed, stream);
     }
+    if (ran(st))
+      for (const Tensors* l : {&p, &m, &v, &c, &ms, &vs})
+        for (Py_ssize_t i = 0; i < l->n; ++i) written(&(*l)[i]);
     return refused(st);
   });
 }
@@ -532,6 +554,8 @@ PyObject* adamw_moments(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ov = gv ? *gv : empty({total}, ScalarType::Float, like);
       st = convrot_adamw_moments(e.data(), entries(e), static_cast<float*>(om.data_ptr()), static_cast<float*>(ov.data_ptr()), stream);
     }
+    if (ran(st))
+      for (const Tensor* t : {gm, gv}) written(t);
     return st ? refused(st) : pack({&om, &ov});
   });
 }
