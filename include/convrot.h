@@ -796,7 +796,8 @@ cr_status convrot_layer_norm_backward(const void* dy, cr_out dy_type, int64_t ld
  *   convrot_adamw_moments: m and v of 8-bit entries as float32, entry after entry
  *                in exp_avg_out and exp_avg_sq_out [sum of n] (param, grad and copy of the
  *                entries are not read).
- * 1 <= count <= 65536, step >= 1, lr, eps and weight_decay >= 0, 0 <= beta < 1. One launch for
+ * 1 <= count <= 65536, step >= 1, lr, eps and weight_decay >= 0, eps 0 or from 2^-126 on (with 0 an
+ * element whose gradients were all 0 becomes NaN, as the formula has it), 0 <= beta < 1. One launch for
  * up to 63 entries (84 of convrot_adamw_moments) of 2^31 elements together, in the list's order; entries of a list
  * may hold the same tensor only once.
  */

@@ -213,3 +213,14 @@ def test_host_layer_under_sanitizers(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=600)
     assert r.returncode == 0, (r.stdout + r.stderr)[-4000:]
     assert "all ok" in r.stdout or "skipped" in r.stdout
+
+
+def test_adamw_refuses_an_eps_whose_reciprocal_is_infinite(cr):
+    """Below 2^-126 a float32 eps is subnormal (or zero): without a gradient the update would be 0 times infinity, not 0."""
+    e = (_Entry * 1)(_Entry(param=A, grad=A, avg=A, sq=A, n=100))
+
+    def s(eps):
+        return cr.lib.convrot_adamw_step(ctypes.addressof(e), 1, 1, 32, 1e-3, 0.9, 0.999, eps, 0.0, 1, None, 0, None)
+
+    assert [s(eps) for eps in (0.0, 2.0 ** -126, 1e-30, 1e-8, 1.0)] == [4] * 5
+    assert [s(eps) for eps in (2.0 ** -126 * (1 - 2.0 ** -23), 2.0 ** -127, 1e-40, 1e-50, 5e-324)] == [1] * 5

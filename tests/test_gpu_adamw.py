@@ -221,3 +221,21 @@ def test_a_backward_pass_behind_the_step_is_refused(cr, given):
     assert torch.equal(again, 2 * p.detach()) and torch.equal(copy.detach(), p.detach().to(torch.bfloat16))
     # 1 - 0.5 * 3 / (3 + 1e-8), a few roundings off
     assert float((p.detach() - 0.5).abs().max()) < 1e-6
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_smallest_eps(cr, bits):
+    """Elements without a gradient stay where they are; the others move by the rate (m / sqrt(v) is 1 in a first step)."""
+    n = 600
+    p, grad = torch.ones(n, device=DEV), torch.zeros(n, device=DEV)
+    grad[::3] = 1e-4
+    if bits == 8:
+        m, v, ms, vs = _codes(n)
+        extra = dict(exp_avg_scales=[ms], exp_avg_sq_scales=[vs], seed=9)
+    else:
+        m, v, extra = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV), {}
+    cr.convrot_adamw_step([p], [grad], [m], [v], step=1, lr=0.25, eps=2.0 ** -126, weight_decay=0.0, **extra)
+    want = torch.ones(n, device=DEV)
+    want[::3] = 0.75
+    # 24 roundings on the way to the update of a quarter
+    assert float((p - want).abs().max()) <= 24 * U and torch.equal(p[1::3], want[1::3])

@@ -256,6 +256,8 @@ cr_status convrot_adamw_step(const cr_adamw_tensor* tensors, int count, cr_out g
   if (!(lr >= 0.0) || !(eps >= 0.0) || !(weight_decay >= 0.0) || !(beta1 >= 0.0 && beta1 < 1.0) ||
       !(beta2 >= 0.0 && beta2 < 1.0) || step < 1 || !aligned4(grad_scale))
     return CR_ERR_INVALID_ARGUMENT;
+  // the kernel multiplies by the denominator's reciprocal, which is infinite where that is eps alone and subnormal
+  if (eps > 0.0 && (float)eps < 0x1p-126f) return CR_ERR_INVALID_ARGUMENT;
   if ((st = adamw_entries(tensors, count, true, state_bits == 8)) != CR_OK) return st;
   if ((st = cr::host_device_check()) != CR_OK) return st;
   cr::AdamwStep p;
