@@ -726,6 +726,8 @@ cr_status mxfp4_gemm(const void* a_codes, const void* a_scales, const void* w_co
  *                ldw and ldbias (not read with S = 1), so that both can be columns of one
  *                modulation tensor; each may be NULL (weight: 1 whatever one_plus is, bias: 0)
  *   one_plus     0, or 1: the weight is given without its 1 (adaLN's scale)
+ *   eps          0, or from 2^-149 (the smallest float32) to 1e30; with 0 a row without
+ *                variance is NaN, as the formula has it
  *   seg_offsets  int32 [S + 1] on the device, ascending; NULL with S = 1: all rows
  *                are one sequence. Empty sequences are fine. One below an earlier one
  *                counts as that earlier one. Rows before the first or behind the last

@@ -224,3 +224,12 @@ def test_adamw_refuses_an_eps_whose_reciprocal_is_infinite(cr):
 
     assert [s(eps) for eps in (0.0, 2.0 ** -126, 1e-30, 1e-8, 1.0)] == [4] * 5
     assert [s(eps) for eps in (2.0 ** -126 * (1 - 2.0 ** -23), 2.0 ** -127, 1e-40, 1e-50, 5e-324)] == [1] * 5
+
+
+def test_norm_refuses_an_eps_that_rounds_to_zero(cr):
+    """As a float32 it would be 0: a row without variance then has no rstd, where the formula's is finite and xh 0."""
+    def f(eps):
+        return cr.lib.convrot_layer_norm_forward(A, 0, 64, None, 64, None, 64, 0, 0, None, 1, eps, A, 0, 64, A, A, 5, 64, None)
+
+    assert [f(eps) for eps in (0.0, 2.0 ** -149, 1e-40, 1e-6, 1.0)] == [4] * 5
+    assert [f(eps) for eps in (2.0 ** -151, 1e-50, 5e-324)] == [1] * 3

@@ -371,3 +371,16 @@ def test_what_stands_in_no_sequence_does_not_matter(cr):
             t[610:] = v
         for a, e in zip(run(), want):
             assert torch.equal(a, e)
+
+
+def test_the_smallest_eps(cr):
+    """Rows without variance are all bias, whatever the eps above 0."""
+    x = torch.cat([torch.zeros((3, 520), device=DEV), torch.full((2, 520), 4.0, device=DEV)])
+    b = torch.randn(520, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    for eps in (2.0 ** -149, 2.0 ** -126, 1e-6):
+        y, mean, rstd = cr.convrot_layer_norm_forward(x, bias=b, eps=eps, out_type=cr.OUT.F32)
+        assert torch.equal(y[:3], b.expand(3, -1)) and bool(torch.isfinite(rstd).all()) and bool((mean[:3] == 0).all())
+        # the mean of 520 fours is within 80 roundings of 4, or no row without variance: y stays finite
+        assert bool(torch.isfinite(y).all())
+    with pytest.raises(cr.ConvRotError):
+        cr.convrot_layer_norm_forward(x, eps=1e-50)

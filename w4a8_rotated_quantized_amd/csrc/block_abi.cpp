@@ -152,6 +152,7 @@ cr_status convrot_layer_norm_forward(const void* x, cr_out x_type, int64_t ldx, 
       !absent_or_aligned(seg_offsets))
     return CR_ERR_INVALID_ARGUMENT;
   if (one_plus < 0 || one_plus > 1 || !(eps >= 0.0) || !(eps < 1e30)) return CR_ERR_INVALID_ARGUMENT;
+  if (eps > 0.0 && (float)eps == 0.f) return CR_ERR_INVALID_ARGUMENT;
   cr_status st;
   for (const int type : {(int)x_type, (int)y_type, (int)affine_type})
     if ((st = float_output(type)) != CR_OK) return st;
