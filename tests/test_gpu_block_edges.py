@@ -286,3 +286,140 @@ def test_adamw_longest_tensor(cr):
             assert torch.equal(t[at], want)
             t[at] = 0
             assert t.count_nonzero() == 0
+
+
+# 256 x 256 blocks with more stages than their ring of four has places: 10, 12 and 21 of them, ragged at every end
+LARGE = [(3850, 4088, 1184), (3850, 4088, 1536), (1531, 9208, 2592)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", LARGE)
+def test_large_blocks_past_their_ring(cr, shape, out):
+    M, N, K = shape
+    say(f"mx large blocks {shape} {out}")
+    a, ac, ab = _operand(1, M, K)
+    w, wc, wb = _operand(2, N, K)
+    bias = torch.randn(N, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV).to(torch.bfloat16)
+    want, mag = mx.gemm(a, w, bias.double().cpu().numpy())
+    hold = torch.full((M + 1, N + 8), -5.0, dtype=torch.bfloat16 if out == "bf16" else torch.float32, device=DEV)
+    y = cr.mxfp4_gemm(ac, ab, wc, wb, bias=bias, out_type=cr.OUT.BF16 if out == "bf16" else cr.OUT.F32, out=hold[:M, :N])
+    half = 2.0 ** -8 if out == "bf16" else 2.0 ** -24
+    # exact products, K + 1 float32 sums that may cut (2^-23 each), one rounding
+    assert np.all(np.abs(y.double().cpu().numpy() - want) <= 2.0 ** -23 * (K + 2) * mag + half * (1 + 2.0 ** -8) * np.abs(want))
+    assert bool((hold[:, N:] == -5).all()) and bool((hold[M] == -5).all())
+
+
+@pytest.mark.parametrize("shape", LARGE)
+def test_large_blocks_exact(cr, shape):
+    """Unit powers: products are quarters of whole numbers up to 144, so their sums stay below 2^24 quarters and are exact."""
+    M, N, K = shape
+    g = np.random.default_rng([9, M, N, K])
+    one = np.full((1, K // 32), 127, np.uint8)
+    ca, cw = (g.integers(0, 16, (rows, K)).astype(np.uint8) for rows in (M, N))
+    (pa, ba), (pw, bw) = (mx.pack(c, np.repeat(one, len(c), 0)) for c in (ca, cw))
+    # whole numbers: the float32 product of values times two is exact too
+    two = [torch.from_numpy(2 * mx.values(c, np.repeat(one, len(c), 0))).float().to(DEV) for c in (ca, cw)]
+    want = (two[0].double() @ two[1].double().T) / 4
+    for _ in range(3):
+        assert torch.equal(cr.mxfp4_gemm(dev(pa), dev(ba), dev(pw), dev(bw), out_type=cr.OUT.F32).double(), want)
+
+
+def test_sizes_take_the_blocks_that_they_test(cr):
+    """The kernel that each size of this file runs: a change of the rule that drops one from the tests shows here."""
+    few = {(3, 1000, 2080): "mx_few_kernel<1, 16,", (50, 4360, 416): "mx_few_kernel<4, 8,"}
+    small = {(70, 200, 352): "64, 64, 1, 1, 4, 4, 1,", (70, 200, 2336): "64, 64, 1, 1, 4, 1, 4,", (90, 152, 2080): "64, 64, 1, 1, 4, 1, 4,",
+             (65, 8, 4256): "64, 64, 1, 1, 4, 1, 4,", (513, 4096, 160): "64, 64, 1, 1, 4, 4, 1,", (1531, 2568, 96): "128, 64, 2, 1,",
+             (2049, 2056, 32): "128, 128, 2, 2,", (3850, 4088, 416): "256, 256, 4, 2,"}
+    want = {**few, **{s: f"mx_gemm_kernel<{t}" for s, t in small.items()}, **{s: "mx_gemm_kernel<256, 256, 4, 2," for s in LARGE}}
+    assert set(SHAPES) | set(LARGE) == set(want)
+    torch.cuda.synchronize()
+    from torch.profiler import ProfilerActivity, profile
+    for (M, N, K), name in want.items():
+        a, w = ((torch.zeros((-(-K // 128), r, 64), dtype=torch.uint8, device=DEV), torch.zeros((-(-K // 128), r, 4), dtype=torch.uint8, device=DEV))
+                for r in (M, N))
+        torch.cuda.synchronize()
+        with profile(activities=[ProfilerActivity.CUDA]) as trace:
+            cr.mxfp4_gemm(*a, *w)
+            torch.cuda.synchronize()
+        ran = [e.name for e in trace.events() if "mx_" in e.name]
+        if not ran:
+            pytest.skip("no kernel trace on this host")
+        assert len(ran) == 1 and name in ran[0], ((M, N, K), ran)
+
+
+@pytest.mark.parametrize("C", [2568, 4104, 8200])
+def test_more_rows_of_a_block_each_than_a_grid_row(cr, C):
+    """Three, four and eight waves a row, a row a block: beyond 2^20 rows the grid goes on along its second axis, whose surplus
+    blocks write nothing. The block's shape depends on the columns alone here, so rows equal those of a call on them alone."""
+    rows = (1 << 20) + 3
+    say(f"norm {rows} rows of {C}")
+    g = torch.Generator(device=DEV).manual_seed(C)
+    x = torch.randn(rows, C, generator=g, device=DEV, dtype=torch.bfloat16)
+    w, b = torch.randn((2, C), generator=g, device=DEV), torch.randn((2, C), generator=g, device=DEV)
+    cut = rows // 2
+    off = torch.tensor([0, cut, rows], dtype=torch.int32, device=DEV)
+    out = torch.full((rows + 3, C), 7.0, device=DEV, dtype=torch.bfloat16)
+    mean, rstd = torch.full((rows + 3,), 7.0, device=DEV), torch.full((rows + 3,), 7.0, device=DEV)
+    cr.convrot_layer_norm_forward(x, w, b, seg_offsets=off, out=out[:rows], mean=mean[:rows], rstd=rstd[:rows])
+    at = torch.cat([_spread(rows), torch.arange((1 << 20) - 40, rows, device=DEV)]).unique()
+    some = torch.tensor([0, int((at < cut).sum()), at.numel()], dtype=torch.int32, device=DEV)
+    y, m, r = cr.convrot_layer_norm_forward(x[at], w, b, seg_offsets=some)
+    assert torch.equal(out[at], y) and torch.equal(mean[at], m) and torch.equal(rstd[at], r)
+    assert bool((out[rows:] == 7).all()) and bool((mean[rows:] == 7).all()) and bool((rstd[rows:] == 7).all())
+    for lo in range(0, rows, 1 << 17):                   # every row is normalised: mean 0, variance 1 before weight and bias
+        hi = min(rows, lo + (1 << 17))
+        t = x[lo:hi].float()
+        assert bool(((mean[lo:hi] - t.mean(1)).abs() < 1e-5).all()) and bool(((rstd[lo:hi] * t.std(1, unbiased=False) - 1).abs() < 1e-4).all())
+
+
+@pytest.mark.parametrize("C", [512, 520, 2048, 4096, 8192])
+def test_sums_of_many_rows(cr, C):
+    """d_weight and d_bias of terms of one sign, the hardest for a sum: off by at most 2^-24 of the magnitudes for each sum on
+    a term's way. Those are the rows of a part that one group of the block takes, the groups, and the parts."""
+    rows = 60001
+    groups = 8 if C <= 512 else 4 if C <= 1536 else 3 if C <= 2048 else 2 if C <= 4096 else 1
+    parts = 512 if C <= 512 else 256
+    part = -(-(-(-rows // parts)) // groups) * groups
+    g = torch.Generator(device=DEV).manual_seed(C)
+    x = torch.rand((rows, C), generator=g, device=DEV).to(torch.bfloat16)
+    dy = (torch.rand((rows, C), generator=g, device=DEV) + 0.5).to(torch.bfloat16)
+    mean, rstd = torch.full((rows,), -1.0, device=DEV), torch.full((rows,), 1.0, device=DEV)      # xh = x + 1: above 0
+    _, dw, db = cr.convrot_layer_norm_backward(dy, x, mean, rstd, want_dx=False)
+    xh = x.double() + 1
+    sums = part // groups + groups + min(-(-rows // part), parts)
+    for got, want, own in ((db, dy.double().sum(0), 0), (dw, (dy.double() * xh).sum(0), 2)):     # x - mean and its product: rounded
+        assert bool(((got.double() - want).abs() <= (sums + own) * 2.0 ** -24 * want).all())
+
+
+def test_steps_side_by_side(cr):
+    """Four streams at once, each reading codes back and stepping two optimizers with them: the results of one after the other."""
+    g = torch.Generator(device=DEV).manual_seed(8)
+    rows, K = 520, 1056
+    codes = [cr.mxfp4_quantize(torch.randn((rows, K), generator=g, device=DEV).to(torch.bfloat16)) for _ in range(4)]
+    n = rows * K
+
+    def state():
+        return ([torch.ones(n, device=DEV)], [torch.zeros(n, device=DEV)], [torch.zeros(n, device=DEV)],
+                [torch.ones(n, device=DEV)], [torch.zeros(n, dtype=torch.int8, device=DEV)], [torch.zeros(n, dtype=torch.uint8, device=DEV)],
+                [torch.zeros(-(-n // 256), device=DEV)], [torch.zeros(-(-n // 256), device=DEV)])
+
+    def chain(c, s, stream):
+        for step in range(1, 6):
+            grad = cr.mxfp4_dequantize(*c, K, out_type=cr.OUT.F32, stream=stream)
+            cr.convrot_adamw_step(s[0], [grad], s[1], s[2], step=step, lr=1e-2, stream=stream)
+            cr.convrot_adamw_step(s[3], [grad], s[4], s[5], step=step, lr=1e-2, exp_avg_scales=s[6], exp_avg_sq_scales=s[7], seed=step,
+                                  stream=stream)
+
+    want = [state() for _ in codes]
+    for c, s in zip(codes, want):
+        chain(c, s, None)
+    assert not torch.equal(want[0][0][0], want[1][0][0]) and bool(want[0][4][0].any())
+    streams = [torch.cuda.Stream() for _ in codes]
+    for _ in range(3):
+        got = [state() for _ in codes]
+        torch.cuda.synchronize()
+        for c, s, q in zip(codes, got, streams):
+            chain(c, s, q)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p[0], q[0]) for p, q in zip(a, b))
