@@ -239,3 +239,30 @@ def test_the_smallest_eps(cr, bits):
     want[::3] = 0.75
     # 24 roundings on the way to the update of a quarter
     assert float((p - want).abs().max()) <= 24 * U and torch.equal(p[1::3], want[1::3])
+
+
+def _kernel_steps(cr, n):
+    state = _codes(n)
+
+    def step(grad, t):
+        m, v, ms, vs = state
+        cr.convrot_adamw_step([torch.zeros(n, device=DEV)], [dev(grad)], [m], [v], step=t, lr=1e-3, weight_decay=0.0,
+                              exp_avg_scales=[ms], exp_avg_sq_scales=[vs], seed=t)
+        return v.cpu().numpy()
+
+    step.state = state
+    return step
+
+
+def test_codes_are_right_on_average(cr):
+    """Roots that decay by less than a code's step, and first moments on their way to another gradient, arrive."""
+    from tests import test_oracle_training as oracle
+    check = oracle.check_decaying_roots
+    check(*oracle.decaying_roots(_kernel_steps(cr, oracle.WIDE))[:2])
+    first, then, at = oracle.turning_gradients()
+    step = _kernel_steps(cr, oracle.WIDE)
+    for t in range(1, 121):
+        step(first if t <= 60 else then, t)
+    m, v, ms, vs = step.state
+    values, _ = cr.convrot_adamw_moments([m], [v], [ms], [vs])
+    oracle.check_first_moment(values.double().cpu().numpy(), first, then, at, 60)

@@ -101,3 +101,104 @@ def test_not_finite_blocks():
     codes, scales = tr.encode(x, np.zeros(512, np.float32), 127)
     assert scales[0] == 1 and np.isnan(scales[1]) and not codes[256:].any()
     assert np.isnan(tr.decode(codes, scales, 127)[256:]).all()
+
+
+# ---------------------------------------------------------------------------
+# 8-bit moments over many steps. A code's rounding is right on average, a value's is not:
+# the value goes as the code's square (of a root) or its square with a sign, so its average
+# lies above by the variance of the code.
+# ---------------------------------------------------------------------------
+STEPS, WIDE = 200, 4096
+
+
+def decaying_roots(step_fn, n=WIDE):
+    """One step with gradients of all sizes, then STEPS without, but for the largest of each block, which keeps its size and
+    so the block's scale. step_fn(gradient, step) -> codes of the roots. (Codes after the first step, codes at the end,
+    elements that decay)."""
+    g = np.random.default_rng(21)
+    first = np.exp2(g.uniform(-6, -0.1, n)).astype(np.float32)
+    first[::256] = 1
+    rest = np.zeros(n, np.float32)
+    rest[::256] = np.sqrt(np.float32(1 - 0.999))
+    start = step_fn(first, 1).astype(np.float64)
+    for step in range(2, STEPS + 2):
+        last = step_fn(rest, step)
+    at = np.arange(n) % 256 != 0
+    return start[at], last.astype(np.float64)[at], at
+
+
+def check_decaying_roots(start, last):
+    """With beta2 = 0.999 a root's code is 255 sqrt(root / s) and falls by 0.999^(1/4) a step, on average exactly that from one
+    code to the next. What is cut off or added in a step has the variance f (1 - f) <= 1/4 with f the code's fall, at most
+    2.6e-4 of it: over all steps at most STEPS * 2.6e-4 times the code. Six deviations of the mean over the elements."""
+    kept = 0.999 ** (STEPS / 4)
+    deviation = np.sqrt((STEPS * 2.6e-4 * start).sum()) / len(start)
+    off = (last - kept * start).mean()
+    assert start.min() > 25 and abs(off) <= 6 * deviation, (off, deviation)
+
+
+def _steps(encode_u=None):
+    """step_fn of the oracle; encode_u: in the place of the random numbers (a planted mistake)."""
+    state = {"r": (np.zeros(WIDE, np.uint8), np.zeros(WIDE // 256, np.float32)), "m": (np.zeros(WIDE, np.int8), np.zeros(WIDE // 256, np.float32))}
+    kept = tr.random_pair
+
+    def step(g, t):
+        p = np.zeros(WIDE, np.float32)
+        if encode_u is not None:
+            tr.random_pair = lambda seed, tensor, n: (np.full(n, encode_u, np.float32),) * 2
+        try:
+            _, mc, ms, vc, vs = tr.adamw8(p, g, *state["m"], *state["r"], t, 1e-3, 0.9, 0.999, 1e-8, 0.0, t, 0)
+        finally:
+            tr.random_pair = kept
+        state["m"], state["r"] = (mc, ms), (vc, vs)
+        return vc
+
+    step.state = state
+    return step
+
+
+def test_roots_decay_on_average():
+    check_decaying_roots(*decaying_roots(_steps())[:2])
+
+
+def test_roots_rounded_to_the_nearest_would_stick():
+    start, last, _ = decaying_roots(_steps(0.5))
+    assert np.array_equal(start, last)
+    with pytest.raises(AssertionError):
+        check_decaying_roots(start, last)
+
+
+def turning_gradients(n=WIDE):
+    """A gradient, and three quarters of it but for the largest of each block, which keeps the block's scale."""
+    g = np.random.default_rng(22)
+    first = np.exp2(g.uniform(-6, 0, n)) * np.where(g.integers(0, 2, n), 1, -1)
+    first[::256] = 1
+    at = np.arange(n) % 256 != 0
+    return first.astype(np.float32), np.where(at, 0.75 * first, first).astype(np.float32), at
+
+
+def check_first_moment(values, first, then, at, steps):
+    """After `steps` of either gradient m = then (1 - 0.9^steps) + first (1 - 0.9^steps) 0.9^steps. With s <= 1 the largest of a
+    block: a step's rounding moves the code by what it cuts or adds, variance at most 1/4, so the value by 2 c / 127^2 of that,
+    and by at most 1 / (4 127^2) on average, always away from zero; what came before counts 0.9, so the mean adds up to 10 times
+    that and the variance to 1 / (1 - 0.81). Six deviations of the mean over the elements, signs taken out."""
+    fade = 0.9 ** steps
+    want = (1 - fade) * (np.abs(then) + fade * np.abs(first))
+    code = 127 * np.sqrt(np.abs(first))
+    deviation = np.sqrt(((2 * code + 1) ** 2 / 4 / (1 - 0.81))[at].sum()) / 127 ** 2 / at.sum()
+    off = (values * np.sign(first) - want)[at].mean()
+    assert -6 * deviation <= off <= 10 / (4 * 127 ** 2) + 6 * deviation, (off, deviation)
+
+
+@pytest.mark.parametrize("u", [None, 0.5])
+def test_first_moment_follows_on_average(u):
+    first, then, at = turning_gradients()
+    step = _steps(u)
+    for t in range(1, 121):
+        step(first if t <= 60 else then, t)
+    m = tr.decode(*step.state["m"], 127).astype(np.float64)
+    if u is None:
+        check_first_moment(m, first, then, at, 60)
+    else:                                                # the nearest code: it stops on its way
+        with pytest.raises(AssertionError):
+            check_first_moment(m, first, then, at, 60)
