@@ -673,7 +673,9 @@ cr_status convrot_act_backward(const void* dy, int64_t lddy, const void* codes, 
  *   mxfp4_quantize    x bf16 [rows, K], leading dimension ldx; rot_group 0 (none),
  *                     16, 64, 256 or 1024: each group of rot_group columns is
  *                     rotated first (float32, in the butterfly order above). With
- *                     non-finite values under a rotation the group is NaN.
+ *                     non-finite values under a rotation the group is NaN; so are the
+ *                     blocks of 32 in which a sum before the factor 1/sqrt(rot_group) is
+ *                     not below 2^128 (never with magnitudes below 2^128 / rot_group).
  *   mxfp4_dequantize  out [rows, K] bf16 or float32, leading dimension ldo: the values
  *                     of the codes, rotated back (float32, same butterflies, times
  *                     1/sqrt(rot_group)) and rounded once
@@ -717,7 +719,10 @@ cr_status mxfp4_gemm(const void* a_codes, const void* a_scales, const void* w_co
  *     dx[m, c] = dx_base[m, c] + rstd[m] (g[m, c] - sum_c g / C - xh[m, c] sum_c (g xh) / C)
  *     d_weight[s, c] = sum_m dy[m, c] xh[m, c],  d_bias[s, c] = sum_m dy[m, c]    over the rows of s
  *   All of it in float32; y and dx are rounded once. No atomics on values: the rows'
- *   sums are split into parts that are added in order, fixed by the sizes and offsets.
+ *   sums are split into at most 512 (C <= 512) or 256 parts that are added in order, fixed by the
+ *   sizes and offsets. A part's rows are added one by one, in 1 to 8 sums by C: with
+ *   one sign throughout d_weight and d_bias are off by up to about 2^-24 times
+ *   (rows / 256 + 256) of their value, and far less with signs that vary.
  *   A row's y and dx do not depend on other rows; what is not finite in a row
  *   reaches d_weight and d_bias of its sequence only.
  *

@@ -210,3 +210,20 @@ def test_linear_and_its_gradient(cr, rot):
     assert np.all(np.abs(dx - want) <= 2.0 ** -23 * (N + 2) * mag)
     exact = bf16_to_f32(dy).astype(np.float64) @ bf16_to_f32(w).astype(np.float64)
     assert np.linalg.norm(dx - exact) < 0.25 * np.linalg.norm(exact)
+
+
+@pytest.mark.parametrize("rot", [16, 64, 256, 1024])
+def test_rotated_at_the_largest_values(cr, rot):
+    """Finite values whose sums leave float32: the blocks in which that happens stand for NaN, others keep their codes."""
+    g = np.random.default_rng(rot + 1)
+    x = g.uniform(-1, 1, (24, 1024)).astype(np.float32) * np.exp2(np.linspace(118, 127.9, 24))[:, None].astype(np.float32)
+    x[20:, 1::2] = 0
+    x[22:, 5:] = 0                                       # few large ones: their sums stay finite
+    x = bf16_to_f32(wl.bf16_bits_from_f32(x))
+    assert np.isfinite(x).all()
+    want = mx.quantize(x, rot)[1]
+    assert (want == 255).any() and (want[:, :] != 255).any()
+    codes, scales = cr.mxfp4_quantize(bf16_dev(wl.bf16_bits_from_f32(x)), rot)
+    _check_codes(codes, scales, x, rot)
+    small = np.abs(x).max(1) < 2.0 ** 128 / rot
+    assert not (want[small] == 255).any()
