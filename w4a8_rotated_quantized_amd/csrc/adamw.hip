@@ -127,8 +127,8 @@ CR_DEV v4f root_values(uint32_t c, float s) {
   return v;
 }
 
-// sqrt(x) rounded once, for 2^-100 <= x <= 1: a step on the root and half its
-// reciprocal together, then one with the exact residual.
+// sqrt(x) rounded once, for 2^-100 <= x <= 1: a step of Goldschmidt's iteration on the root and half
+// its reciprocal together, then one of Newton's with the exact residual.
 CR_DEV float sqrt_rn(float x) {
   const float y = __builtin_amdgcn_rsqf(x);
   float s = x * y, h = 0.5f * y;

@@ -277,8 +277,9 @@ __global__ __launch_bounds__((BM / (32 * TM)) * (BN / (32 * TN)) * 64 * KG, MINB
 // its NW waves take the 128-column tiles in turn and read their fragments straight
 // from memory: v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows x 64 B of a tile,
 // which is 1 KB in one piece (lane l: row l % 16, columns 32 (l / 16) .. +31).
-// U tiles a wave are loaded before the first is used, so the whole of a
-// matrix is on its way at once. Tokens past the end are zeros without a load.
+// U tiles a wave are loaded before the first is used: with U = 2 all of a matrix up to K = 4096
+// (16 waves) or 2048 (8) is on its way at once, a longer one takes further trips, each with a latency
+// of its own (K = 2560 with 8 waves: four of them make a second). Tokens past the end are zeros without a load.
 // Partial sums meet in LDS in a fixed order.
 // ---------------------------------------------------------------------------
 template <int FM, int NW, int U, bool F32>
@@ -377,7 +378,7 @@ static hipError_t launch_out(const MxGemm& p, hipStream_t s) {
     return hipGetLastError();
   }
   // The block shape with the least time. A compute unit that has n blocks to do takes at least `alone` a
-  // stage (one block's own chain of waits) and n times `each` once they fill it, in ns. Measured with K = 4096
+  // stage (one block's own chain of waits) and n times `each` once they fill it, in ns. Measured with K = 4096, the product alone in a row
   // (256 x 256, 128 x 128, 128 x 64, 64 x 64 blocks, in us): 8192 x 12288: 218, 253, -, -; 4096 x 4096: 39, 50, 53, 62;
   // 2048 x 4096: 31, 23, 30, 33; 1024 x 4096: 29, 17, 15, 18; 512 x 4096: 29, 16, 13, 11; and 1531 x 2560, N = 9216:
   // 25, 29, 32, 36.

@@ -497,6 +497,9 @@ size_t norm_backward_ws_bytes(int64_t rows, int64_t C, int S) {
 // make up a block. Sixteen columns a lane, or more blocks instead of groups, leave a block's few waves waiting for their
 // row: both launches in us, with 16 columns a lane and one group / 8 and one / 8 and these groups: 1531 x 2560: 19, 16, 13;
 // 8192 x 2048: 34, 26, 23; 8192 x 4096: 46, 45, 44; 8192 x 1024: 19, 18, 15.
+// The variants of 16 columns a lane keep 21 to 76 registers in scratch (w, dw and db of 16 columns beside the row),
+// <8, 1, 2> with x or dy in float32 4 to 10: 8192 x 12288 and x 16384 with a base, x bf16 / float32, run at 4.0 / 3.8 and
+// 4.2 / 3.6 TB/s (203 / 265 and 257 / 374 us), 8192 x 8192 at 4.6 / 4.8 (116 / 141), 8192 x 4096 at 4.7 / 4.4 (57 / 77).
 template <bool XF, bool DF>
 static void backward_xd(const NormBackward& p, hipStream_t s) {
   const dim3 grid((unsigned)p.parts);
