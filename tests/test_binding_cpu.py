@@ -115,7 +115,7 @@ moments = lambda: ([T(i8, 300), T(i8, 5)], [T(u8, 300), T(u8, 5)], [T(f32, 2), T
 two = lambda dtype: [T(dtype, 300), T(dtype, 5)]
 
 def calls():
-    # name, function, arguments, places of the tensors that it writes (in lists: all of a list)
+    # function, arguments, places of the tensors that it writes for others than itself (in lists: all of a list)
     m, v, ms, vs = moments()
     yield "mxfp4_quantize", [T(bf, M, C), 0, T(u8, 1, M, 64), T(u8, 1, M, 4), 0], [2, 3]
     yield "mxfp4_dequantize", [T(u8, 1, M, 64), T(u8, 1, M, 4), C, 0, 0, T(bf, M, C), 0], [5]
@@ -123,8 +123,8 @@ def calls():
     yield "layer_norm_forward", [T(bf, M, C), T(bf, C), T(bf, C), None, 1e-6, False, 0, T(bf, M, C), T(f32, M), T(f32, M), 0], [7, 8, 9]
     yield "layer_norm_backward", [T(bf, M, C), T(bf, M, C), T(f32, M), T(f32, M), T(bf, C), None, False, None, 0, T(bf, M, C), T(f32, C),
                                   T(f32, C), True, True, True, T(u8, 64), 0], [9, 10, 11, 15]
-    yield "adamw_step", [two(f32), two(f32), two(f32), two(f32), None, None, None, None, 1, .1, .9, .99, 1e-8, 0., 0, 0], [0, 2, 3]
-    yield "adamw_step", [two(f32), two(bf), m, v, two(bf), ms, vs, T(f32, 1), 1, .1, .9, .99, 1e-8, 0., 0, 0], [0, 2, 3, 4, 5, 6]
+    yield "adamw_step", [two(f32), two(f32), two(f32), two(f32), None, None, None, None, 1, .1, .9, .99, 1e-8, 0., 0, 0], [0]
+    yield "adamw_step", [two(f32), two(bf), m, v, two(bf), ms, vs, T(f32, 1), 1, .1, .9, .99, 1e-8, 0., 0, 0], [0, 4]
     m, v, ms, vs = moments()
     yield "adamw_moments", [m, v, ms, vs, T(f32, 305), T(f32, 305), 0], [4, 5]
 

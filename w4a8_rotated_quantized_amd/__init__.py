@@ -834,8 +834,8 @@ def convrot_adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1=0.9
     8-bit moments; start them as zeros; give each step another seed). copies:
     bf16 tensors that receive the new params. grad_scale: float32 [1] on the GPU,
     multiplies the gradients. step counts from 1. A tensor may stand in the lists
-    once. The written tensors' versions change as in torch's own in-place calls: a
-    backward pass that still needs an earlier value of theirs raises."""
+    once. The versions of params and copies change as in torch's own in-place calls:
+    a backward pass that still needs an earlier value of theirs raises."""
     if not len(params):
         raise ValueError("params is empty")
     args = (params, grads, exp_avgs, exp_avg_sqs, copies, exp_avg_scales, exp_avg_sq_scales, grad_scale, step, lr, beta1, beta2,

@@ -17,6 +17,7 @@
 #include <ATen/ATen.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <c10/util/SmallVector.h>
 
 #include <cstdio>
 #include <cstring>
@@ -439,32 +440,38 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // ---------------------------------------------------------------------------
 // optimizer step
 // ---------------------------------------------------------------------------
-// a list or tuple of tensors, held with its tensors until the call has returned: the caller's list may change
-// while the interpreter's lock is given up
+// a list or tuple of tensors, which are held until the call has returned: the caller's list may change while the
+// interpreter's lock is given up
 struct Tensors {
-  PyObject* held = nullptr;
+  c10::SmallVector<PyObject*, 64> held;
+  bool given;
   const char* what;
   Py_ssize_t n = 0;
-  Tensors(PyObject* o, const char* what) : what(what) {
-    if (o == Py_None) return;
-    held = PySequence_Tuple(o);
-    if (!held) throw python_error();
-    n = PyTuple_GET_SIZE(held);
+  Tensors(PyObject* o, const char* what) : given(o != Py_None), what(what) {
+    if (!given) return;
+    PyObject* items = PySequence_Fast(o, "lists of tensors are wanted");
+    if (!items) throw python_error();
+    n = PySequence_Fast_GET_SIZE(items);
+    held.append(PySequence_Fast_ITEMS(items), PySequence_Fast_ITEMS(items) + n);
+    for (PyObject* t : held) Py_INCREF(t);
+    Py_DECREF(items);
   }
-  ~Tensors() { Py_XDECREF(held); }
+  ~Tensors() {
+    for (PyObject* t : held) Py_DECREF(t);
+  }
   Tensors(const Tensors&) = delete;
   Tensors& operator=(const Tensors&) = delete;
-  explicit operator bool() const { return held != nullptr; }
-  const Tensor& operator[](Py_ssize_t i) const { return tensor(PyTuple_GET_ITEM(held, i), what); }
+  explicit operator bool() const { return given; }
+  const Tensor& operator[](Py_ssize_t i) const { return tensor(held[(size_t)i], what); }
 };
 
-void* element(const Tensors& l, Py_ssize_t i, ScalarType type, int index, int64_t numel) {
-  const Tensor& t = l[i];
+void* element(const Tensors& l, const Tensor& t, ScalarType type, int index, int64_t numel) {
   if (t.numel() != numel) wrong("%s must hold one tensor for each of params, of its size", l.what);
   if (t.scalar_type() != type || !on(t, index) || !t.is_contiguous())
     wrong("%s must be contiguous %s tensors on GPU %d", l.what, type_name(type), index);
   return t.data_ptr();
 }
+void* element(const Tensors& l, Py_ssize_t i, ScalarType type, int index, int64_t numel) { return element(l, l[i], type, index, numel); }
 
 // Fills the moments of every entry; `sizes` from the first list.
 void moments(std::vector<cr_adamw_tensor>& e, const Tensors& m, const Tensors& v, const Tensors& ms, const Tensors& vs, int index) {
@@ -503,8 +510,9 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (Py_ssize_t i = 0; i < p.n; ++i) {
       cr_adamw_tensor& t = e[(size_t)i];
       t = cr_adamw_tensor{};
-      t.n = p[i].numel();
-      t.param = element(p, i, ScalarType::Float, index, t.n);
+      const Tensor& param = p[i];
+      t.n = param.numel();
+      t.param = element(p, param, ScalarType::Float, index, t.n);
       t.grad = element(g, i, gt, index, t.n);
       if (c) t.copy = element(c, i, ScalarType::BFloat16, index, t.n);
     }
@@ -519,9 +527,10 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const Unlocked free;
       st = convrot_adamw_step(e.data(), entries(e), grad_type, ms ? 8 : 32, lr, beta1, beta2, eps, decay, step, scale, seed, stream);
     }
+    // what a graph of the model can hold; the moments are the optimizer's own (252 tensors: 2 us of the host's for 10 with them)
     if (ran(st))
-      for (const Tensors* l : {&p, &m, &v, &c, &ms, &vs})
-        for (Py_ssize_t i = 0; i < l->n; ++i) written(&(*l)[i]);
+      for (const Tensors* l : {&p, &c})
+        for (PyObject* t : l->held) written(&THPVariable_Unpack(t));
     return refused(st);
   });
 }
