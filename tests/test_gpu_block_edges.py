@@ -338,7 +338,7 @@ def test_sizes_take_the_blocks_that_they_test(cr):
         a, w = ((torch.zeros((-(-K // 128), r, 64), dtype=torch.uint8, device=DEV), torch.zeros((-(-K // 128), r, 4), dtype=torch.uint8, device=DEV))
                 for r in (M, N))
         torch.cuda.synchronize()
-        with profile(activities=[ProfilerActivity.CUDA]) as trace:
+        with profile(activities=[ProfilerActivity.CUDA], acc_events=True) as trace:
             cr.mxfp4_gemm(*a, *w)
             torch.cuda.synchronize()
         ran = [e.name for e in trace.events() if "mx_" in e.name]
