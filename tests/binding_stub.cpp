@@ -3,6 +3,7 @@
 // word from another thread, and answer CR_OK if it came and CR_ERR_HIP if not.
 #include <atomic>
 #include <chrono>
+#include <cstdlib>
 #include <thread>
 
 #include "convrot.h"
@@ -22,6 +23,13 @@ extern "C" {
 int stub_calls() { return g_calls; }
 void stub_word() { ++g_words; }
 void stub_wait(int on) { g_wait = on; }
+// The process's end, behind the interpreter's, gives the waiting call its word and stays for half a second.
+void stub_linger() {
+  std::atexit([] {
+    g_words = 1 << 30;
+    std::this_thread::sleep_for(std::chrono::milliseconds(500));
+  });
+}
 
 cr_status mxfp4_quantize(const void*, int64_t, int64_t, int64_t, int, void*, void*, hipStream_t) { return met(); }
 cr_status mxfp4_dequantize(const void*, const void*, int64_t, int64_t, int, void*, cr_out, int64_t, hipStream_t) { return met(); }

@@ -180,3 +180,19 @@ print("ok")
 def test_written_tensors_change_their_version(stub):
     """Autograd then refuses a backward pass that needs what was there before."""
     assert "ok" in _python(VERSIONS, ROOT, stub, NATIVE)
+
+
+LEFT = HARNESS + """
+name, args, _ = [c for c in calls() if c[0] == sys.argv[3]][-1]
+stub.stub_linger()
+threading.Thread(target=lambda: getattr(n, name)(*args), daemon=True).start()
+while stub.stub_calls() == 0:
+    time.sleep(0.001)
+print("ok", flush=True)
+"""
+
+
+@pytest.mark.parametrize("name", ["mxfp4_gemm", "layer_norm_backward", "adamw_step"])
+def test_a_call_that_outlives_the_interpreter(stub, name):
+    """A daemon thread whose call ends when the interpreter is gone ends quietly, and the process as it would have."""
+    assert "ok" in _python(LEFT, ROOT, stub, NATIVE, name)

@@ -10,6 +10,7 @@
 // allocating in Python through ctypes took 12.4 us for a layer norm of 77 rows,
 // 3 us of it the launch, while the kernel takes 4.
 #include <Python.h>
+#include <unistd.h>
 
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -176,7 +177,15 @@ bool ran(cr_status st) { return st == CR_OK || st == CR_ERR_HIP; }
 struct Unlocked {
   PyThreadState* thread = PyEval_SaveThread();
   Unlocked() = default;
-  ~Unlocked() { PyEval_RestoreThread(thread); }
+  // An interpreter that has ended meanwhile unwinds the thread instead of returning to it. What the call holds
+  // is not to be given back then, so the thread waits here for the end of the process.
+  ~Unlocked() {
+    try {
+      PyEval_RestoreThread(thread);
+    } catch (...) {
+      for (;;) pause();
+    }
+  }
   Unlocked(const Unlocked&) = delete;
   Unlocked& operator=(const Unlocked&) = delete;
 };
